@@ -18,7 +18,8 @@
  *    library never allocates or frees device memory on these paths.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *    stream) and never synchronise the host, except moe_prepare_weights,
- *    moe_get_device_status, moe_route_noalloc_status and moe_tensor_peak.
+ *    moe_prepare_matvec, moe_get_device_status, moe_route_noalloc_status,
+ *    moe_ffn_status and moe_tensor_peak.
  *  - The return value is a status: MOE_OK (0) or a negative MOE_ERR_* code.  On an
  *    error nothing has been launched unless the code is MOE_ERR_CUDA.
  *  - Shapes: 1 <= T, T * k <= 2^24, H % 32 == 0 with 32 <= H <= 8192, I % 32 == 0
@@ -326,8 +327,128 @@ int moe_forward_launches(int T, int H, int I, int E, int k);
 #define MOE_PEAK_BF16 1
 int moe_tensor_peak(int kind, int mmas_per_sm, double* tflops, moe_stream_t stream);
 
-/* moe_set_wait_limit_ns: how long (ns) each pipeline wait of the expert GEMMs may
- * take before it gives up, for launches made after the call (process-wide; 0
+/* ------------------------------------------------------------------ dense operators
+ * What a decoder's half layer needs beside the experts: the norms before and after a
+ * block, a dense gated feed-forward block, and products of a few tokens with MXFP4
+ * weights that need no routing.  The pages name the pieces ("triton-kernels" README,
+ * "Kernels": rmsnorm_residual_fused, swiglu_fused, the W4A16 GEMM); the operators below
+ * are this library's own.  `dtype` is the type of the activations and weights
+ * (MOE_DTYPE_BF16 or MOE_DTYPE_F16); every array is contiguous, row major.           */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+#define MOE_DTYPE_F32 2 /* only as stream_dtype of the norms */
+
+#define MOE_GATE_NONE 0
+#define MOE_GATE_FEATURE 1 /* gate [H], of `dtype`                                    */
+#define MOE_GATE_TOKEN 2   /* gate f32 [T]                                            */
+#define MOE_GATE_FULL 3    /* gate [T, H], of `dtype`                                 */
+
+#define MOE_ACT_SILU 0
+#define MOE_ACT_GELU 1 /* tanh form                                                   */
+
+/* moe_block_norm: the end of one block and the start of the next in one launch.
+ *   n = block / sqrt(mean_H(block^2) + eps) * norm_weight   (n = block without norm_weight)
+ *   s = residual_scale * residual + gate * n                rounded to stream_dtype
+ *   out = s / sqrt(mean_H(s^2) + eps) * next_weight         of the rounded s
+ * All arithmetic is f32; s and out are rounded once.
+ *   block [T, H]; norm_weight [H] or NULL; gate by gate_kind (NULL for MOE_GATE_NONE);
+ *   residual [T, H] of stream_dtype, or NULL for none; next_weight [H] or NULL;
+ *   stream_dtype: dtype or MOE_DTYPE_F32.
+ *   residual_out: s, [T, H] of stream_dtype, or NULL when only `out` is wanted; it may
+ *   be `residual` itself.  out: [T, H] of dtype; NULL exactly when next_weight is; it
+ *   may be `block` itself.
+ *   1 <= T <= 2^24, H % 8 == 0 with 8 <= H <= 8192; arrays 16-byte aligned (a token
+ *   gate 4); eps finite and >= 0; residual_scale finite.
+ * Source: "triton-kernels" README, "Kernels" (rmsnorm_residual_fused), with the norm
+ * after the block, its gate and the residual scale added.                           */
+int moe_block_norm(const void* block, const void* norm_weight, const void* gate, int gate_kind, const void* residual,
+                   float residual_scale, const void* next_weight, float eps, int T, int H, int dtype, int stream_dtype,
+                   void* residual_out, void* out, moe_stream_t stream);
+
+/* moe_block_norm_backward: every gradient of moe_block_norm, from the same arguments.
+ *   d_residual_out [T, H] of stream_dtype: gradient into s from what reads the stream
+ *   later, or NULL for none; d_out [T, H] of dtype: NULL exactly when next_weight is (one
+ *   of the two must be given).  residual_out: the s of the forward (needed with
+ *   next_weight; the rounding of s passes the gradient through).
+ *   d_block [T, H] of dtype: written.  d_residual [T, H] of stream_dtype, or NULL.
+ *   d_norm_weight, d_next_weight: f32 [H], or NULL.  d_gate, or NULL: f32 [H] for a
+ *   feature gate, f32 [T] for a token gate, [T, H] of dtype for a full gate.
+ *   d_block may be `block`, d_residual may be `d_residual_out`; no other aliasing.
+ *   workspace: moe_block_norm_workspace_bytes(T, H) bytes, 256-byte aligned, contents
+ *   irrelevant before and after.  The weight gradients are summed in a fixed order, so
+ *   results repeat bit for bit.                                                     */
+size_t moe_block_norm_workspace_bytes(int T, int H);
+int moe_block_norm_backward(const void* d_residual_out, const void* d_out, const void* block, const void* norm_weight,
+                            const void* gate, int gate_kind, const void* residual_out, float residual_scale,
+                            const void* next_weight, float eps, int T, int H, int dtype, int stream_dtype,
+                            void* d_block, void* d_residual, float* d_norm_weight, void* d_gate, float* d_next_weight,
+                            void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_ffn_forward: a dense gated feed-forward block with 16-bit weights (a shared expert
+ * or a dense layer beside the experts).
+ *   g = x W_gate^T, u = x W_up^T, h = act(g) * u        one kernel
+ *   out = h W_down^T
+ * Sums are f32; h is rounded to dtype between the products.
+ *   x [T, H]; w_gateup [2I, H], gate rows [0, I) then up rows; w_down [H, I]: as stored,
+ *   nothing is prepared; out [T, H].
+ *   gateup_out: f32 [T, 2I] (g, then u), written for moe_ffn_backward; NULL to skip.
+ *   1 <= T <= 2^24, H and I multiples of 8 from 8 to 2^17; arrays 16-byte aligned,
+ *   workspace moe_ffn_workspace_bytes(T, H, I, 0) bytes, 256-byte aligned, contents
+ *   irrelevant before and after.  Up to 16 tokens take a kernel that streams the weights
+ *   through mma.sync, more the tcgen05 GEMMs.
+ * Source: "triton-kernels" README, "Kernels" (swiglu_fused).                        */
+size_t moe_ffn_workspace_bytes(int T, int H, int I, int backward);
+int moe_ffn_forward(const void* x, const void* w_gateup, const void* w_down, int T, int H, int I, int act, int dtype,
+                    float* gateup_out, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_ffn_backward: the gradients of moe_ffn_forward, from its inputs and saved g, u.
+ *   dh = d_out W_down;  dg = dh * u * act'(g);  du = dh * act(g);  h = act(g) * u
+ *   d_x = [dg du] w_gateup;  d_w_gateup = [dg du]^T x;  d_w_down = d_out^T h
+ * dg, du and h are formed in f32 and rounded to dtype as the next products' operands.
+ *   d_x [T, H], d_w_gateup [2I, H], d_w_down [H, I] of dtype: overwritten; each may be
+ *   NULL (not all).  workspace: moe_ffn_workspace_bytes(T, H, I, 1) bytes.
+ *   No output may overlap an input.  Everything else is as for moe_ffn_forward.      */
+int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, const void* w_gateup, const void* w_down,
+                     int T, int H, int I, int act, int dtype, void* d_x, void* d_w_gateup, void* d_w_down,
+                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_ffn_status: the device status of the feed-forward GEMMs on the current device,
+ * as moe_get_device_status (bits and returns) for one word that the library holds per
+ * GPU: synchronises `stream`, reads the word into *status and clears it when set.  A
+ * bounded wait that gave up (moe_set_wait_limit_ns) sets it; the results of calls since
+ * the last reading are then not reliable.  Not for the hot path.                    */
+int moe_ffn_status(int* status, moe_stream_t stream);
+
+/* moe_prepare_matvec: one-time re-layout of raw MXFP4 weights [rows][K/2] codes and
+ * [rows][K/32] scales (as the expert weights of one expert) for moe_matvec_mxfp4.  The
+ * bytes are only moved.
+ *   kind: MOE_WEIGHTS_DOWN for a plain product, MOE_WEIGHTS_GATEUP for gate rows
+ *   [0, rows/2) and up rows [rows/2, rows) (rows even).
+ *   1 <= rows <= 2^22, K % 32 == 0 with 32 <= K <= 65536; codes 16-byte aligned; dst
+ *   moe_prepared_matvec_bytes(...) bytes, 256-byte aligned.
+ * Scale bytes of 255 are rejected with MOE_ERR_NAN_SCALE after the stream has finished
+ * (it synchronises `stream`, as a load-time call may).                              */
+size_t moe_prepared_matvec_bytes(int rows, int K, int kind);
+int moe_prepare_matvec(const uint8_t* codes, const uint8_t* scales, int rows, int K, int kind, void* dst,
+                       size_t dst_bytes, moe_stream_t stream);
+
+/* moe_matvec_mxfp4: products of 1 to 64 tokens with prepared MXFP4 weights.
+ *   MOE_WEIGHTS_DOWN:   out[t, n] = sum_k x[t, k] W[n, k] + bias[n]        out [T, rows]
+ *   MOE_WEIGHTS_GATEUP: g, u the products (+ bias) of gate row i and up row i,
+ *                       out[t, i] = act(g) * u                             out [T, rows/2]
+ * The weights are used exactly as stored; sums are f32 in a fixed order, one rounding
+ * at the end.  bf16 x is carried as f16 times a power of two per token and K chunk:
+ * values below 2^-28 of their chunk's largest lose relative precision (absolute error
+ * 2^-39 of that largest), and sums are formed at up to 2^15 times their final size per
+ * unit of x, so a group scale above 2^96 may overflow them.
+ *   x [T, K] of dtype; bias f32 [rows] or NULL; act is read for MOE_WEIGHTS_GATEUP.
+ * Source: "triton-kernels" README, "Kernels" (W4A16 GEMM: 4-bit weights with group
+ * scales, 16-bit activations), on the layer's MXFP4 format.                         */
+int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int rows, int K, int kind, int act,
+                     int dtype, void* out, moe_stream_t stream);
+
+/* moe_set_wait_limit_ns: how long (ns) each pipeline wait of the expert GEMMs (and of
+ * the dense feed-forward GEMMs, whose status moe_ffn_status reads) may take before it gives up, for launches made after the call (process-wide; 0
  * restores the default of 1 s; at most 10 s, else MOE_ERR_INVALID_ARG).  A wait
  * that gives up sets a bit of the workspace status word (moe_get_device_status), the
  * kernel drops its remaining work, waits (up to 1 s) for the copies and tensor-core

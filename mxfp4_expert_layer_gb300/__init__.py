@@ -5,6 +5,7 @@ The compute path is the CUDA library ``libmoe_mxfp4.so`` (C ABI in
 """
 
 from . import _lib  # noqa: F401
+from ._lib import MOE_ACT_GELU, MOE_ACT_SILU, MOE_WEIGHTS_DOWN, MOE_WEIGHTS_GATEUP  # noqa: F401
 from .build import build, LIB_PATH  # noqa: F401
 
 
@@ -14,4 +15,8 @@ def __getattr__(name):
                 "build_tile_table", "tile_rows", "max_tiles"):
         from . import api
         return getattr(api, name)
+    if name in ("block_norm", "block_norm_backward", "BlockNormGrads", "ffn_forward", "ffn_backward", "FfnGrads",
+                "ffn_status", "MatvecMXFP4"):
+        from . import dense
+        return getattr(dense, name)
     raise AttributeError(name)

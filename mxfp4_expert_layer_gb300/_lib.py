@@ -26,11 +26,21 @@ MOE_ROUTE_GATING_SOFTMAX_ALL = 2
 MOE_ROUTE_GATING_SIGMOID = 4
 MOE_PEAK_MXF4 = 0
 MOE_PEAK_BF16 = 1
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
+MOE_GATE_NONE = 0
+MOE_GATE_FEATURE = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
+MOE_ACT_SILU = 0
+MOE_ACT_GELU = 1
 
 # every symbol the header declares, with its C signature
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _S = ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = {
     "moe_error_string": (ctypes.c_char_p, [_I]),
     "moe_prepared_weight_bytes": (_S, [_I, _I, _I, _I]),
@@ -56,6 +66,17 @@ SIGNATURES = {
     "moe_forward_launches": (_I, [_I, _I, _I, _I, _I]),
     "moe_get_device_status": (_I, [_P, _S, ctypes.POINTER(_I), _P]),
     "moe_tensor_peak": (_I, [_I, _I, ctypes.POINTER(ctypes.c_double), _P]),
+    "moe_block_norm": (_I, [_P, _P, _P, _I, _P, _F, _P, _F, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_block_norm_workspace_bytes": (_S, [_I, _I]),
+    "moe_block_norm_backward": (_I, [_P, _P, _P, _P, _P, _I, _P, _F, _P, _F, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                                     _S, _P]),
+    "moe_ffn_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "moe_ffn_forward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _S, _P]),
+    "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P]),
+    "moe_ffn_status": (_I, [ctypes.POINTER(_I), _P]),
+    "moe_prepared_matvec_bytes": (_S, [_I, _I, _I]),
+    "moe_prepare_matvec": (_I, [_P, _P, _I, _I, _I, _P, _S, _P]),
+    "moe_matvec_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "moe_set_wait_limit_ns": (_I, [ctypes.c_ulonglong]),
 }
 
@@ -121,4 +142,14 @@ moe_forward_timed = _call("moe_forward_timed")
 moe_forward_launches = _call("moe_forward_launches")
 moe_get_device_status = _call("moe_get_device_status")
 moe_tensor_peak = _call("moe_tensor_peak")
+moe_block_norm = _call("moe_block_norm")
+moe_block_norm_workspace_bytes = _call("moe_block_norm_workspace_bytes")
+moe_block_norm_backward = _call("moe_block_norm_backward")
+moe_ffn_workspace_bytes = _call("moe_ffn_workspace_bytes")
+moe_ffn_forward = _call("moe_ffn_forward")
+moe_ffn_backward = _call("moe_ffn_backward")
+moe_ffn_status = _call("moe_ffn_status")
+moe_prepared_matvec_bytes = _call("moe_prepared_matvec_bytes")
+moe_prepare_matvec = _call("moe_prepare_matvec")
+moe_matvec_mxfp4 = _call("moe_matvec_mxfp4")
 moe_set_wait_limit_ns = _call("moe_set_wait_limit_ns")

@@ -1,0 +1,609 @@
+// Dense GEMMs of the gated feed-forward block on the 5th-generation tensor cores:
+//   forward   gu = x Wgu^T, h = act(g) u (one kernel);  out = h Wd^T
+//   backward  dh = dout Wd, with dg = dh u act'(g), du = dh act(g) and h again in its
+//             epilogue;  dx = dgu Wgu;  dWgu = dgu^T x;  dWd = dout^T h
+// All are C[m, n] = sum_k A[m, k] B[n, k].  The operands are used as they are stored: a
+// matrix whose rows run along K is a K-major operand, one whose rows run along M or N
+// an MN-major one (both are forms of the same swizzled shared-memory tile), so nothing
+// is transposed in memory.
+//
+// One persistent block per SM.  Warp 0 issues the TMA loads into a ring of stages of 64
+// K values, warp 1 the MMAs into one of two accumulators in tensor memory, warps 2-5 run
+// the epilogue of one tile while the next one's MMAs proceed.  Large products run on
+// pairs of SMs (cta_group::2): the pair computes a 256 x BN tile, each SM loading its
+// own 128 rows of A and half of B, so the bytes an SM must bring in per MMA are halved
+// against a 128-row tile of one SM; the first block of the pair issues the MMAs for both.
+// Sums are f32; g and u are saved in f32 so that the backward's derivatives carry no
+// rounding but their own; h, dg and du are rounded to 16 bits because the next
+// product's tensor-core operands have that type.
+#include "moe_dense.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+using namespace ptx;
+
+namespace {
+
+constexpr int kDenseThreads = 192;
+constexpr uint64_t kDrainLimit = 1000000000ull;  // ns for MMAs already issued (1 s)
+constexpr uint64_t kLandingNs = 20000000ull;     // ns after a time-out in which every issued copy has landed (20 ms)
+
+__device__ uint32_t g_dense_status;  // bits as in the layer's status word
+
+// ------------------------------------------------------------------ PTX of CTA pairs
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc_g(uint32_t* dst, uint32_t ncols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, ncols);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_dealloc_g(uint32_t taddr, uint32_t ncols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
+}
+// 2-D tiled load; in a pair the barrier may be the peer's (a cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16_g(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile("{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, P;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+  else
+    mma_bf16(d, a, b, idesc, accumulate);
+}
+// Arrive on `bar` -- in a pair on both blocks' barrier of that offset -- when the MMAs
+// issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit_g(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float (&f)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+// ------------------------------------------------------------------ configuration
+template <int BN, bool PAIR>
+struct DenseCfg {
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kTileM = 128 * kCtas;
+  static constexpr int kBRows = BN / kCtas;               // rows of B in this block's shared memory
+  static constexpr int kABytes = 128 * 128, kBBytes = kBRows * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 196608 / kStageBytes > 8 ? 8 : 196608 / kStageBytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr uint32_t kTx = (uint32_t)kStageBytes * kCtas;  // the pair's copies all count on one barrier
+  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
+};
+
+// Tiles in groups of kRasterM row tiles, the row tile running fastest inside a group, so
+// the tiles in flight at one time share both operands through L2; K slices slowest.
+constexpr int kRasterM = 8;
+__device__ __forceinline__ void map_tile(int u, int tm, int tn, int& m, int& n, int& split) {
+  split = u / (tm * tn);
+  u -= split * tm * tn;
+  const int first = u / (kRasterM * tn) * kRasterM;
+  const int rows = min(kRasterM, tm - first);
+  const int within = u - first * tn;
+  n = within / rows;
+  m = first + within - n * rows;
+}
+
+template <typename X, int MODE, int BN, bool PAIR>
+__global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __grid_constant__ DenseGemmParams p) {
+  using C = DenseCfg<BN, PAIR>;
+  extern __shared__ uint8_t dense_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dense_smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages], accf_bar[2], acce_bar[2], drain_bar;
+  __shared__ uint32_t tmem_slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf_bar[b], 1);
+      mbar_init(&acce_bar[b], 4 * C::kCtas);  // one lane of each epilogue warp
+    }
+    mbar_init(&drain_bar, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+  }
+  if (warp == 1) tmem_alloc_g<PAIR>(&tmem_slot, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {  // the peer's barriers exist before anything arrives on them
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int units = p.tiles_m * p.tiles_n * p.splits;
+  const int first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
+  auto slice = [&](int split, int& k0, int& k1) {
+    k0 = (int)((long long)split * p.kgroups / p.splits);
+    k1 = (int)((long long)(split + 1) * p.kgroups / p.splits);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full_bar), 0) : smem_u32(full_bar);
+      int g = 0;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step) {
+        int mt, nt, split, k0, k1;
+        map_tile(u, p.tiles_m, p.tiles_n, mt, nt, split);
+        slice(split, k0, k1);
+        const int m0 = mt * C::kTileM + (int)rank * 128;
+        for (int kk = k0; kk < k1; ++kk, ++g) {
+          const int s = g % C::kStages;
+          if (!mbar_wait_bounded(&empty_bar[s], ((g / C::kStages) & 1) ^ 1, p.wait_ns)) {
+            atomicOr(&g_dense_status, kStatusTimeoutProducer);
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], C::kTx);
+          const uint32_t bar = full0 + 8 * s, a = smem_u32(smem + s * C::kStageBytes), b = a + C::kABytes;
+          if (p.a_mn) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tma_load_2d<PAIR>(a + c * 8192, &p.tm_a, bar, m0 + 64 * c, kk * 64);
+          } else {
+            tma_load_2d<PAIR>(a, &p.tm_a, bar, kk * 64, m0);
+          }
+          if (p.b_mn) {
+            const int n0 = nt * BN + (int)rank * C::kBRows;
+#pragma unroll
+            for (int c = 0; c < C::kBRows / 64; ++c) tma_load_2d<PAIR>(b + c * 8192, &p.tm_b, bar, n0 + 64 * c, kk * 64);
+          } else {
+            // boxes of BN / 2 rows: gate then up features, or the two halves of the columns
+#pragma unroll
+            for (int c = 0; c < 2 / C::kCtas; ++c) {
+              const int half = PAIR ? (int)rank : c;
+              const int row = MODE == kDenseGateUp ? half * p.N + nt * (BN / 2) : nt * BN + half * (BN / 2);
+              tma_load_2d<PAIR>(b + c * (BN / 2) * 128, &p.tm_b, bar, kk * 64, row);
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t kFmt = std::is_same<X, __half>::value ? 0u : 1u;  // operand format: f16 0, bf16 1
+      const uint32_t idesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
+                             ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(C::kTileM >> 4) << 24);
+      // K major: rows of 128 bytes in groups of 8 (1024 bytes), 32 bytes per K = 16 step.
+      // MN major: 64 K rows of 128 bytes (64 values) per 8192-byte chunk, 8 K rows per
+      // 1024 bytes, 2048 bytes per K = 16 step.
+      const uint32_t a_lbo = p.a_mn ? 8192 : 16, b_lbo = p.b_mn ? 8192 : 16;
+      const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;  // in 16 bytes
+      const uint32_t base = smem_u32(smem);
+      int g = 0, i = 0;
+      bool ok = true;
+      for (int u = first; u < units && ok; u += step, ++i) {
+        int mt, nt, split, k0, k1;
+        map_tile(u, p.tiles_m, p.tiles_n, mt, nt, split);
+        slice(split, k0, k1);
+        const int b = i & 1;
+        const bool free = PAIR ? mbar_wait_cluster_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns)
+                               : mbar_wait_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
+        if (!free) {
+          atomicOr(&g_dense_status, kStatusTimeoutMain);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + b * BN;
+        for (int kk = k0; kk < k1; ++kk, ++g) {
+          const int s = g % C::kStages;
+          if (!mbar_wait_bounded(&full_bar[s], (g / C::kStages) & 1, p.wait_ns)) {
+            atomicOr(&g_dense_status, kStatusTimeoutMain);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = smem_desc(base + s * C::kStageBytes, a_lbo, 1024, 2);
+          const uint64_t bd = smem_desc(base + s * C::kStageBytes + C::kABytes, b_lbo, 1024, 2);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f16_g<PAIR>(acc, ad + (uint64_t)(a_step * ks), bd + (uint64_t)(b_step * ks), idesc,
+                            kk > k0 || ks > 0 ? 1u : 0u);
+          commit_g<PAIR>(&empty_bar[s]);
+        }
+        if (ok) commit_g<PAIR>(&accf_bar[b]);
+      }
+      // all tensor-core work is done before the tensor memory is freed
+      commit_g<PAIR>(&drain_bar);
+      mbar_wait_bounded(&drain_bar, 0, kDrainLimit);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // tensor-memory lane quarter of this warp
+    int i = 0;
+    for (int u = first; u < units; u += step, ++i) {
+      int mt, nt, split;
+      map_tile(u, p.tiles_m, p.tiles_n, mt, nt, split);
+      const int b = i & 1;
+      if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
+        if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
+        break;
+      }
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * BN;
+      const int m = mt * C::kTileM + (int)rank * 128 + q * 32 + lane;
+      const bool live = m < p.M;
+      X* out = reinterpret_cast<X*>(p.out);
+      if constexpr (MODE == kDenseStore || MODE == kDensePartial) {
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(acc + c, v);
+          tmem_wait_ld();
+          const int n = nt * BN + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (!live || n + j >= p.N) continue;
+            if constexpr (MODE == kDenseStore) {
+              *reinterpret_cast<uint4*>(out + (size_t)m * p.N + n + j) =
+                  make_uint4(pack2<X>(v[j], v[j + 1]), pack2<X>(v[j + 2], v[j + 3]), pack2<X>(v[j + 4], v[j + 5]),
+                             pack2<X>(v[j + 6], v[j + 7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.partial + ((size_t)split * p.M + m) * p.N + n + j);
+              dst[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+              dst[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+            }
+          }
+        }
+      } else if constexpr (MODE == kDenseGateUp) {
+#pragma unroll 1
+        for (int c = 0; c < BN / 2; c += 32) {
+          float gv[32], uv[32];
+          tmem_ld_32x32b_x32(acc + c, gv);
+          tmem_ld_32x32b_x32(acc + BN / 2 + c, uv);
+          tmem_wait_ld();
+          const int n = nt * (BN / 2) + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (!live || n + j >= p.N) continue;
+            if (p.gateup) {
+              float4* dg = reinterpret_cast<float4*>(p.gateup + (size_t)m * 2 * p.N + n + j);
+              float4* du = reinterpret_cast<float4*>(p.gateup + (size_t)m * 2 * p.N + p.N + n + j);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                dg[k] = make_float4(gv[j + 4 * k], gv[j + 4 * k + 1], gv[j + 4 * k + 2], gv[j + 4 * k + 3]);
+                du[k] = make_float4(uv[j + 4 * k], uv[j + 4 * k + 1], uv[j + 4 * k + 2], uv[j + 4 * k + 3]);
+              }
+            }
+            float h[8];
+            if (p.act == kActSilu) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[k] = act_f<kActSilu>(gv[j + k]) * uv[j + k];
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) h[k] = act_f<kActGelu>(gv[j + k]) * uv[j + k];
+            }
+            *reinterpret_cast<uint4*>(out + (size_t)m * p.N + n + j) =
+                make_uint4(pack2<X>(h[0], h[1]), pack2<X>(h[2], h[3]), pack2<X>(h[4], h[5]), pack2<X>(h[6], h[7]));
+          }
+        }
+      } else {
+        X* out_h = reinterpret_cast<X*>(p.out_h);
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          float dh[32];
+          tmem_ld_32x32b_x32(acc + c, dh);
+          tmem_wait_ld();
+          const int n = nt * BN + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (!live || n + j >= p.N) continue;
+            Vec8<float> t;
+            float gv[8], uv[8], dg[8], du[8], h[8];
+            const size_t row = (size_t)m * 2 * p.N;
+            t.load(p.gateup + row + n + j, 0);
+            t.get(gv);
+            t.load(p.gateup + row + p.N + n + j, 0);
+            t.get(uv);
+            auto grad = [&](auto tag) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                float slope;
+                const float a = act_f<decltype(tag)::value>(gv[k], slope);
+                h[k] = a * uv[k];
+                dg[k] = dh[j + k] * uv[k] * slope;
+                du[k] = dh[j + k] * a;
+              }
+            };
+            if (p.act == kActSilu)
+              grad(std::integral_constant<int, kActSilu>{});
+            else
+              grad(std::integral_constant<int, kActGelu>{});
+            Vec8<X> o;
+            o.set(dg);
+            o.store(out + row + n + j, 0);
+            o.set(du);
+            o.store(out + row + p.N + n + j, 0);
+            o.set(h);
+            o.store(out_h + (size_t)m * p.N + n + j, 0);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(mapa_shared(smem_u32(&acce_bar[b]), 0));
+        else
+          mbar_arrive(&acce_bar[b]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) {  // neither block's memory goes while the other may still use it
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  tc_fence_after();
+  // Ordinarily every copy has been consumed by now.  After a time-out of either block
+  // (both see it past the barrier above) some may still be on their way: stay until they
+  // have surely landed.
+  if (threadIdx.x == 0 && __ldcg(&g_dense_status) != 0) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kLandingNs) __nanosleep(1000);
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc_g<PAIR>(tmem, C::kTmemCols);
+}
+
+// Sum of the K slices in slice order, rounded once.  Eight columns per thread.
+template <typename X>
+__global__ void __launch_bounds__(256) dense_join_kernel(const float* partial, int splits, size_t count, X* out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const size_t v = blockIdx.x * (size_t)256 + threadIdx.x;
+  if (v >= count / 8) return;
+  float acc[8];
+  Vec8<float> t;
+  t.load(partial, v);
+  t.get(acc);
+  for (int s = 1; s < splits; ++s) {
+    float f[8];
+    t.load(partial + s * count, v);
+    t.get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += f[i];
+  }
+  Vec8<X> o;
+  o.set(acc);
+  o.store(out, v);
+}
+
+// ------------------------------------------------------------------ host side
+struct Shape {
+  int bn;
+  bool pair;
+  int tiles_m, tiles_n, splits;
+};
+
+// Tile shape.  Pairs of SMs on 256 x 256 tiles once there are rows and tiles for them;
+// one SM on 128 x 128 or 128 x 64 tiles below, where more and smaller tiles keep all SMs
+// streaming weights; K split (a plain store only) while whole tiles leave SMs idle.
+Shape pick_shape(int M, int N, int K, int mode) {
+  const int cols = mode == kDenseGateUp ? 2 * N : N;
+  Shape s{};
+  const long long pair_tiles = (long long)ceil_div(M, 256) * ceil_div(cols, 256);
+  if (M > 128 && pair_tiles >= 48) {
+    s.bn = 256;
+    s.pair = true;
+  } else {
+    s.bn = (long long)ceil_div(M, 128) * ceil_div(cols, 128) >= kMaxCtas ? 128 : 64;
+  }
+  s.tiles_m = ceil_div(M, s.pair ? 256 : 128);
+  s.tiles_n = mode == kDenseGateUp ? ceil_div(N, s.bn / 2) : ceil_div(N, s.bn);
+  s.splits = 1;
+  if (mode == kDenseStore && !s.pair) {
+    const long long tiles = (long long)s.tiles_m * s.tiles_n;
+    const int kg = ceil_div(K, 64);
+    int want = (int)(2LL * kMaxCtas / tiles);
+    if (want > kg / 8) want = kg / 8;  // a slice keeps at least eight stages
+    if (want > 8) want = 8;
+    if (want > 1) s.splits = want;
+  }
+  return s;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiled>(f);
+  });
+  return fn;
+}
+
+// A 16-bit matrix as boxes of 64 columns (128 bytes, swizzled) by `box_rows` rows.
+bool operand_map(CUtensorMap* map, const DenseOperand& o, int box_rows, int dtype) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)o.cols * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return enc(map, dtype == kDtypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(o.ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Blocks that are resident together: pairs may not fill every SM.
+template <typename Kern>
+cudaError_t resident_blocks(Kern kern, int smem, bool pair, std::atomic<int> (&cached)[kMaxDevices], int* blocks) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < kMaxDevices && (*blocks = cached[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  int n = 0;
+  if (pair) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kDenseThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    n *= 2;
+  } else {
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  }
+  if (e != cudaSuccess) return e;
+  if (n < 2) n = 2;
+  if (dev >= 0 && dev < kMaxDevices) cached[dev].store(n, std::memory_order_relaxed);
+  *blocks = n;
+  return cudaSuccess;
+}
+
+template <typename X, int MODE, int BN, bool PAIR>
+cudaError_t launch_kernel(const DenseGemmParams& p, cudaStream_t stream) {
+  using C = DenseCfg<BN, PAIR>;
+  auto kern = dense_gemm_kernel<X, MODE, BN, PAIR>;
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.ensure(kern, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> cached[kMaxDevices] = {};
+  int blocks = 0;
+  e = resident_blocks(kern, C::kSmemBytes, PAIR, cached, &blocks);
+  if (e != cudaSuccess) return e;
+  const long long need = (long long)p.tiles_m * p.tiles_n * p.splits * C::kCtas;
+  if (need < blocks) blocks = (int)need;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kDenseThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <typename X, int MODE>
+cudaError_t launch_shape(const DenseGemmParams& p, const Shape& s, cudaStream_t stream) {
+  if constexpr (MODE != kDensePartial)
+    if (s.pair) return launch_kernel<X, MODE, 256, true>(p, stream);
+  return s.bn == 128 ? launch_kernel<X, MODE, 128, false>(p, stream) : launch_kernel<X, MODE, 64, false>(p, stream);
+}
+
+template <typename X>
+cudaError_t launch_mode(const DenseGemmParams& p, const Shape& s, int mode, cudaStream_t stream) {
+  if (mode == kDenseGateUp) return launch_shape<X, kDenseGateUp>(p, s, stream);
+  if (mode == kDenseGateUpGrad) return launch_shape<X, kDenseGateUpGrad>(p, s, stream);
+  if (s.splits == 1) return launch_shape<X, kDenseStore>(p, s, stream);
+  const cudaError_t e = launch_shape<X, kDensePartial>(p, s, stream);
+  if (e != cudaSuccess) return e;
+  const size_t count = (size_t)p.M * p.N;
+  return launch_pdl(dense_join_kernel<X>, dim3((unsigned)((count / 8 + 255) / 256)), dim3(256), 0, stream,
+                    (const float*)p.partial, p.splits, count, reinterpret_cast<X*>(p.out));
+}
+
+}  // namespace
+
+size_t dense_partial_bytes(int M, int N, int K, int mode) {
+  const Shape s = pick_shape(M, N, K, mode);
+  return s.splits > 1 ? (size_t)s.splits * M * N * sizeof(float) : 0;
+}
+
+int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
+                      cudaStream_t stream) {
+  const Shape s = pick_shape(p.M, p.N, p.K, mode);
+  p.a_mn = a.mn_major;
+  p.b_mn = b.mn_major;
+  p.tiles_m = s.tiles_m;
+  p.tiles_n = s.tiles_n;
+  p.splits = s.splits;
+  p.kgroups = ceil_div(p.K, 64);
+  p.wait_ns = gemm_wait_limit_ns();
+  if (!operand_map(&p.tm_a, a, a.mn_major ? 64 : 128, dtype)) return MOE_ERR_CUDA;
+  if (!operand_map(&p.tm_b, b, b.mn_major ? 64 : s.bn / 2, dtype)) return MOE_ERR_CUDA;
+  const cudaError_t e = dtype == kDtypeF16 ? launch_mode<__half>(p, s, mode, stream)
+                                           : launch_mode<__nv_bfloat16>(p, s, mode, stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+uint32_t* dense_status_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_dense_status) == cudaSuccess ? static_cast<uint32_t*>(p) : nullptr;
+}
+
+}  // namespace moe
