@@ -19,7 +19,7 @@
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *    stream) and never synchronise the host, except moe_prepare_weights,
  *    moe_prepare_matvec, moe_get_device_status, moe_route_noalloc_status,
- *    moe_ffn_status and moe_tensor_peak.
+ *    moe_dense_status and moe_tensor_peak.
  *  - The return value is a status: MOE_OK (0) or a negative MOE_ERR_* code.  On an
  *    error nothing has been launched unless the code is MOE_ERR_CUDA.
  *  - Shapes: 1 <= T, T * k <= 2^24, H % 32 == 0 with 32 <= H <= 8192, I % 32 == 0
@@ -412,12 +412,13 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
                      int T, int H, int I, int act, int dtype, void* d_x, void* d_w_gateup, void* d_w_down,
                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
-/* moe_ffn_status: the device status of the feed-forward GEMMs on the current device,
- * as moe_get_device_status (bits and returns) for one word that the library holds per
- * GPU: synchronises `stream`, reads the word into *status and clears it when set.  A
- * bounded wait that gave up (moe_set_wait_limit_ns) sets it; the results of calls since
- * the last reading are then not reliable.  Not for the hot path.                    */
-int moe_ffn_status(int* status, moe_stream_t stream);
+/* moe_dense_status: the device status of the dense operators' pipelines (feed-forward
+ * GEMMs, MXFP4 products) on the current device, as moe_get_device_status (bits and
+ * returns) for words that the library holds per GPU: synchronises `stream`, reads them
+ * into *status and clears them when set.  A bounded wait that gave up sets a bit (the
+ * GEMMs' limit is moe_set_wait_limit_ns, the products' 1 s); results of calls since the
+ * last reading are then not reliable.  Not for the hot path.                        */
+int moe_dense_status(int* status, moe_stream_t stream);
 
 /* moe_prepare_matvec: one-time re-layout of raw MXFP4 weights [rows][K/2] codes and
  * [rows][K/32] scales (as the expert weights of one expert) for moe_matvec_mxfp4.  The
@@ -436,19 +437,22 @@ int moe_prepare_matvec(const uint8_t* codes, const uint8_t* scales, int rows, in
  *   MOE_WEIGHTS_DOWN:   out[t, n] = sum_k x[t, k] W[n, k] + bias[n]        out [T, rows]
  *   MOE_WEIGHTS_GATEUP: g, u the products (+ bias) of gate row i and up row i,
  *                       out[t, i] = act(g) * u                             out [T, rows/2]
- * The weights are used exactly as stored; sums are f32 in a fixed order, one rounding
- * at the end.  bf16 x is carried as f16 times a power of two per token and K chunk:
- * values below 2^-28 of their chunk's largest lose relative precision (absolute error
- * 2^-39 of that largest), and sums are formed at up to 2^15 times their final size per
- * unit of x, so a group scale above 2^96 may overflow them.
+ * Sums are f32 in a fixed order, one rounding at the end.  The codes are used exactly;
+ * a group whose scale is below 2^-126 of its row's largest counts as zero.  bf16 x is
+ * carried as f16 times a power of two per token: values below 2^-28 of their token's
+ * largest lose relative precision (absolute error 2^-39 of it).
  *   x [T, K] of dtype; bias f32 [rows] or NULL; act is read for MOE_WEIGHTS_GATEUP.
+ *   workspace: moe_matvec_workspace_bytes(T, K) bytes (0 where x fits the
+ *   kernel's shared memory: then it may be NULL), 256-byte aligned, contents irrelevant
+ *   before and after.
  * Source: "triton-kernels" README, "Kernels" (W4A16 GEMM: 4-bit weights with group
  * scales, 16-bit activations), on the layer's MXFP4 format.                         */
+size_t moe_matvec_workspace_bytes(int T, int K);
 int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int rows, int K, int kind, int act,
-                     int dtype, void* out, moe_stream_t stream);
+                     int dtype, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* moe_set_wait_limit_ns: how long (ns) each pipeline wait of the expert GEMMs (and of
- * the dense feed-forward GEMMs, whose status moe_ffn_status reads) may take before it gives up, for launches made after the call (process-wide; 0
+ * the dense feed-forward GEMMs, whose status moe_dense_status reads) may take before it gives up, for launches made after the call (process-wide; 0
  * restores the default of 1 s; at most 10 s, else MOE_ERR_INVALID_ARG).  A wait
  * that gives up sets a bit of the workspace status word (moe_get_device_status), the
  * kernel drops its remaining work, waits (up to 1 s) for the copies and tensor-core

@@ -16,7 +16,8 @@ def __getattr__(name):
         from . import api
         return getattr(api, name)
     if name in ("block_norm", "block_norm_backward", "BlockNormGrads", "ffn_forward", "ffn_backward", "FfnGrads",
-                "ffn_status", "MatvecMXFP4"):
+                "dense_status", "MatvecMXFP4"):
         from . import dense
-        return getattr(dense, name)
+        value = globals()[name] = getattr(dense, name)  # found directly from now on
+        return value
     raise AttributeError(name)

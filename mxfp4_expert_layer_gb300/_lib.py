@@ -73,10 +73,11 @@ SIGNATURES = {
     "moe_ffn_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "moe_ffn_forward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _S, _P]),
     "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P]),
-    "moe_ffn_status": (_I, [ctypes.POINTER(_I), _P]),
+    "moe_dense_status": (_I, [ctypes.POINTER(_I), _P]),
     "moe_prepared_matvec_bytes": (_S, [_I, _I, _I]),
     "moe_prepare_matvec": (_I, [_P, _P, _I, _I, _I, _P, _S, _P]),
-    "moe_matvec_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_matvec_workspace_bytes": (_S, [_I, _I]),
+    "moe_matvec_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _S, _P]),
     "moe_set_wait_limit_ns": (_I, [ctypes.c_ulonglong]),
 }
 
@@ -148,8 +149,9 @@ moe_block_norm_backward = _call("moe_block_norm_backward")
 moe_ffn_workspace_bytes = _call("moe_ffn_workspace_bytes")
 moe_ffn_forward = _call("moe_ffn_forward")
 moe_ffn_backward = _call("moe_ffn_backward")
-moe_ffn_status = _call("moe_ffn_status")
+moe_dense_status = _call("moe_dense_status")
 moe_prepared_matvec_bytes = _call("moe_prepared_matvec_bytes")
 moe_prepare_matvec = _call("moe_prepare_matvec")
+moe_matvec_workspace_bytes = _call("moe_matvec_workspace_bytes")
 moe_matvec_mxfp4 = _call("moe_matvec_mxfp4")
 moe_set_wait_limit_ns = _call("moe_set_wait_limit_ns")

@@ -10,6 +10,18 @@
 
 namespace moe {
 
+// SMs of the current device (looked up once per device).
+inline int device_sms() {
+  static std::atomic<int> cached[kMaxDevices] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return kMaxCtas;
+  const bool keep = dev >= 0 && dev < kMaxDevices;
+  if (keep && (n = cached[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return kMaxCtas;
+  if (keep) cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // ------------------------------------------------------------------ element types
 constexpr int kDtypeBf16 = 0, kDtypeF16 = 1, kDtypeF32 = 2;
 
@@ -153,21 +165,26 @@ cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int dty
                                        cudaStream_t stream);
 
 // ------------------------------------------------------------------ products of a few tokens
-constexpr int kThinTokens = 16;   // tokens of one block of the few-token kernels
+constexpr int kThinTokens = 16;   // tokens of the 16-bit few-token kernel
 constexpr int kThinRows = 16;     // weight rows of one of their tiles (MMA M)
 constexpr int kMatvecMaxTokens = 64;
 
 // Prepared MXFP4 weights of the few-token products.  Tiles of 16 rows (plain: rows 16 i
 // ..; gated: gate rows 8 i .. then up rows 8 i ..), cut along K into units of 128 codes:
-//   codes  [tiles][KU][2][32 lanes][16 bytes]: lane 4 g + t holds, of row g (first half)
-//          or g + 8 (second), word t (codes 8 t .. 8 t + 7) of each of the unit's four
-//          32-code groups, so one 16-byte load per lane and half feeds eight MMAs;
-//   scales [tiles][KU][8 g][2 halves][4 groups] E8M0 bytes;
+//   [tiles / 8][KU][8 tiles] units of 1088 bytes: [2][32 lanes][16 bytes] codes -- lane
+//   4 g + t holds, of row g (first half) or g + 8 (second), word t (codes 8 t .. 8 t + 7)
+//   of each of the unit's four 32-code groups, so one 16-byte read per lane and half feeds
+//   eight MMAs -- then [8 g][2 halves][4 groups] scale bytes, 127 + the E8M0 byte - the
+//   row's largest (0, which counts as a scale of 0, for groups below 2^-126 of it);
+//   [tiles][16] the rows' largest E8M0 bytes;
 //   trailer (256 bytes): set when a scale byte of 255 (NaN) was met.
-// Rows and codes past the matrix are zero codes with scale 127.
+// Tiles are rounded up to eight; rows and codes past the matrix are zero.  Eight tiles' K
+// units, and so a run of K for 128 rows, are contiguous.
+constexpr int kMatvecUnitBytes = 1024 + 64;
+constexpr int kMatvecGroup = 8;
 struct MatvecLayout {
-  int rows, K, gated, tiles, ku;
-  size_t scales_off, flag_off, total;
+  int rows, K, gated, tiles, ku;  // tiles: rounded up to whole groups
+  size_t exp_off, flag_off, total;
 };
 inline MatvecLayout make_matvec_layout(int rows, int K, int gated) {
   MatvecLayout L{};
@@ -175,9 +192,10 @@ inline MatvecLayout make_matvec_layout(int rows, int K, int gated) {
   L.K = K;
   L.gated = gated;
   L.tiles = gated ? ceil_div(rows / 2, kThinRows / 2) : ceil_div(rows, kThinRows);
+  L.tiles = ceil_div(L.tiles, kMatvecGroup) * kMatvecGroup;
   L.ku = ceil_div(K, 128);
-  L.scales_off = (size_t)L.tiles * L.ku * 1024;
-  L.flag_off = align_up(L.scales_off + (size_t)L.tiles * L.ku * 64, 256);
+  L.exp_off = (size_t)L.tiles * L.ku * kMatvecUnitBytes;
+  L.flag_off = align_up(L.exp_off + (size_t)L.tiles * 16, 256);
   L.total = L.flag_off + 256;
   return L;
 }
@@ -191,17 +209,22 @@ cudaError_t launch_matvec_prepare(const MatvecPrepareParams& p, cudaStream_t str
 struct ThinParams {
   const void* x;            // [T, K]
   const void* w;            // prepared MXFP4 tiles, or 16-bit rows [rows, K]
-  const uint8_t* w_sf;      // MXFP4: the prepared scales
   const float* bias;        // f32 [rows] or null (MXFP4 only)
   int T, K, n_out;          // n_out: output features (gated: half the rows)
   int tiles, ku;            // row tiles, K units (128 codes, or 32 16-bit values)
   int act;
-  int prefetch;             // the weights may be read before the dependency wait
+  int kw;                   // MXFP4: K slices (blocks of a cluster)
+  const uint8_t* row_exp;   // MXFP4: the rows' largest E8M0 bytes, tile order
+  uint8_t* packed;          // MXFP4: workspace for x in fragment order
+  float* x_scale;           // MXFP4: and, behind it, its tokens' scales
   void* out;                // [T, n_out]
   float* gateup;            // f32 [T, 2 n_out] or null: the products before the activation
 };
 cudaError_t launch_matvec(const ThinParams& p, int dtype, bool gated, cudaStream_t stream);
 cudaError_t launch_thin16(const ThinParams& p, int dtype, bool gated, cudaStream_t stream);
+size_t matvec_workspace_bytes(int T, int K);
+uint32_t* thin_status_word();  // device addresses on the current device, or null
+uint32_t* dense_status_word();
 
 // ------------------------------------------------------------------ dense GEMMs
 // C[m, n] = sum_k A[m, k] B[n, k] of 16-bit operands, each stored with K or with M / N
@@ -233,6 +256,5 @@ struct DenseOperand {
 size_t dense_partial_bytes(int M, int N, int K, int mode);
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream);
-uint32_t* dense_status_word();  // device address on the current device, or null
 
 }  // namespace moe

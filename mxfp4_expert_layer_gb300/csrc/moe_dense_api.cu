@@ -186,11 +186,19 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
   return MOE_OK;
 }
 
-int moe_ffn_status(int* status, moe_stream_t stream) {
+int moe_dense_status(int* status, moe_stream_t stream) {
   if (!status) return MOE_ERR_INVALID_ARG;
-  uint32_t* word = dense_status_word();
-  if (!word) return MOE_ERR_CUDA;
-  return read_and_clear_status(word, sizeof(uint32_t), reinterpret_cast<cudaStream_t>(stream), status);
+  uint32_t* words[] = {dense_status_word(), thin_status_word()};
+  int all = 0;
+  for (uint32_t* word : words) {
+    if (!word) return MOE_ERR_CUDA;
+    int bits = 0;
+    const int st = read_and_clear_status(word, sizeof(uint32_t), reinterpret_cast<cudaStream_t>(stream), &bits);
+    if (st == MOE_ERR_CUDA) return st;
+    all |= bits;
+  }
+  *status = all;
+  return all ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
 
 int moe_block_norm(const void* block, const void* norm_weight, const void* gate, int gate_kind, const void* residual,
@@ -275,18 +283,27 @@ int moe_prepare_matvec(const uint8_t* codes, const uint8_t* scales, int rows, in
   return h ? MOE_ERR_NAN_SCALE : MOE_OK;
 }
 
+size_t moe_matvec_workspace_bytes(int T, int K) {
+  if (T < 1 || T > kMatvecMaxTokens || K < 32 || K > kMaxMatvecDim || K % 32) return 0;
+  return matvec_workspace_bytes(T, K);
+}
+
 int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int rows, int K, int kind, int act,
-                     int dtype, void* out, moe_stream_t stream) {
+                     int dtype, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   if (T < 1 || T > kMatvecMaxTokens || moe_prepared_matvec_bytes(rows, K, kind) == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!dtype16(dtype) || (act != MOE_ACT_SILU && act != MOE_ACT_GELU)) return MOE_ERR_INVALID_ARG;
   if (!x || !w || !out || !aligned(x, 16) || !aligned(w, 256) || !aligned(out, 16) || !aligned(bias, 4))
     return MOE_ERR_INVALID_ARG;
+  const size_t need = matvec_workspace_bytes(T, K);
+  if (need && (!workspace || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
+  if (need > workspace_bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const bool gated = kind == MOE_WEIGHTS_GATEUP;
   const MatvecLayout L = make_matvec_layout(rows, K, gated);
   ThinParams p{};
   p.x = x;
   p.w = w;
-  p.w_sf = static_cast<const uint8_t*>(w) + L.scales_off;
+  p.row_exp = static_cast<const uint8_t*>(w) + L.exp_off;
+  p.packed = static_cast<uint8_t*>(workspace);
   p.bias = bias;
   p.T = T;
   p.K = K;

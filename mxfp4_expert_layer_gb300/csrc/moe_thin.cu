@@ -3,19 +3,17 @@
 //   plain  y[t, n] = sum_k x[t, k] W[n, k] (+ bias[n])
 //   gated  h[t, i] = act(g) u,  g and u the products with gate row i and up row i
 //
-// At these sizes every weight byte is read once and used for at most 16 tokens, so the
-// kernels are bound by HBM, and what matters is the bytes in flight and the
-// instructions spent per weight.  One block takes RT tiles of 16 weight rows; its eight
-// warps split K and add their sums through shared memory in warp order (no partial
-// sums leave the block, and the order is fixed).  The products run on mma.sync
-// (m16n8k16, f32 sums): the weights are the 16-row operand, up to 8 tokens a column
-// group.  The sum over K is free to take its terms in any order, so each lane's
-// 16-byte weight load is its own operand fragments, with x permuted to match: no
-// shuffles and no shared memory on the weight side.
+// At these sizes every weight byte is read once and used for a few tokens, so the kernels
+// are bound by HBM, and what matters is the bytes in flight and the instructions spent
+// per weight.  The products run on mma.sync (m16n8k16, f32 sums): 16 weight rows are one
+// operand, the other up to 8 tokens a column group.  The sum over K is free to take its terms in any order, so each lane's
+// 16-byte weight read is its own operand fragments, with x permuted to match: no
+// shuffles.  Sums are added in a fixed order everywhere.
 //
 // MXFP4: two codes become an f16 pair by one conversion instruction (exact); a group's
-// 32 products are summed by two MMAs and then scaled in f32 by the group's E8M0 scale.
-// x as f16: a power of two per (token, K chunk) brings its largest value to [2^14,
+// 32 products are summed by two MMAs and then scaled in f32 by the group's scale, kept
+// relative to the largest of its row (taken out of the sum once, at the end).
+// x as f16: a power of two per (token, 128 values) brings its largest value to [2^14,
 // 2^15), so bf16 values are exact down to 2^-28 of the largest (absolute error 2^-39 of
 // it below), and is taken out again in f32.
 #include "moe_dense.cuh"
@@ -26,6 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kThinThreads = 256;
+__device__ uint32_t g_thin_status;  // bits as in the layer's status word
 constexpr int kThinWarps = kThinThreads / 32;
 
 template <typename X>
@@ -34,7 +33,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 template <>
 __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                  uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
                "%2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -42,10 +41,19 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uin
 template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, "
                "%1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d = a b of f16 operands (no addend).
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+               "%10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The eight E2M1 codes of a word as four f16 pairs (low nibble first).
@@ -57,9 +65,9 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
-// 2^(byte - 127); byte 0 is the subnormal 2^-127.
-__device__ __forceinline__ float e8m0_f32(uint32_t word, int b) {
-  return __uint_as_float(max(((word >> (8 * b)) & 0xFFu) << 23, 0x00400000u));
+// Byte b of a prepared scale word as 2^(byte - 127), 0 for byte 0 (bytes are at most 127).
+__device__ __forceinline__ float group_scale(uint32_t word, int b) {
+  return __uint_as_float(__byte_perm(word, 0, 0x0444 | (b << 12)) >> 1);
 }
 
 __device__ __forceinline__ uint4 load_weights(const void* p) {
@@ -70,8 +78,12 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
   return v;
 }
 
-// Adds the warps' sums (fragment layout: register pair c < 2 is row g, c >= 2 row g + 8,
-// token 2 t + (c & 1)) in warp order and writes the block's outputs.
+// Adds the eight warps' sums (fragment layout: register pair c < 2 is row g, c >= 2 row
+// g + 8, token 2 t + (c & 1)) in warp order and writes the block's outputs.
+template <int NT, int RT>
+__device__ __host__ constexpr int finish_bytes() {
+  return kThinWarps * NT * 8 * (RT * kThinRows + 4) * 4;
+}
 template <typename X, int NT, int RT, bool GATED, int ACT>
 __device__ __forceinline__ void finish(const ThinParams& p, const float (&total)[RT][NT][4], float* red, int tile0,
                                        int t0, int nt) {
@@ -99,11 +111,7 @@ __device__ __forceinline__ void finish(const ThinParams& p, const float (&total)
     if constexpr (GATED) {
       const int f = tile0 * 8 + o, r = (o >> 3) * 16 + (o & 7);
       if (f >= p.n_out) continue;
-      float gv = sum(r), uv = sum(r + 8);
-      if (p.bias) {
-        gv += p.bias[f];
-        uv += p.bias[p.n_out + f];
-      }
+      const float gv = sum(r), uv = sum(r + 8);
       if (p.gateup) {
         p.gateup[row * 2 * p.n_out + f] = gv;
         p.gateup[row * 2 * p.n_out + p.n_out + f] = uv;
@@ -111,167 +119,382 @@ __device__ __forceinline__ void finish(const ThinParams& p, const float (&total)
       out[row * p.n_out + f] = static_cast<X>(act_f<ACT>(gv) * uv);
     } else {
       const int f = tile0 * 16 + o;
-      if (f >= p.n_out) continue;
-      float v = sum(o);
-      if (p.bias) v += p.bias[f];
-      out[row * p.n_out + f] = static_cast<X>(v);
+      if (f < p.n_out) out[row * p.n_out + f] = static_cast<X>(sum(o));
     }
   }
+}
+
+// x as f16.  bf16: a power of two that brings the largest finite exponent (of the values
+// scaled together) to 14 takes values to f16, and its inverse is returned; f16 as it is.
+template <typename X>
+__device__ __forceinline__ uint32_t max_exponent(const uint4& v) {
+  if constexpr (std::is_same<X, __half>::value) return 0;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t e = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = (w[j] >> 7) & 0xFFu, hi = (w[j] >> 23) & 0xFFu;
+    e = max(e, max(lo == 255u ? 0u : lo, hi == 255u ? 0u : hi));
+  }
+  return e;
+}
+template <typename X>
+__device__ __forceinline__ float scale_to_f16(uint4& v, uint32_t emax) {
+  if constexpr (std::is_same<X, __half>::value) return 1.f;
+  const int pw = emax == 0 ? 0 : min(126, 14 + 127 - (int)emax);
+  const float up = pow2_int(pw);
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack2<__nv_bfloat16>(w[j]);
+    w[j] = pack2<__half>(f.x * up, f.y * up);
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+  return pow2_int(-pw);
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t base, uint32_t off) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(base + off));
+  return v;
 }
 
 // ------------------------------------------------------------------ MXFP4 weights
-template <typename X, int NT, int RT>
-struct MatvecCfg {
-  static constexpr int kUnits = RT == 4 ? 1 : RT == 2 ? 2 : 4;  // K units per chunk: 4 unit tiles in flight
-  static constexpr int kRowHalves = kUnits * 128 + 32;          // x row in shared memory (64 bytes of padding)
-  static int smem(int tokens) {
-    const int x = kThinWarps * tokens * kRowHalves * 2;
-    const int red = kThinWarps * NT * 8 * (RT * kThinRows + 4) * 4;
-    return x > red ? x : red;
-  }
-};
+// A block's eight warps take a tile each and walk K together.  A pipeline stage is one or
+// two K units of the block's tiles (contiguous in the prepared weights: one bulk copy)
+// and, where x is not resident, the same units of x; the warps refill the stages in turn.  So the bytes in flight do not depend on registers or on how
+// far the arithmetic has got, and the 16-byte shared-memory reads are the fragments.
+// x, as f16, comes in one of two ways:
+//   resident (few tokens, short K): the block converts it itself, once; rows padded by 64
+//     bytes, so that two tokens' 64-byte pieces fall into different banks;
+//   packed: a launch before wrote it to the workspace in fragment order.
+// Blocks are persistent over row groups; where there are too few groups to fill the GPU,
+// a cluster of blocks splits K and adds its sums through distributed shared memory, in
+// rank order.
+constexpr int kUnitBytes = kMatvecUnitBytes;
+constexpr int kGroupBytes = kMatvecGroup * kUnitBytes;  // one K unit of eight tiles
+constexpr uint64_t kMatvecWaitNs = 1000000000ull;       // a wait may take 1 s
+constexpr int kResidentPieces = 64;                     // resident x: (token, unit) pairs, at most
+static_assert(kMatvecGroup == kThinWarps, "one tile per warp and group");
 
-template <typename X, int NT, int RT, bool GATED, int ACT>
-__global__ void __launch_bounds__(kThinThreads) matvec_kernel(const __grid_constant__ ThinParams p) {
-  using C = MatvecCfg<X, NT, RT>;
-  extern __shared__ __align__(128) uint8_t thin_smem[];
-  __shared__ float s_scale[kThinWarps][NT * 8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tile0 = blockIdx.x * RT, t0 = blockIdx.y * kThinTokens;
-  const int nt = min(p.T - t0, NT * 8);
-  const int u_end = (int)((long long)(warp + 1) * p.ku / kThinWarps);
-  int u = (int)((long long)warp * p.ku / kThinWarps);
-  uint16_t* xs = reinterpret_cast<uint16_t*>(thin_smem) + (size_t)warp * nt * C::kRowHalves;
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  float total[RT][NT][4] = {};
-  for (; u < u_end; u += C::kUnits) {
-    // this chunk's weights, all loads in flight at once
-    uint4 wr[RT][C::kUnits][2];
-    uint2 sc[RT][C::kUnits];
+template <int NT, bool PACKED>
+struct MatvecCfg {
+  static constexpr int kPerSm = NT == 4 ? 2 : 3;  // resident blocks, by registers
+  // K units per stage: two where registers and memory allow (the eight warps meet at every
+  // stage; one token x 131072 x 4096: 53.6 us, 60.8 with one unit and twice the stages)
+  static constexpr int kUnits = NT == 1 ? 2 : 1;
+  static constexpr int kStages = NT == 1 ? 3 : NT == 2 ? 5 : 6;
+  static constexpr int kUnitTotal = kGroupBytes + (PACKED ? NT * 2048 : 0);
+  static constexpr int kStageBytes = kUnits * kUnitTotal;
+  static constexpr int kStride = kMatvecGroup * kThinRows + 4;  // a token's sums, where a cluster adds them
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static_assert(NT * 8 * kStride * 4 <= kRingBytes, "the sums take the ring's memory");
+};
+__host__ __device__ inline int resident_row_halves(int ku) { return ku * 128 + 32; }
+inline bool matvec_resident(int tokens, int ku) { return tokens <= 8 && tokens * ku <= kResidentPieces; }
+
+// One K unit of a row tile against NT column groups: `sum` += products, scaled by the
+// groups' scales.  `read_x(blk, n8)` gives this lane's x fragment.
+template <int NT, typename ReadX>
+__device__ __forceinline__ void unit_product(const uint8_t* unit, float (&sum)[NT][4], ReadX read_x) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  const uint4 w0 = *reinterpret_cast<const uint4*>(unit + lane * 16);
+  const uint4 w1 = *reinterpret_cast<const uint4*>(unit + 512 + lane * 16);
+  const uint2 sc = *reinterpret_cast<const uint2*>(unit + 1024 + g * 8);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const size_t tile = min(tile0 + rt, p.tiles - 1);
+  for (int blk = 0; blk < 4; ++blk) {
+    uint32_t h0[4], h1[4];
+    e2m1x8_to_f16(blk == 0 ? w0.x : blk == 1 ? w0.y : blk == 2 ? w0.z : w0.w, h0);
+    e2m1x8_to_f16(blk == 0 ? w1.x : blk == 1 ? w1.y : blk == 2 ? w1.z : w1.w, h1);
+    const float s0 = group_scale(sc.x, blk), s1 = group_scale(sc.y, blk);
 #pragma unroll
-      for (int j = 0; j < C::kUnits; ++j) {
-        const size_t unit = tile * p.ku + min(u + j, p.ku - 1);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(p.w) + unit * 1024 + lane * 16;
-        wr[rt][j][0] = load_weights(src);
-        wr[rt][j][1] = load_weights(src + 512);
-        sc[rt][j] = __ldg(reinterpret_cast<const uint2*>(p.w_sf + unit * 64) + g);
-      }
-    }
-    // x of this chunk as f16 in shared memory (this warp's own), zero past K and past
-    // the warp's last unit
-    const int k0 = u * 128, k1 = min(u_end * 128, p.K);
-    __syncwarp();
-    for (int tok = 0; tok < nt; ++tok) {
-      const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + (size_t)(t0 + tok) * p.K);
-      constexpr int kVecs = C::kUnits * 16, kPer = (kVecs + 31) / 32;
-      uint4 v[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int q = lane + 32 * i;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (q < kVecs && k0 + 8 * q < k1) v[i] = __ldcg(row + (k0 >> 3) + q);
-      }
-      if constexpr (sizeof(X) == 2 && !std::is_same<X, __half>::value) {
-        // largest finite exponent of the chunk, then x * 2^p with that exponent at 14
-        uint32_t emax = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = (w[j] >> 7) & 0xFFu, hi = (w[j] >> 23) & 0xFFu;
-            emax = max(emax, max(lo == 255u ? 0u : lo, hi == 255u ? 0u : hi));
-          }
-        }
-        emax = __reduce_max_sync(0xffffffffu, emax);
-        const int pw = emax == 0 ? 0 : min(126, 14 + 127 - (int)emax);
-        const float up = pow2_int(pw);
-        if (lane == 0) s_scale[warp][tok] = pow2_int(-pw);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack2<__nv_bfloat16>(w[j]);
-            w[j] = pack2<__half>(f.x * up, f.y * up);
-          }
-          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int q = lane + 32 * i;
-        if (q < kVecs) *reinterpret_cast<uint4*>(xs + tok * C::kRowHalves + 8 * q) = v[i];
-      }
-    }
-    __syncwarp();
-    float acc[RT][NT][4] = {};
-#pragma unroll
-    for (int j = 0; j < C::kUnits; ++j) {
-      if (u + j >= u_end) break;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint4 xf[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          xf[n] = make_uint4(0, 0, 0, 0);
-          if (g + 8 * n < nt)
-            xf[n] = *reinterpret_cast<const uint4*>(xs + (g + 8 * n) * C::kRowHalves + j * 128 + 32 * b + 8 * t);
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint4 w0 = wr[rt][j][0], w1 = wr[rt][j][1];
-          uint32_t h0[4], h1[4];
-          e2m1x8_to_f16(b == 0 ? w0.x : b == 1 ? w0.y : b == 2 ? w0.z : w0.w, h0);
-          e2m1x8_to_f16(b == 0 ? w1.x : b == 1 ? w1.y : b == 2 ? w1.z : w1.w, h1);
-          const float s0 = e8m0_f32(sc[rt][j].x, b), s1 = e8m0_f32(sc[rt][j].y, b);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<__half>(d, h0[0], h1[0], h0[1], h1[1], xf[n].x, xf[n].y);
-            mma16816<__half>(d, h0[2], h1[2], h0[3], h1[3], xf[n].z, xf[n].w);
-            acc[rt][n][0] = fmaf(d[0], s0, acc[rt][n][0]);
-            acc[rt][n][1] = fmaf(d[1], s0, acc[rt][n][1]);
-            acc[rt][n][2] = fmaf(d[2], s1, acc[rt][n][2]);
-            acc[rt][n][3] = fmaf(d[3], s1, acc[rt][n][3]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float q0 = 1.f, q1 = 1.f;
-      if constexpr (!std::is_same<X, __half>::value) {
-        const int a = 8 * n + 2 * t;
-        q0 = a < nt ? s_scale[warp][a] : 0.f;
-        q1 = a + 1 < nt ? s_scale[warp][a + 1] : 0.f;
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        total[rt][n][0] = fmaf(acc[rt][n][0], q0, total[rt][n][0]);
-        total[rt][n][1] = fmaf(acc[rt][n][1], q1, total[rt][n][1]);
-        total[rt][n][2] = fmaf(acc[rt][n][2], q0, total[rt][n][2]);
-        total[rt][n][3] = fmaf(acc[rt][n][3], q1, total[rt][n][3]);
-      }
+    for (int n8 = 0; n8 < NT; ++n8) {
+      const uint4 x = read_x(blk, n8);
+      float d[4];
+      mma16816_zero(d, h0[0], h1[0], h0[1], h1[1], x.x, x.y);
+      mma16816<__half>(d, h0[2], h1[2], h0[3], h1[3], x.z, x.w);
+      sum[n8][0] = fmaf(d[0], s0, sum[n8][0]);
+      sum[n8][1] = fmaf(d[1], s0, sum[n8][1]);
+      sum[n8][2] = fmaf(d[2], s1, sum[n8][2]);
+      sum[n8][3] = fmaf(d[3], s1, sum[n8][3]);
     }
   }
-  __syncthreads();  // every warp is done with its x before the sums take the same memory
-  finish<X, NT, RT, GATED, ACT>(p, total, reinterpret_cast<float*>(thin_smem), tile0, t0, nt);
 }
 
-// One thread per 16-byte chunk of the prepared codes, then one per scale byte.
+// A product's row scale: 2^(byte - 127) of the row's largest group scale; byte 0 is the
+// subnormal 2^-127.
+__device__ __forceinline__ float row_scale(const ThinParams& p, int tile_row) {
+  return __uint_as_float(max((uint32_t)__ldg(p.row_exp + tile_row) << 23, 0x00400000u));
+}
+
+// ---- packed x: [token group][K units][4 groups][NT][32 lanes][16 bytes] f16, then the
+// tokens' f32 scales.  One block per token of the padded groups.
+template <int NT>
+inline size_t packed_bytes(int T, int ku) { return (size_t)ceil_div(T, NT * 8) * ku * NT * 2048; }
+
+template <typename X, int NT>
+__global__ void __launch_bounds__(256) matvec_pack_kernel(const __grid_constant__ ThinParams p) {
+  __shared__ uint32_t s_max[8];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int tok = blockIdx.x, vecs = p.ku * 16;
+  const uint4* row = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + (size_t)tok * p.K);
+  auto load = [&](int i) { return tok < p.T && 8 * i < p.K ? __ldcg(row + i) : make_uint4(0, 0, 0, 0); };
+  uint4 first[4];  // rows of up to 8192 values are read once
+  uint32_t emax = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = threadIdx.x + 256 * j;
+    first[j] = i < vecs ? load(i) : make_uint4(0, 0, 0, 0);
+    emax = max(emax, max_exponent<X>(first[j]));
+  }
+  for (int i = threadIdx.x + 1024; i < vecs; i += 256) emax = max(emax, max_exponent<X>(load(i)));
+  emax = __reduce_max_sync(0xffffffffu, emax);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = emax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) emax = max(emax, s_max[w]);
+  const int group = tok / (NT * 8), r = tok - group * NT * 8;
+  float down = 1.f;
+  auto put = [&](int i, uint4 v) {
+    down = scale_to_f16<X>(v, emax);
+    // vector i: unit i / 16, its group (i % 16) / 4, fragment lane 4 (token % 8) + i % 4
+    uint8_t* unit = p.packed + ((size_t)group * p.ku + (i >> 4)) * (NT * 2048);
+    *reinterpret_cast<uint4*>(unit + (((i >> 2) & 3) * NT + (r >> 3)) * 512 + (4 * (r & 7) + (i & 3)) * 16) = v;
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = threadIdx.x + 256 * j;
+    if (i < vecs) put(i, first[j]);
+  }
+  for (int i = threadIdx.x + 1024; i < vecs; i += 256) put(i, load(i));
+  if (threadIdx.x == 0) p.x_scale[tok] = down;
+}
+
+template <typename X, int NT, bool PACKED, bool GATED, int ACT>
+__global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
+    matvec_kernel(const __grid_constant__ ThinParams p) {
+  using C = MatvecCfg<NT, PACKED>;
+  static_assert(PACKED || NT == 1, "resident x: one column group");
+  extern __shared__ __align__(128) uint8_t thin_smem[];
+  __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
+  __shared__ uint32_t s_max[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int S = p.kw, rank = blockIdx.x % S, groups = p.tiles / kMatvecGroup;
+  const int t0 = blockIdx.y * NT * 8, nt = min(p.T - t0, NT * 8);
+  const int k_begin = rank * p.ku / S, k_end = (rank + 1) * p.ku / S, steps = ceil_div(k_end - k_begin, C::kUnits);
+  const int grp_step = gridDim.x / S, grp0 = blockIdx.x / S;
+  const int all = grp0 < groups ? (groups - grp0 + grp_step - 1) / grp_step * steps : 0;  // stages of this block
+  uint8_t* const xs = thin_smem + C::kRingBytes;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      ptx::mbar_init(&full_bar[i], 1);
+      ptx::mbar_init(&empty_bar[i], kThinWarps);
+    }
+    ptx::fence_mbar_init();
+  }
+  if (!PACKED && threadIdx.x < 8) s_max[threadIdx.x] = 0;
+  __syncthreads();
+  // stage i of the block: its weights, and its units of x
+  auto issue_w = [&](int i) {
+    const int u = k_begin + i % steps * C::kUnits, n = min(C::kUnits, k_end - u);
+    uint64_t* bar = &full_bar[i % C::kStages];
+    ptx::mbar_arrive_expect_tx(bar, n * C::kUnitTotal);
+    ptx::bulk_load(thin_smem + i % C::kStages * C::kStageBytes,
+                   reinterpret_cast<const uint8_t*>(p.w) + ((size_t)(grp0 + i / steps * grp_step) * p.ku + u) * kGroupBytes,
+                   n * kGroupBytes, bar);
+  };
+  auto issue_x = [&](int i) {
+    const int u = k_begin + i % steps * C::kUnits, n = min(C::kUnits, k_end - u);
+    ptx::bulk_load(thin_smem + i % C::kStages * C::kStageBytes + C::kUnits * kGroupBytes,
+                   p.packed + ((size_t)blockIdx.y * p.ku + u) * (NT * 2048), n * NT * 2048, &full_bar[i % C::kStages]);
+  };
+  // Weights of packed x's kernel may be read before the dependency wait: the launch before
+  // it is the packing one, which began its work only when all earlier work had completed.
+  if (PACKED && threadIdx.x == 0)
+    for (int i = 0; i < C::kStages && i < all; ++i) issue_w(i);
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (threadIdx.x == 0)
+    for (int i = 0; i < C::kStages && i < all; ++i) {
+      if (PACKED) issue_x(i);
+      else issue_w(i);
+    }
+  float down[2] = {1.f, 1.f};  // scales of x's tokens 2 t, 2 t + 1 (resident x)
+  const int row_halves = resident_row_halves(p.ku);
+  if constexpr (!PACKED) {
+    // 16 lanes take one (token, unit), 8 values each; zero past K
+    const int pieces = nt * p.ku, l = lane & 15;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = (threadIdx.x >> 4) + 16 * i, tok = q / p.ku, u = q - tok * p.ku, k = u * 128 + l * 8;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (q < pieces && k < p.K) {
+        v[i] = __ldcg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + (size_t)tok * p.K + k));
+        if constexpr (!std::is_same<X, __half>::value) atomicMax(&s_max[tok], max_exponent<X>(v[i]));
+      }
+    }
+    if constexpr (!std::is_same<X, __half>::value) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = (threadIdx.x >> 4) + 16 * i, tok = q / p.ku, u = q - tok * p.ku;
+      if (q >= pieces) continue;
+      scale_to_f16<X>(v[i], s_max[tok]);
+      *reinterpret_cast<uint4*>(xs + ((size_t)tok * row_halves + u * 128 + l * 8) * 2) = v[i];
+    }
+    __syncthreads();
+    if constexpr (!std::is_same<X, __half>::value) {
+      uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) down[c] = scale_to_f16<X>(none, s_max[min(2 * t + c, 7)]);
+    }
+  }
+  // resident x: lanes of absent tokens read the last token's row; their columns are never written
+  const uint8_t* const x_row = xs + (min(g, nt - 1) * row_halves + 8 * t) * 2;
+  X* const out = reinterpret_cast<X*>(p.out);
+
+  int i = 0;
+  bool ok = true;
+  for (int grp = grp0; grp < groups; grp += grp_step) {
+    float total[NT][4] = {};
+    for (int u0 = k_begin; u0 < k_end; u0 += C::kUnits, ++i) {
+      const int s = i % C::kStages;
+      if (ok && !ptx::mbar_wait_bounded(&full_bar[s], (i / C::kStages) & 1, kMatvecWaitNs)) ok = false;
+      const uint8_t* st = thin_smem + s * C::kStageBytes;
+#pragma unroll
+      for (int j = 0; j < C::kUnits; ++j) {
+        if (u0 + j >= k_end) break;
+        unit_product<NT>(st + j * kGroupBytes + warp * kUnitBytes, total, [&](int blk, int n8) {
+          if constexpr (PACKED)
+            return *reinterpret_cast<const uint4*>(st + C::kUnits * kGroupBytes + ((j * 4 + blk) * NT + n8) * 512 + lane * 16);
+          else
+            return *reinterpret_cast<const uint4*>(x_row + ((u0 + j) * 128 + 32 * blk) * 2);
+        });
+      }
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&empty_bar[s]);
+        // refill the stage before this one, which the other warps have most likely left too
+        const int prev = i - 1, next = prev + C::kStages;
+        if (warp == i % kThinWarps && prev >= 0 && next < all) {
+          if (!ptx::mbar_wait_bounded(&empty_bar[prev % C::kStages], (prev / C::kStages) & 1, kMatvecWaitNs)) ok = false;
+          if (ok) {
+            issue_w(next);
+            if (PACKED) issue_x(next);
+          }
+        }
+      }
+    }
+    const int tile0 = grp * kMatvecGroup;
+    if (S == 1) {
+      // this warp's outputs straight from its fragments: row g and g + 8, tokens 2 t, 2 t + 1
+      const int tile = tile0 + warp, f = tile * (GATED ? 8 : 16) + g;
+      if (f >= p.n_out) continue;
+      const int f8 = GATED ? p.n_out + f : f + 8;  // the weight row of the second half
+      const bool low = GATED || f8 < p.n_out;
+      const float b0 = p.bias ? p.bias[f] : 0.f, b1 = p.bias && low ? p.bias[f8] : 0.f;
+      const float r0 = row_scale(p, tile * 16 + g), r1 = row_scale(p, tile * 16 + g + 8);
+#pragma unroll
+      for (int n8 = 0; n8 < NT; ++n8)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int tok = 8 * n8 + 2 * t + c;
+          if (tok >= nt) continue;
+          const size_t row = (size_t)(t0 + tok) * p.n_out;
+          const float q = PACKED ? __ldcg(p.x_scale + t0 + tok) : down[c];
+          const float v0 = fmaf(total[n8][c] * q, r0, b0), v1 = fmaf(total[n8][2 + c] * q, r1, b1);
+          if constexpr (GATED) {
+            out[row + f] = static_cast<X>(act_f<ACT>(v0) * v1);
+          } else {
+            out[row + f] = static_cast<X>(v0);
+            if (low) out[row + f8] = static_cast<X>(v1);
+          }
+        }
+    } else {
+      // (one group per cluster) the blocks' sums, [token][row], in the ring's memory: every
+      // copy has been consumed
+      __syncthreads();
+      float* red = reinterpret_cast<float*>(thin_smem);
+#pragma unroll
+      for (int n8 = 0; n8 < NT; ++n8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          red[(n8 * 8 + 2 * t + (c & 1)) * C::kStride + warp * 16 + g + 8 * (c >> 1)] =
+              PACKED ? total[n8][c] : total[n8][c] * down[c & 1];
+      ptx::cluster_arrive_release();
+      ptx::cluster_wait_acquire();
+      // this block's share of the tiles
+      const int a = rank * kMatvecGroup / S, share = kMatvecGroup / S * (GATED ? 8 : 16);
+      const uint32_t red0 = ptx::smem_u32(red);
+      for (int o = threadIdx.x; o < nt * share; o += kThinThreads) {
+        const int tok = o / share, e = o - tok * share;
+        auto sum = [&](int r) {
+          float v = 0.f;
+          for (int s = 0; s < S; ++s) v += ld_cluster_f32(ptx::mapa_shared(red0, s), (tok * C::kStride + r) * 4);
+          if (PACKED) v *= __ldcg(p.x_scale + t0 + tok);
+          return v * row_scale(p, tile0 * 16 + r);
+        };
+        const size_t row = (size_t)(t0 + tok) * p.n_out;
+        const int f = (tile0 + a) * (GATED ? 8 : 16) + e;
+        if (f >= p.n_out) continue;
+        if constexpr (GATED) {
+          const int r = a * 16 + (e >> 3) * 16 + (e & 7);
+          float gv = sum(r), uv = sum(r + 8);
+          if (p.bias) {
+            gv += p.bias[f];
+            uv += p.bias[p.n_out + f];
+          }
+          out[row + f] = static_cast<X>(act_f<ACT>(gv) * uv);
+        } else {
+          float v = sum(a * 16 + e);
+          if (p.bias) v += p.bias[f];
+          out[row + f] = static_cast<X>(v);
+        }
+      }
+      ptx::cluster_arrive_release();  // the peers have read this block's sums
+      ptx::cluster_wait_acquire();
+    }
+  }
+  // a copy waited for in vain may still land: report, and stay until it surely has
+  if (!ok) {
+    report_status(&g_thin_status, kStatusTimeoutMain);
+    const uint64_t start = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - start < kMatvecWaitNs / 50) __nanosleep(1000);
+  }
+}
+
+// The largest group scale of each weight row, in tile order (127 past the matrix).
+__device__ __forceinline__ long long matvec_raw_row(const MatvecLayout& L, long long tile, int r) {
+  if (!L.gated) return tile * 16 + r < L.rows ? tile * 16 + r : -1;
+  const long long f = tile * 8 + (r & 7);
+  return f < L.rows / 2 ? f + (r >= 8 ? L.rows / 2 : 0) : -1;
+}
+// Byte offset of a tile's K unit.
+__device__ __forceinline__ size_t matvec_unit_offset(const MatvecLayout& L, long long tile, int u) {
+  return (((size_t)(tile / kMatvecGroup) * L.ku + u) * kMatvecGroup + tile % kMatvecGroup) * kMatvecUnitBytes;
+}
+__global__ void __launch_bounds__(256) matvec_row_exp_kernel(MatvecPrepareParams p) {
+  const MatvecLayout& L = p.L;
+  const long long i = (blockIdx.x * 256LL + threadIdx.x) >> 5;
+  if (i >= (long long)L.tiles * 16) return;  // whole warps
+  const long long row = matvec_raw_row(L, i >> 4, (int)(i & 15));
+  const int groups = L.K / 32;
+  uint32_t m = 0;
+  if (row >= 0)
+    for (int b = threadIdx.x & 31; b < groups; b += 32) {
+      const uint32_t s = p.scales[(size_t)row * groups + b];
+      if (s == 255) atomicOr(reinterpret_cast<unsigned int*>(p.dst + L.flag_off), 1u);
+      m = max(m, s);
+    }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) p.dst[L.exp_off + i] = row >= 0 ? (uint8_t)m : 127;
+}
+
+// One thread per 16-byte chunk of the prepared codes, then one per scale byte (relative
+// to its row's largest, which the kernel before found).
 __global__ void matvec_prepare_kernel(MatvecPrepareParams p) {
   const MatvecLayout& L = p.L;
-  const int half_rows = L.rows / 2, groups = L.K / 32;
-  auto row_of = [&](long long tile, int r) -> long long {  // raw row, or -1
-    if (!L.gated) return tile * 16 + r < L.rows ? tile * 16 + r : -1;
-    const long long f = tile * 8 + (r & 7);
-    return f < half_rows ? f + (r >= 8 ? half_rows : 0) : -1;
-  };
+  const int groups = L.K / 32;
   const long long chunks = (long long)L.tiles * L.ku * 64, scales = (long long)L.tiles * L.ku * 64;
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < chunks + scales;
        i += (long long)gridDim.x * blockDim.x) {
@@ -279,7 +502,7 @@ __global__ void matvec_prepare_kernel(MatvecPrepareParams p) {
       const int lane = (int)(i & 31), half = (int)((i >> 5) & 1);
       const long long unit = i >> 6, tile = unit / L.ku;
       const int u = (int)(unit - tile * L.ku);
-      const long long row = row_of(tile, (lane >> 2) + 8 * half);
+      const long long row = matvec_raw_row(L, tile, (lane >> 2) + 8 * half);
       uint32_t w[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -287,17 +510,17 @@ __global__ void matvec_prepare_kernel(MatvecPrepareParams p) {
                    ? __ldg(reinterpret_cast<const uint32_t*>(p.codes + (size_t)row * (L.K / 2) + u * 64 + 16 * b) +
                            (lane & 3))
                    : 0u;
-      reinterpret_cast<uint4*>(p.dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(p.dst + matvec_unit_offset(L, tile, u))[i & 63] = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       const long long q = i - chunks, unit = q >> 6, tile = unit / L.ku;
       const int u = (int)(unit - tile * L.ku), g = (int)(q >> 3) & 7, half = (int)(q >> 2) & 1, b = (int)q & 3;
-      const long long row = row_of(tile, g + 8 * half);
-      uint8_t s = 127;
+      const long long row = matvec_raw_row(L, tile, g + 8 * half);
+      int s = 0;
       if (row >= 0 && 4 * u + b < groups) {
-        s = p.scales[(size_t)row * groups + 4 * u + b];
-        if (s == 255) atomicOr(reinterpret_cast<unsigned int*>(p.dst + L.flag_off), 1u);
+        s = 127 + (int)p.scales[(size_t)row * groups + 4 * u + b] - (int)p.dst[L.exp_off + tile * 16 + g + 8 * half];
+        if (s < 0) s = 0;
       }
-      p.dst[L.scales_off + q] = s;
+      p.dst[matvec_unit_offset(L, tile, u) + 1024 + (q & 63)] = (uint8_t)s;
     }
   }
 }
@@ -366,38 +589,74 @@ __global__ void __launch_bounds__(kThinThreads) thin16_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ launchers
-template <bool MX, typename X, int NT, int RT, bool GATED, int ACT>
-cudaError_t launch_t(const ThinParams& p, cudaStream_t stream) {
-  const int red = kThinWarps * NT * 8 * (RT * kThinRows + 4) * 4;
-  const dim3 grid(ceil_div(p.tiles, RT), ceil_div(p.T, kThinTokens));
-  static SmemOptIn opt_in;
-  if constexpr (MX) {
-    auto kern = matvec_kernel<X, NT, RT, GATED, ACT>;
-    const int tokens = p.T < NT * 8 ? p.T : NT * 8;
-    const cudaError_t e = opt_in.ensure(kern, MatvecCfg<X, NT, RT>::smem(NT * 8));
+template <typename X, int NT, bool PACKED, bool GATED, int ACT>
+cudaError_t launch_matvec_t(ThinParams p, cudaStream_t stream) {
+  using C = MatvecCfg<NT, PACKED>;
+  const int groups_t = ceil_div(p.T, NT * 8);
+  cudaError_t e;
+  if constexpr (PACKED) {
+    p.x_scale = reinterpret_cast<float*>(p.packed + packed_bytes<NT>(p.T, p.ku));
+    e = launch_pdl(matvec_pack_kernel<X, NT>, dim3(groups_t * NT * 8), dim3(256), 0, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid, dim3(kThinThreads), MatvecCfg<X, NT, RT>::smem(tokens), stream, p);
-  } else {
-    auto kern = thin16_kernel<X, NT, RT, GATED, ACT>;
-    const cudaError_t e = opt_in.ensure(kern, red);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid, dim3(kThinThreads), red, stream, p);
   }
+  // clusters along K while whole groups leave resident blocks idle and a block keeps two units
+  const int groups = p.tiles / kMatvecGroup, resident = C::kPerSm * device_sms();
+  p.kw = 1;
+  while (p.kw < 8 && 2 * groups * groups_t * p.kw <= resident && p.ku >= 4 * p.kw) p.kw *= 2;
+  const int blocks = p.kw > 1 || groups * groups_t < resident ? groups * p.kw : max(1, resident / groups_t);
+  const int smem = C::kRingBytes + (PACKED ? 0 : p.T * resident_row_halves(p.ku) * 2);
+  auto kern = matvec_kernel<X, NT, PACKED, GATED, ACT>;
+  static SmemOptIn opt_in;
+  e = opt_in.ensure(kern, C::kRingBytes + (PACKED ? 0 : kResidentPieces * 256 + 8 * 64));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, groups_t);
+  cfg.blockDim = dim3(kThinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)p.kw, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = p.kw > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Column groups of 8 tokens per block: up to four.
+template <typename X, bool GATED, int ACT>
+cudaError_t launch_matvec_nt(const ThinParams& p, cudaStream_t stream) {
+  if (matvec_resident(p.T, p.ku)) return launch_matvec_t<X, 1, false, GATED, ACT>(p, stream);
+  if (p.T <= 8) return launch_matvec_t<X, 1, true, GATED, ACT>(p, stream);
+  if (p.T <= 16) return launch_matvec_t<X, 2, true, GATED, ACT>(p, stream);
+  return launch_matvec_t<X, 4, true, GATED, ACT>(p, stream);
+}
+
+template <typename X, int NT, int RT, bool GATED, int ACT>
+cudaError_t launch_thin16_t(const ThinParams& p, cudaStream_t stream) {
+  auto kern = thin16_kernel<X, NT, RT, GATED, ACT>;
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in.ensure(kern, finish_bytes<NT, RT>());
+  if (e != cudaSuccess) return e;
+  const dim3 grid(ceil_div(p.tiles, RT), ceil_div(p.T, kThinTokens));
+  return launch_pdl(kern, grid, dim3(kThinThreads), finish_bytes<NT, RT>(), stream, p);
 }
 
 // Row tiles per block: as many (up to four) as leave two blocks for every SM -- more
 // tiles share each x fragment, fewer leave SMs without work.
-template <bool MX, typename X, int NT, bool GATED, int ACT>
-cudaError_t launch_rt(const ThinParams& p, cudaStream_t stream) {
+template <typename X, int NT, bool GATED, int ACT>
+cudaError_t launch_thin16_rt(const ThinParams& p, cudaStream_t stream) {
   const int want = 2 * kMaxCtas;
-  if (ceil_div(p.tiles, 4) >= want) return launch_t<MX, X, NT, 4, GATED, ACT>(p, stream);
-  if (ceil_div(p.tiles, 2) >= want) return launch_t<MX, X, NT, 2, GATED, ACT>(p, stream);
-  return launch_t<MX, X, NT, 1, GATED, ACT>(p, stream);
+  if (ceil_div(p.tiles, 4) >= want) return launch_thin16_t<X, NT, 4, GATED, ACT>(p, stream);
+  if (ceil_div(p.tiles, 2) >= want) return launch_thin16_t<X, NT, 2, GATED, ACT>(p, stream);
+  return launch_thin16_t<X, NT, 1, GATED, ACT>(p, stream);
 }
 
 template <bool MX, typename X, bool GATED, int ACT>
 cudaError_t launch_nt(const ThinParams& p, cudaStream_t stream) {
-  return p.T <= 8 ? launch_rt<MX, X, 1, GATED, ACT>(p, stream) : launch_rt<MX, X, 2, GATED, ACT>(p, stream);
+  if constexpr (MX) return launch_matvec_nt<X, GATED, ACT>(p, stream);
+  return p.T <= 8 ? launch_thin16_rt<X, 1, GATED, ACT>(p, stream) : launch_thin16_rt<X, 2, GATED, ACT>(p, stream);
 }
 
 template <bool MX, typename X>
@@ -418,7 +677,21 @@ cudaError_t launch_thin16(const ThinParams& p, int dtype, bool gated, cudaStream
                              : launch_act<false, __half>(p, gated, stream);
 }
 
+size_t matvec_workspace_bytes(int T, int K) {
+  const int ku = ceil_div(K, 128);
+  if (matvec_resident(T, ku)) return 0;
+  const size_t x = T <= 8 ? packed_bytes<1>(T, ku) : T <= 16 ? packed_bytes<2>(T, ku) : packed_bytes<4>(T, ku);
+  return x + kMatvecMaxTokens * sizeof(float);
+}
+
+uint32_t* thin_status_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_thin_status) == cudaSuccess ? static_cast<uint32_t*>(p) : nullptr;
+}
+
 cudaError_t launch_matvec_prepare(const MatvecPrepareParams& p, cudaStream_t stream) {
+  const long long rows = (long long)p.L.tiles * 16;
+  matvec_row_exp_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(p);
   matvec_prepare_kernel<<<1184, 256, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -17,6 +17,7 @@ the current stream of its tensors' device, takes its workspace from torch's allo
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -24,6 +25,20 @@ import torch
 from . import _lib as L
 
 _DTYPES = {torch.bfloat16: L.MOE_DTYPE_BF16, torch.float16: L.MOE_DTYPE_F16, torch.float32: L.MOE_DTYPE_F32}
+
+
+class _Library:
+    """The library's functions, looked up once each."""
+
+    def __getattr__(self, name):
+        fn = getattr(L.load(), name)
+        setattr(self, name, fn)
+        return fn
+
+
+_C = _Library()
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _dtype16(t: torch.Tensor) -> int:
@@ -37,24 +52,39 @@ def _need(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> Optiona
     """The address of a contiguous tensor of this shape, type and device (None for None)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _call(device: torch.device, name: str, *args) -> None:
+def _call(device: torch.device, fn, *args) -> None:
     """One library call on the current stream of `device`, with it current."""
     if device.type != "cuda":
         raise ValueError("CUDA tensors are needed")
-    fn = getattr(L.load(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == _current_device():
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    if st != L.MOE_OK:
-        raise L.MoEError(name, st)
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        raise L.MoEError(fn.__name__, st)
+
+
+@functools.lru_cache(maxsize=None)
+def _ffn_bytes(T: int, H: int, I: int, backward: int) -> int:
+    return _C.moe_ffn_workspace_bytes(T, H, I, backward)
+
+
+@functools.lru_cache(maxsize=None)
+def _matvec_bytes(T: int, K: int) -> int:
+    return _C.moe_matvec_workspace_bytes(T, K)
+
+
+@functools.lru_cache(maxsize=None)
+def _norm_bytes(T: int, H: int) -> int:
+    return _C.moe_block_norm_workspace_bytes(T, H)
 
 
 # ------------------------------------------------------------------ norms around a block
@@ -87,13 +117,13 @@ def block_norm(block: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
         raise ValueError(f"the residual stream is {dt} or float32, got {sdt}")
     kind, gate_ptr = _gate(gate, T, H, dt, dev)
     if residual_out is None:
-        residual_out = torch.empty(block.shape, dtype=sdt, device=dev)
+        residual_out = torch.empty_like(block, dtype=sdt)
     if next_weight is None:
         if out is not None:
             raise ValueError("out needs next_weight")
     elif out is None:
-        out = torch.empty(block.shape, dtype=dt, device=dev)
-    _call(dev, "moe_block_norm", _need("block", block, (T, H), dt, dev),
+        out = torch.empty_like(block)
+    _call(dev, _C.moe_block_norm, _need("block", block, (T, H), dt, dev),
           _need("norm_weight", norm_weight, (H,), dt, dev), gate_ptr, kind, _need("residual", residual, (T, H), sdt, dev),
           residual_scale, _need("next_weight", next_weight, (H,), dt, dev), eps, T, H, code, _DTYPES[sdt],
           _need("residual_out", residual_out, (T, H), sdt, dev), _need("out", out, (T, H), dt, dev))
@@ -125,7 +155,7 @@ def block_norm_backward(d_residual_out: Optional[torch.Tensor], d_out: Optional[
     if sdt != dt and sdt != torch.float32:
         raise ValueError(f"the residual stream is {dt} or float32, got {sdt}")
     kind, gate_ptr = _gate(gate, T, H, dt, dev)
-    nbytes = L.load().moe_block_norm_workspace_bytes(T, H)
+    nbytes = _norm_bytes(T, H)
     if nbytes == 0:
         raise L.MoEError("moe_block_norm_backward", L.MOE_ERR_UNSUPPORTED_SHAPE)
     d_block = torch.empty_like(block)
@@ -138,7 +168,7 @@ def block_norm_backward(d_residual_out: Optional[torch.Tensor], d_out: Optional[
     else:
         d_gate = torch.empty_like(gate) if kind == L.MOE_GATE_FULL else torch.empty(gate.shape, **f32)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _call(dev, "moe_block_norm_backward", _need("d_residual_out", d_residual_out, (T, H), sdt, dev),
+    _call(dev, _C.moe_block_norm_backward, _need("d_residual_out", d_residual_out, (T, H), sdt, dev),
           _need("d_out", d_out, (T, H), dt, dev), _need("block", block, (T, H), dt, dev),
           _need("norm_weight", norm_weight, (H,), dt, dev), gate_ptr, kind,
           _need("residual_out", residual_out, (T, H), sdt, dev), residual_scale,
@@ -163,14 +193,14 @@ def ffn_forward(x: torch.Tensor, w_gateup: torch.Tensor, w_down: torch.Tensor, *
     ffn_backward."""
     T, H, I = _ffn_shape(x, w_gateup)
     code, dt, dev = _dtype16(x), x.dtype, x.device
-    nbytes = L.load().moe_ffn_workspace_bytes(T, H, I, 0)
+    nbytes = _ffn_bytes(T, H, I, 0)
     if nbytes == 0:
         raise L.MoEError("moe_ffn_forward", L.MOE_ERR_UNSUPPORTED_SHAPE)
     if out is None:
         out = torch.empty(T, H, dtype=dt, device=dev)
     gateup = torch.empty(T, 2 * I, dtype=torch.float32, device=dev) if save else None
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _call(dev, "moe_ffn_forward", _need("x", x, (T, H), dt, dev), _need("w_gateup", w_gateup, (2 * I, H), dt, dev),
+    _call(dev, _C.moe_ffn_forward, _need("x", x, (T, H), dt, dev), _need("w_gateup", w_gateup, (2 * I, H), dt, dev),
           _need("w_down", w_down, (H, I), dt, dev), T, H, I, act, code, None if gateup is None else gateup.data_ptr(),
           _need("out", out, (T, H), dt, dev), ws.data_ptr(), nbytes)
     return (out, gateup) if save else out
@@ -190,27 +220,27 @@ def ffn_backward(d_out: torch.Tensor, x: torch.Tensor, gateup: torch.Tensor, w_g
     saved and ``act`` as given there; all of x's type."""
     T, H, I = _ffn_shape(x, w_gateup)
     code, dt, dev = _dtype16(x), x.dtype, x.device
-    nbytes = L.load().moe_ffn_workspace_bytes(T, H, I, 1)
+    nbytes = _ffn_bytes(T, H, I, 1)
     if nbytes == 0:
         raise L.MoEError("moe_ffn_backward", L.MOE_ERR_UNSUPPORTED_SHAPE)
     d_x = torch.empty(T, H, dtype=dt, device=dev) if need_x else None
     d_wgu = torch.empty(2 * I, H, dtype=dt, device=dev) if need_weights else None
     d_wd = torch.empty(H, I, dtype=dt, device=dev) if need_weights else None
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _call(dev, "moe_ffn_backward", _need("d_out", d_out, (T, H), dt, dev), _need("x", x, (T, H), dt, dev),
+    _call(dev, _C.moe_ffn_backward, _need("d_out", d_out, (T, H), dt, dev), _need("x", x, (T, H), dt, dev),
           _need("gateup", gateup, (T, 2 * I), torch.float32, dev), _need("w_gateup", w_gateup, (2 * I, H), dt, dev),
           _need("w_down", w_down, (H, I), dt, dev), T, H, I, act, code, None if d_x is None else d_x.data_ptr(),
           None if d_wgu is None else d_wgu.data_ptr(), None if d_wd is None else d_wd.data_ptr(), ws.data_ptr(), nbytes)
     return FfnGrads(d_x, d_wgu, d_wd)
 
 
-def ffn_status() -> int:
+def dense_status() -> int:
     """The feed-forward GEMMs' device status word on the current device (0 = healthy), read
-    after the current stream and cleared (moe_ffn_status)."""
+    after the current stream and cleared (moe_dense_status)."""
     st = ctypes.c_int(0)
-    rc = L.load().moe_ffn_status(ctypes.byref(st), torch.cuda.current_stream().cuda_stream)
+    rc = _C.moe_dense_status(ctypes.byref(st), torch.cuda.current_stream().cuda_stream)
     if rc not in (L.MOE_OK, L.MOE_ERR_DEVICE_TIMEOUT):
-        raise L.MoEError("moe_ffn_status", rc)
+        raise L.MoEError("moe_dense_status", rc)
     return st.value
 
 
@@ -227,13 +257,13 @@ class MatvecMXFP4:
         rows, half = codes.shape
         self.rows, self.K, self.kind, self.act, self.bias = rows, 2 * half, kind, act, bias
         dev = codes.device
-        nbytes = L.load().moe_prepared_matvec_bytes(rows, self.K, kind)
+        nbytes = _C.moe_prepared_matvec_bytes(rows, self.K, kind)
         if nbytes == 0:
             raise L.MoEError("moe_prepare_matvec", L.MOE_ERR_UNSUPPORTED_SHAPE)
         _need("bias", bias, (rows,), torch.float32, dev)
         self.n_out = rows // 2 if kind == L.MOE_WEIGHTS_GATEUP else rows
         self.weight = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _call(dev, "moe_prepare_matvec", _need("codes", codes, (rows, half), torch.uint8, dev),
+        _call(dev, _C.moe_prepare_matvec, _need("codes", codes, (rows, half), torch.uint8, dev),
               _need("scales", scales, (rows, self.K // 32), torch.uint8, dev), rows, self.K, kind,
               self.weight.data_ptr(), nbytes)
 
@@ -244,9 +274,11 @@ class MatvecMXFP4:
         if out is None:
             out = torch.empty(T, self.n_out, dtype=x.dtype, device=dev)
         bias = self.bias
-        _call(dev, "moe_matvec_mxfp4", _need("x", x, (T, self.K), x.dtype, dev), self.weight.data_ptr(),
+        nbytes = _matvec_bytes(T, self.K)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _call(dev, _C.moe_matvec_mxfp4, _need("x", x, (T, self.K), x.dtype, dev), self.weight.data_ptr(),
               None if bias is None else bias.data_ptr(), T, self.rows, self.K, self.kind, self.act, code,
-              _need("out", out, (T, self.n_out), x.dtype, dev))
+              _need("out", out, (T, self.n_out), x.dtype, dev), None if ws is None else ws.data_ptr(), nbytes)
         return out
 
     __call__ = forward

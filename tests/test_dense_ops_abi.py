@@ -48,20 +48,28 @@ def test_block_norm_backward_refusals(L):
 
 def test_matvec_sizes_and_refusals(L):
     DOWN, GU = L.MOE_WEIGHTS_DOWN, L.MOE_WEIGHTS_GATEUP
-    # 1024 bytes of codes and 64 of scales per 16 rows x 128 codes, a 256-byte trailer
-    assert L.moe_prepared_matvec_bytes(2880, 2880, DOWN) == (180 * 23 * 1088 + 255) // 256 * 256 + 256
-    assert L.moe_prepared_matvec_bytes(18, 128, GU) == (2 * 1088 + 255) // 256 * 256 + 256  # nine features: two tiles
+    # 1024 bytes of codes and 64 of scales per 16 rows x 128 codes, 16 per tile, tiles in eights, a 256-byte trailer
+    assert L.moe_prepared_matvec_bytes(2880, 2880, DOWN) == (184 * (23 * 1088 + 16) + 255) // 256 * 256 + 256
+    assert L.moe_prepared_matvec_bytes(130, 128, GU) == (16 * (1088 + 16) + 255) // 256 * 256 + 256  # 65 features: nine tiles
+    assert L.moe_matvec_workspace_bytes(1, 2880) == 0                        # staged by the kernel itself
+    assert L.moe_matvec_workspace_bytes(16, 4096) == 32 * 2 * 2048 + 256     # f16 values, 64 scales
+    assert L.moe_matvec_workspace_bytes(33, 4000) == 2 * 32 * 4 * 2048 + 256  # two groups of 32 tokens
+    assert L.moe_matvec_workspace_bytes(65, 4096) == 0 and L.moe_matvec_workspace_bytes(4, 4100) == 0
     for rows, K, kind in ((0, 64, DOWN), (8, 48, DOWN), (8, 0, DOWN), (7, 64, GU), (8, 64, 2), (8, 65536 + 32, DOWN),
                           ((1 << 22) + 1, 64, DOWN)):
         assert L.moe_prepared_matvec_bytes(rows, K, kind) == 0
         assert L.moe_prepare_matvec(FAKE, FAKE, rows, K, kind, FAKE, 1 << 40, None) == L.MOE_ERR_UNSUPPORTED_SHAPE
-        assert L.moe_matvec_mxfp4(FAKE, FAKE, None, 1, rows, K, kind, 0, 0, FAKE, None) == L.MOE_ERR_UNSUPPORTED_SHAPE
+        assert L.moe_matvec_mxfp4(FAKE, FAKE, None, 1, rows, K, kind, 0, 0, FAKE, None, 0, None) == L.MOE_ERR_UNSUPPORTED_SHAPE
     assert L.moe_prepare_matvec(FAKE, FAKE, 32, 64, DOWN, FAKE, 16, None) == L.MOE_ERR_WORKSPACE_TOO_SMALL
     for a in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (FAKE + 8, FAKE, FAKE), (FAKE, FAKE, FAKE + 16)):
         assert L.moe_prepare_matvec(a[0], a[1], 32, 64, DOWN, a[2], 1 << 20, None) == L.MOE_ERR_INVALID_ARG
 
-    def f(x=FAKE, w=FAKE, b=None, T=1, act=0, dt=0, out=FAKE):
-        return L.moe_matvec_mxfp4(x, w, b, T, 32, 64, DOWN, act, dt, out, None)
+    def f(x=FAKE, w=FAKE, b=None, T=1, act=0, dt=0, out=FAKE, K=64, ws=None, n=0):
+        return L.moe_matvec_mxfp4(x, w, b, T, 32, K, DOWN, act, dt, out, ws, n, None)
+    need = L.moe_matvec_workspace_bytes(16, 4096)
+    assert f(T=16, K=4096, ws=FAKE, n=need - 1) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert f(T=16, K=4096, ws=None, n=need) == L.MOE_ERR_INVALID_ARG
+    assert f(T=16, K=4096, ws=FAKE + 16, n=need) == L.MOE_ERR_INVALID_ARG
     assert f(T=0) == L.MOE_ERR_UNSUPPORTED_SHAPE and f(T=65) == L.MOE_ERR_UNSUPPORTED_SHAPE
     for kw in (dict(x=None), dict(w=None), dict(out=None), dict(x=FAKE + 8), dict(w=FAKE + 16), dict(out=FAKE + 8),
                dict(b=FAKE + 2), dict(act=2), dict(dt=2)):

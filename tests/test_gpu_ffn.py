@@ -72,7 +72,7 @@ def check(m, act="silu", backward=True):
             tol = step(K) * (A.abs() @ B.abs())
             tol = tol + (eA @ B.abs() if eA is not None else A.abs() @ eB)
             within(got, want, tol + hs * (want.abs() + tol) + fl)
-    assert pkg.ffn_status() == 0
+    assert pkg.dense_status() == 0
     return out, gu
 
 
@@ -198,7 +198,7 @@ def test_captured_twice_and_on_side_streams():
         for _, got in graphs:
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
-    assert pkg.ffn_status() == 0
+    assert pkg.dense_status() == 0
 
 
 def test_waits_that_give_up_are_reported():
@@ -208,14 +208,14 @@ def test_waits_that_give_up_are_reported():
     from mxfp4_expert_layer_gb300 import _lib as L
     m = make(600, 512, 1024, torch.bfloat16, seed=9)
     want = pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
-    assert pkg.ffn_status() == 0
+    assert pkg.dense_status() == 0
     assert L.moe_set_wait_limit_ns(1) == L.MOE_OK
     try:
         pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
         torch.cuda.synchronize()
     finally:
         assert L.moe_set_wait_limit_ns(0) == L.MOE_OK
-    st = pkg.ffn_status()
+    st = pkg.dense_status()
     assert st != 0 and st & ~0b111 == 0
-    assert pkg.ffn_status() == 0
+    assert pkg.dense_status() == 0
     assert torch.equal(pkg.ffn_forward(m["x"], m["wgu"], m["wd"]), want)

@@ -1,11 +1,12 @@
 """GPU parity of the few-token products with MXFP4 weights (moe_matvec_mxfp4) against the
 64-bit product with the dequantised weights.
 
-Bound.  The weights are exact; f16 x is exact, bf16 x is exact down to 2^-28 of its K
-chunk's largest value and off by at most 2^-39 of that below.  The sums are f32: tensor
-core steps of 16 products (counted as 2^-22 of the terms' magnitude each: products of
-different sizes are aligned before they are added), a group's scaling, a warp's chain of
-groups (at most K / 256 + 1 of them) and eight warps' sums.  One rounding at the end."""
+Bound.  The weights are exact (group scales down to 2^-126 of their row's largest); f16 x
+is exact, bf16 x is exact down to 2^-28 of its token's largest value and off by at most
+2^-39 of that below.  The sums are f32: tensor core steps of 16 products (counted as
+2^-22 of the terms' magnitude each: products of different sizes are aligned before they
+are added), a group's scaling, a warp's chain of groups and the warps' sums: a step and
+K / 32 + 8 roundings of 2^-24, less than 8 + K / 128 of 2^-22.  One rounding at the end."""
 
 import pytest
 import torch
@@ -35,7 +36,7 @@ def expect(m, gated, act="silu"):
     x, w = m["x"].double(), ref.dequantise(m["codes"], m["scales"])
     K, dt = x.shape[1], m["x"].dtype
     y, mag = x @ w.t(), x.abs() @ w.t().abs()
-    err = 4 * U32 * (8 + K / 256) * mag
+    err = 4 * U32 * (8 + K / 128) * mag
     if dt == torch.bfloat16:
         err = err + 2.0 ** -39 * x.abs().amax(1, keepdim=True) * w.abs().sum(1)
     if m["bias"] is not None:
@@ -92,6 +93,14 @@ def test_every_code_and_the_ends_of_the_scale():
     for dtype, std in ((torch.bfloat16, 1.0), (torch.bfloat16, 2.0 ** 20)):
         x = (torch.randn(3, K, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) * std).to(dtype)
         check(dict(x=x, codes=codes.contiguous(), scales=scales.contiguous(), bias=None), False)
+
+
+def test_group_scales_far_below_their_row():
+    """Scales from 2^-127 to 2^30 in one row: groups below 2^-126 of the largest drop out."""
+    m = make(3, 48, 1024, torch.bfloat16, seed=2, lo=0, hi=158, bias=False)
+    check(m, False)
+    m = make(20, 48, 2048, torch.float16, seed=2, lo=1, hi=140, bias=False)
+    check(m, True)
 
 
 def test_wide_ranges_of_x():
