@@ -413,10 +413,10 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* moe_dense_status: the device status of the dense operators' pipelines (feed-forward
- * GEMMs, MXFP4 products) on the current device, as moe_get_device_status (bits and
+ * GEMMs, MXFP4 products, norms' row copies) on the current device, as moe_get_device_status (bits and
  * returns) for words that the library holds per GPU: synchronises `stream`, reads them
  * into *status and clears them when set.  A bounded wait that gave up sets a bit (the
- * GEMMs' limit is moe_set_wait_limit_ns, the products' 1 s); results of calls since the
+ * GEMMs' limit is moe_set_wait_limit_ns, the others' 1 s); results of calls since the
  * last reading are then not reliable.  Not for the hot path.                        */
 int moe_dense_status(int* status, moe_stream_t stream);
 

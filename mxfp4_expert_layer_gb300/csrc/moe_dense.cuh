@@ -68,6 +68,7 @@ struct Vec8 {
   __device__ __forceinline__ void load_weight(const void* base, size_t vec) {
     raw = reinterpret_cast<const uint4*>(base)[vec];
   }
+  __device__ __forceinline__ void load_shared(const void* base, int vec) { raw = reinterpret_cast<const uint4*>(base)[vec]; }
   __device__ __forceinline__ void zero() { raw = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -89,6 +90,10 @@ struct Vec8<float> {
   __device__ __forceinline__ void load(const void* base, size_t vec) {
     a = __ldcg(reinterpret_cast<const float4*>(base) + 2 * vec);
     b = __ldcg(reinterpret_cast<const float4*>(base) + 2 * vec + 1);
+  }
+  __device__ __forceinline__ void load_shared(const void* base, int vec) {
+    a = reinterpret_cast<const float4*>(base)[2 * vec];
+    b = reinterpret_cast<const float4*>(base)[2 * vec + 1];
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -134,7 +139,8 @@ __device__ __forceinline__ float act_f(float g, float& slope) {
 
 // ------------------------------------------------------------------ norms around a block
 constexpr int kGateNone = 0, kGateFeature = 1, kGateToken = 2, kGateFull = 3;
-constexpr int kNormMaxPartials = 320;  // rows of partial weight gradients of the backward
+constexpr int kNormBlocks = 152;    // blocks of the backward, each a row of partial weight gradients
+constexpr int kNormMaxGroups = 15;  // rows that one of them takes side by side (a named barrier each)
 
 struct BlockNormParams {
   const void* block;        // z [T, H]
@@ -160,7 +166,9 @@ struct BlockNormBackwardParams {
   int blocks;                 // persistent blocks = rows of partials
 };
 cudaError_t launch_block_norm(const BlockNormParams& p, int dtype, int stream_dtype, cudaStream_t stream);
+int block_norm_backward_groups(int H);
 int block_norm_backward_blocks(int T, int H);
+uint32_t* norm_status_word();
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int dtype, int stream_dtype,
                                        cudaStream_t stream);
 

@@ -188,7 +188,7 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
 
 int moe_dense_status(int* status, moe_stream_t stream) {
   if (!status) return MOE_ERR_INVALID_ARG;
-  uint32_t* words[] = {dense_status_word(), thin_status_word()};
+  uint32_t* words[] = {dense_status_word(), thin_status_word(), norm_status_word()};
   int all = 0;
   for (uint32_t* word : words) {
     if (!word) return MOE_ERR_CUDA;

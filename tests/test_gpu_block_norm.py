@@ -6,7 +6,8 @@ whose own error is a small multiple of 2^-24 of the terms it is formed from: eac
 and sum rounds once, a row's sum over at most 1024 threads of 8 values is a chain of 8 and
 two butterflies of 5, and rsqrt is good to 2 units.  64 roundings cover the longest chain
 (two norms in the backward); the weight gradients add one rounding per row that a block
-takes in turn and per partial sum (T / 320 + 48)."""
+takes in turn (at most T / 152 + 1 rows, fewer where a block takes several side by side),
+per row side by side (15) and per block (152, in eight chains: 19 + 8)."""
 
 import pytest
 import torch
@@ -64,7 +65,7 @@ def check_backward(m, a, s, grads):
         if name not in want:
             assert t is None, name
             continue
-        chain = 64 + (T / 320 + 48 if name.endswith("weight") or (name == "gate" and m["g"].dim() == 1) else 0)
+        chain = 64 + (T / 152 + 43 if name.endswith("weight") or (name == "gate" and m["g"].dim() == 1) else 0)
         within(t, want[name], half_step(t.dtype) * want[name].abs() + chain * U32 * mag[name] + floor_of(t.dtype))
 
 
