@@ -8,7 +8,7 @@
 // is transposed in memory.
 //
 // One persistent block per SM.  Warp 0 issues the TMA loads into a ring of stages of 64
-// K values, warp 1 the MMAs into one of two accumulators in tensor memory, warps 2-5 run
+// K values, warp 1 the MMAs into one of two accumulators in tensor memory, warps 2-9 run
 // the epilogue of one tile while the next one's MMAs proceed.  Large products run on
 // pairs of SMs (cta_group::2): the pair computes a 256 x BN tile, each SM loading its
 // own 128 rows of A and half of B, so the bytes an SM must bring in per MMA are halved
@@ -25,7 +25,8 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kDenseThreads = 192;
+constexpr int kEpiWarps = 8;                    // two per tensor-memory lane quarter
+constexpr int kDenseThreads = 64 + 32 * kEpiWarps;
 constexpr uint64_t kDrainLimit = 1000000000ull;  // ns for MMAs already issued (1 s)
 constexpr uint64_t kLandingNs = 20000000ull;     // ns after a time-out in which every issued copy has landed (20 ms)
 
@@ -111,6 +112,57 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float (&f)[32
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+// A whole 32-byte sector per thread: with 16-byte accesses of a thread per row, every
+// sector would be asked for twice.
+struct Sector {
+  uint32_t w[8];
+};
+__device__ __forceinline__ void store_sector(void* p, const Sector& s) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]),
+               "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load_sector(float (&f)[8], const float* p) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+               : "l"(p));
+}
+// 16 (or, at the end of a row, 8) values of a row, rounded to 16 bits.
+template <typename X>
+__device__ __forceinline__ void store16(X* p, const float* v, int n) {
+  Sector s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s.w[i] = pack2<X>(v[2 * i], v[2 * i + 1]);
+  if (n >= 16 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    store_sector(p, s);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]);
+    if (n >= 16) reinterpret_cast<uint4*>(p)[1] = make_uint4(s.w[4], s.w[5], s.w[6], s.w[7]);
+  }
+}
+// 8 values in 32 bits (f32 rows of a multiple of 8 values: sectors are aligned where the
+// array is).
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    Sector s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s.w[i] = __float_as_uint(v[i]);
+    store_sector(p, s);
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+__device__ __forceinline__ void load8(float (&f)[8], const float* p) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    load_sector(f, p);
+  } else {
+    Vec8<float> t;
+    t.load(p, 0);
+    t.get(f);
+  }
+}
+
 // ------------------------------------------------------------------ configuration
 template <int BN, bool PAIR>
 struct DenseCfg {
@@ -139,6 +191,75 @@ __device__ __forceinline__ void map_tile(int u, int tm, int tn, int& m, int& n, 
   m = first + within - n * rows;
 }
 
+// What happens to the sums of 32 columns of a row (`left` of them inside the matrix, in
+// eights): v, and for gate/up w the up sums.
+template <typename X, int MODE>
+__device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n, int left, int split, float (&v)[32],
+                                         float (&w)[32]) {
+  X* out = reinterpret_cast<X*>(p.out);
+  if constexpr (MODE == kDenseStore) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 16)
+      if (j < left) store16(out + (size_t)m * p.N + n + j, v + j, left - j);
+  } else if constexpr (MODE == kDensePartial) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+      if (j < left) store8(p.partial + ((size_t)split * p.M + m) * p.N + n + j, v + j);
+  } else if constexpr (MODE == kDenseGateUp) {
+    if (p.gateup) {
+      float* gu = p.gateup + (size_t)m * 2 * p.N + n;
+#pragma unroll
+      for (int j = 0; j < 32; j += 8)
+        if (j < left) {
+          store8(gu + j, v + j);
+          store8(gu + p.N + j, w + j);
+        }
+    }
+    if (p.act == kActSilu) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = act_f<kActSilu>(v[j]) * w[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = act_f<kActGelu>(v[j]) * w[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 16)
+      if (j < left) store16(out + (size_t)m * p.N + n + j, v + j, left - j);
+  } else {
+    X* dg = out + (size_t)m * 2 * p.N + n;
+    X* hh = reinterpret_cast<X*>(p.out_h) + (size_t)m * p.N + n;
+    const float* gu = p.gateup + (size_t)m * 2 * p.N + n;
+    float g[4][8], u[4][8];
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+      if (j < left) {
+        load8(g[j / 8], gu + j);
+        load8(u[j / 8], gu + p.N + j);
+      }
+    auto grad = [&](auto tag) {  // g, u, dh -> dg, du, h in place
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float slope;
+        const float gj = g[j / 8][j % 8], uj = u[j / 8][j % 8], a = act_f<decltype(tag)::value>(gj, slope);
+        g[j / 8][j % 8] = v[j] * uj * slope;
+        u[j / 8][j % 8] = v[j] * a;
+        v[j] = a * uj;
+      }
+    };
+    if (p.act == kActSilu)
+      grad(std::integral_constant<int, kActSilu>{});
+    else
+      grad(std::integral_constant<int, kActGelu>{});
+#pragma unroll
+    for (int j = 0; j < 32; j += 16)
+      if (j < left) {
+        store16(dg + j, &g[j / 8][0], left - j);
+        store16(dg + p.N + j, &u[j / 8][0], left - j);
+        store16(hh + j, v + j, left - j);
+      }
+  }
+}
+
 template <typename X, int MODE, int BN, bool PAIR>
 __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __grid_constant__ DenseGemmParams p) {
   using C = DenseCfg<BN, PAIR>;
@@ -155,7 +276,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf_bar[b], 1);
-      mbar_init(&acce_bar[b], 4 * C::kCtas);  // one lane of each epilogue warp
+      mbar_init(&acce_bar[b], kEpiWarps * C::kCtas);  // one lane of each epilogue warp
     }
     mbar_init(&drain_bar, 1);
     fence_mbar_init();
@@ -274,7 +395,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // tensor-memory lane quarter of this warp
+    const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lane quarter; which 32-column chunks
     int i = 0;
     for (int u = first; u < units; u += step, ++i) {
       int mt, nt, split;
@@ -289,101 +410,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * BN;
       const int m = mt * C::kTileM + (int)rank * 128 + q * 32 + lane;
       const bool live = m < p.M;
-      X* out = reinterpret_cast<X*>(p.out);
-      if constexpr (MODE == kDenseStore || MODE == kDensePartial) {
+      constexpr int kCols = MODE == kDenseGateUp ? BN / 2 : BN;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          float v[32];
-          tmem_ld_32x32b_x32(acc + c, v);
-          tmem_wait_ld();
-          const int n = nt * BN + c;
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (!live || n + j >= p.N) continue;
-            if constexpr (MODE == kDenseStore) {
-              *reinterpret_cast<uint4*>(out + (size_t)m * p.N + n + j) =
-                  make_uint4(pack2<X>(v[j], v[j + 1]), pack2<X>(v[j + 2], v[j + 3]), pack2<X>(v[j + 4], v[j + 5]),
-                             pack2<X>(v[j + 6], v[j + 7]));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(p.partial + ((size_t)split * p.M + m) * p.N + n + j);
-              dst[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-              dst[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
-            }
-          }
-        }
-      } else if constexpr (MODE == kDenseGateUp) {
-#pragma unroll 1
-        for (int c = 0; c < BN / 2; c += 32) {
-          float gv[32], uv[32];
-          tmem_ld_32x32b_x32(acc + c, gv);
-          tmem_ld_32x32b_x32(acc + BN / 2 + c, uv);
-          tmem_wait_ld();
-          const int n = nt * (BN / 2) + c;
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (!live || n + j >= p.N) continue;
-            if (p.gateup) {
-              float4* dg = reinterpret_cast<float4*>(p.gateup + (size_t)m * 2 * p.N + n + j);
-              float4* du = reinterpret_cast<float4*>(p.gateup + (size_t)m * 2 * p.N + p.N + n + j);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                dg[k] = make_float4(gv[j + 4 * k], gv[j + 4 * k + 1], gv[j + 4 * k + 2], gv[j + 4 * k + 3]);
-                du[k] = make_float4(uv[j + 4 * k], uv[j + 4 * k + 1], uv[j + 4 * k + 2], uv[j + 4 * k + 3]);
-              }
-            }
-            float h[8];
-            if (p.act == kActSilu) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) h[k] = act_f<kActSilu>(gv[j + k]) * uv[j + k];
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) h[k] = act_f<kActGelu>(gv[j + k]) * uv[j + k];
-            }
-            *reinterpret_cast<uint4*>(out + (size_t)m * p.N + n + j) =
-                make_uint4(pack2<X>(h[0], h[1]), pack2<X>(h[2], h[3]), pack2<X>(h[4], h[5]), pack2<X>(h[6], h[7]));
-          }
-        }
-      } else {
-        X* out_h = reinterpret_cast<X*>(p.out_h);
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          float dh[32];
-          tmem_ld_32x32b_x32(acc + c, dh);
-          tmem_wait_ld();
-          const int n = nt * BN + c;
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (!live || n + j >= p.N) continue;
-            Vec8<float> t;
-            float gv[8], uv[8], dg[8], du[8], h[8];
-            const size_t row = (size_t)m * 2 * p.N;
-            t.load(p.gateup + row + n + j, 0);
-            t.get(gv);
-            t.load(p.gateup + row + p.N + n + j, 0);
-            t.get(uv);
-            auto grad = [&](auto tag) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float slope;
-                const float a = act_f<decltype(tag)::value>(gv[k], slope);
-                h[k] = a * uv[k];
-                dg[k] = dh[j + k] * uv[k] * slope;
-                du[k] = dh[j + k] * a;
-              }
-            };
-            if (p.act == kActSilu)
-              grad(std::integral_constant<int, kActSilu>{});
-            else
-              grad(std::integral_constant<int, kActGelu>{});
-            Vec8<X> o;
-            o.set(dg);
-            o.store(out + row + n + j, 0);
-            o.set(du);
-            o.store(out + row + p.N + n + j, 0);
-            o.set(h);
-            o.store(out_h + (size_t)m * p.N + n + j, 0);
-          }
-        }
+      for (int c = 32 * half; c < kCols; c += 64) {
+        float v[32], w[32];
+        tmem_ld_32x32b_x32(acc + c, v);
+        if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + BN / 2 + c, w);
+        tmem_wait_ld();
+        const int n = nt * kCols + c, left = p.N - n;  // a multiple of 8
+        if (!live) continue;
+        epilogue<X, MODE>(p, m, n, left, split, v, w);
       }
       tc_fence_before();
       __syncwarp();
