@@ -236,22 +236,23 @@ uint32_t* dense_status_word();
 
 // ------------------------------------------------------------------ dense GEMMs
 // C[m, n] = sum_k A[m, k] B[n, k] of 16-bit operands, each stored with K or with M / N
-// contiguous, and one of four epilogues.
-constexpr int kDenseStore = 0;    // C in the operands' type
-constexpr int kDensePartial = 1;  // f32 partial sums of one K slice
-constexpr int kDenseGateUp = 2;   // B rows: gate, then up; h = act(g) u, and g, u in f32 when asked for
-constexpr int kDenseGateUpGrad = 3;  // C = dh: dg, du from the saved g, u; and h again
+// contiguous, and one of three epilogues.
+constexpr int kDenseStore = 0;       // C in the operands' type
+constexpr int kDenseGateUp = 1;      // B rows: gate, then up; h = act(g) u, and g, u in f32 when asked for
+constexpr int kDenseGateUpGrad = 2;  // C = dh: dg, du from the saved g, u; and h again
+constexpr int kDenseMaxSplits = 16;
 
 struct DenseGemmParams {
   CUtensorMap tm_a, tm_b;
   int M, N, K;              // N: output columns (gate/up: features, half of B's rows)
   int a_mn, b_mn;           // operand stored with M (N) contiguous
-  int tiles_m, tiles_n, splits, kgroups;  // K groups of 64 values, cut into `splits` slices
+  int tiles_m, tiles_n;
+  int full, splits, kgroups;  // tiles after the first `full` are cut into `splits` slices of K (groups of 64)
   int act;
   void* out;                // 16-bit [M, N]; gate/up grad: dgu [M, 2 N]
   void* out_h;              // gate/up grad: h [M, N]
   float* gateup;            // f32 [M, 2 N]: written by gate/up (or null), read by its gradient
-  float* partial;           // f32 [splits][M][N]
+  float* partial;           // f32 [slices][tile rows][tile columns]
   uint64_t wait_ns;
 };
 struct DenseOperand {

@@ -65,17 +65,19 @@ FfnLayout ffn_layout(int T, int H, int I, bool backward) {
   };
   L.h = take((size_t)T * I * 2);
   size_t part = 0;
-  auto need = [&](int M, int N, int K) {
-    const size_t b = dense_partial_bytes(M, N, K, kDenseStore);
+  auto need = [&](int M, int N, int K, int mode) {
+    const size_t b = dense_partial_bytes(M, N, K, mode);
     if (b > part) part = b;
   };
   if (backward) {
     L.dgu = take((size_t)T * I * 4);
-    need(T, H, 2 * I);
-    need(2 * I, H, T);
-    need(H, I, T);
-  } else {
-    need(T, H, I);
+    need(T, I, H, kDenseGateUpGrad);
+    need(T, H, 2 * I, kDenseStore);
+    need(2 * I, H, T, kDenseStore);
+    need(H, I, T, kDenseStore);
+  } else if (T > kThinTokens) {
+    need(T, I, H, kDenseGateUp);
+    need(T, H, I, kDenseStore);
   }
   L.partial = take(part);
   L.total = o;
@@ -139,6 +141,7 @@ int moe_ffn_forward(const void* x, const void* w_gateup, const void* w_down, int
   g.act = act;
   g.out = h;
   g.gateup = gateup_out;
+  g.partial = ws_ptr<float>(workspace, L.partial);
   st = launch_dense_gemm(g, {x, T, H, 0}, {w_gateup, 2 * I, H, 0}, kDenseGateUp, dtype, s);
   if (st != MOE_OK) return st;
   DenseGemmParams d{};
@@ -171,6 +174,7 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
   p.out = dgu;
   p.out_h = h;
   p.gateup = const_cast<float*>(gateup);
+  p.partial = partial;
   st = launch_dense_gemm(p, {d_out, T, H, 0}, {w_down, H, I, 1}, kDenseGateUpGrad, dtype, s);
   if (st != MOE_OK) return st;
   auto product = [&](int M, int N, int K, const DenseOperand& a, const DenseOperand& b, void* out) {

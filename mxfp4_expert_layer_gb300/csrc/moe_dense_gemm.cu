@@ -178,38 +178,49 @@ struct DenseCfg {
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
 
-// Tiles in groups of kRasterM row tiles, the row tile running fastest inside a group, so
-// the tiles in flight at one time share both operands through L2; K slices slowest.
+// Work units: the first `full` tiles whole, each tile after them in `splits` K slices (the
+// last round of tiles, when it would leave most SMs idle).  Tiles in groups of kRasterM
+// row tiles, the row tile running fastest inside a group, so the tiles in flight at one
+// time share both operands through L2.
 constexpr int kRasterM = 8;
-__device__ __forceinline__ void map_tile(int u, int tm, int tn, int& m, int& n, int& split) {
-  split = u / (tm * tn);
-  u -= split * tm * tn;
-  const int first = u / (kRasterM * tn) * kRasterM;
-  const int rows = min(kRasterM, tm - first);
-  const int within = u - first * tn;
-  n = within / rows;
-  m = first + within - n * rows;
+struct Unit {
+  int m, n, slot, k0, k1;  // slot: place of the slice's partial sums, or -1
+};
+__device__ __forceinline__ Unit map_unit(const DenseGemmParams& p, int u) {
+  Unit r;
+  r.slot = u - p.full;
+  r.k0 = 0;
+  r.k1 = p.kgroups;
+  if (r.slot < 0) {
+    r.slot = -1;
+  } else if (p.splits > 1) {
+    const int split = r.slot % p.splits;
+    u = p.full + r.slot / p.splits;
+    r.k0 = (int)((long long)split * p.kgroups / p.splits);
+    r.k1 = (int)((long long)(split + 1) * p.kgroups / p.splits);
+  }
+  const int first = u / (kRasterM * p.tiles_n) * kRasterM;
+  const int rows = min(kRasterM, p.tiles_m - first);
+  const int within = u - first * p.tiles_n;
+  r.n = within / rows;
+  r.m = first + within - r.n * rows;
+  return r;
 }
 
-// What happens to the sums of 32 columns of a row (`left` of them inside the matrix, in
+// What happens to the sums of W columns of a row (`left` of them inside the matrix, in
 // eights): v, and for gate/up w the up sums.
-template <typename X, int MODE>
-__device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n, int left, int split, float (&v)[32],
-                                         float (&w)[32]) {
+template <typename X, int MODE, int W>
+__device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n, int left, float (&v)[W], float (&w)[W]) {
   X* out = reinterpret_cast<X*>(p.out);
   if constexpr (MODE == kDenseStore) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 16)
+    for (int j = 0; j < W; j += 16)
       if (j < left) store16(out + (size_t)m * p.N + n + j, v + j, left - j);
-  } else if constexpr (MODE == kDensePartial) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 8)
-      if (j < left) store8(p.partial + ((size_t)split * p.M + m) * p.N + n + j, v + j);
   } else if constexpr (MODE == kDenseGateUp) {
     if (p.gateup) {
       float* gu = p.gateup + (size_t)m * 2 * p.N + n;
 #pragma unroll
-      for (int j = 0; j < 32; j += 8)
+      for (int j = 0; j < W; j += 8)
         if (j < left) {
           store8(gu + j, v + j);
           store8(gu + p.N + j, w + j);
@@ -217,28 +228,28 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n,
     }
     if (p.act == kActSilu) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_f<kActSilu>(v[j]) * w[j];
+      for (int j = 0; j < W; ++j) v[j] = act_f<kActSilu>(v[j]) * w[j];
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_f<kActGelu>(v[j]) * w[j];
+      for (int j = 0; j < W; ++j) v[j] = act_f<kActGelu>(v[j]) * w[j];
     }
 #pragma unroll
-    for (int j = 0; j < 32; j += 16)
+    for (int j = 0; j < W; j += 16)
       if (j < left) store16(out + (size_t)m * p.N + n + j, v + j, left - j);
   } else {
     X* dg = out + (size_t)m * 2 * p.N + n;
     X* hh = reinterpret_cast<X*>(p.out_h) + (size_t)m * p.N + n;
     const float* gu = p.gateup + (size_t)m * 2 * p.N + n;
-    float g[4][8], u[4][8];
+    float g[W / 8][8], u[W / 8][8];
 #pragma unroll
-    for (int j = 0; j < 32; j += 8)
+    for (int j = 0; j < W; j += 8)
       if (j < left) {
         load8(g[j / 8], gu + j);
         load8(u[j / 8], gu + p.N + j);
       }
     auto grad = [&](auto tag) {  // g, u, dh -> dg, du, h in place
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < W; ++j) {
         float slope;
         const float gj = g[j / 8][j % 8], uj = u[j / 8][j % 8], a = act_f<decltype(tag)::value>(gj, slope);
         g[j / 8][j % 8] = v[j] * uj * slope;
@@ -251,7 +262,7 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n,
     else
       grad(std::integral_constant<int, kActGelu>{});
 #pragma unroll
-    for (int j = 0; j < 32; j += 16)
+    for (int j = 0; j < W; j += 16)
       if (j < left) {
         store16(dg + j, &g[j / 8][0], left - j);
         store16(dg + p.N + j, &u[j / 8][0], left - j);
@@ -295,12 +306,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   pdl_wait();
   pdl_launch_dependents();
 
-  const int units = p.tiles_m * p.tiles_n * p.splits;
+  const int units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   const int first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
-  auto slice = [&](int split, int& k0, int& k1) {
-    k0 = (int)((long long)split * p.kgroups / p.splits);
-    k1 = (int)((long long)(split + 1) * p.kgroups / p.splits);
-  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -309,11 +316,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       int g = 0;
       bool ok = true;
       for (int u = first; u < units && ok; u += step) {
-        int mt, nt, split, k0, k1;
-        map_tile(u, p.tiles_m, p.tiles_n, mt, nt, split);
-        slice(split, k0, k1);
-        const int m0 = mt * C::kTileM + (int)rank * 128;
-        for (int kk = k0; kk < k1; ++kk, ++g) {
+        const Unit w = map_unit(p, u);
+        const int m0 = w.m * C::kTileM + (int)rank * 128, nt = w.n;
+        for (int kk = w.k0; kk < w.k1; ++kk, ++g) {
           const int s = g % C::kStages;
           if (!mbar_wait_bounded(&empty_bar[s], ((g / C::kStages) & 1) ^ 1, p.wait_ns)) {
             atomicOr(&g_dense_status, kStatusTimeoutProducer);
@@ -359,9 +364,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       int g = 0, i = 0;
       bool ok = true;
       for (int u = first; u < units && ok; u += step, ++i) {
-        int mt, nt, split, k0, k1;
-        map_tile(u, p.tiles_m, p.tiles_n, mt, nt, split);
-        slice(split, k0, k1);
+        const Unit w = map_unit(p, u);
         const int b = i & 1;
         const bool free = PAIR ? mbar_wait_cluster_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns)
                                : mbar_wait_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
         }
         tc_fence_after();
         const uint32_t acc = tmem + b * BN;
-        for (int kk = k0; kk < k1; ++kk, ++g) {
+        for (int kk = w.k0; kk < w.k1; ++kk, ++g) {
           const int s = g % C::kStages;
           if (!mbar_wait_bounded(&full_bar[s], (g / C::kStages) & 1, p.wait_ns)) {
             atomicOr(&g_dense_status, kStatusTimeoutMain);
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_f16_g<PAIR>(acc, ad + (uint64_t)(a_step * ks), bd + (uint64_t)(b_step * ks), idesc,
-                            kk > k0 || ks > 0 ? 1u : 0u);
+                            kk > w.k0 || ks > 0 ? 1u : 0u);
           commit_g<PAIR>(&empty_bar[s]);
         }
         if (ok) commit_g<PAIR>(&accf_bar[b]);
@@ -398,8 +401,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lane quarter; which 32-column chunks
     int i = 0;
     for (int u = first; u < units; u += step, ++i) {
-      int mt, nt, split;
-      map_tile(u, p.tiles_m, p.tiles_n, mt, nt, split);
+      const Unit t = map_unit(p, u);
       const int b = i & 1;
       if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
@@ -408,18 +410,34 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       __syncwarp();
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * BN;
-      const int m = mt * C::kTileM + (int)rank * 128 + q * 32 + lane;
+      const int r = (int)rank * 128 + q * 32 + lane, m = t.m * C::kTileM + r;  // row in the tile, in the matrix
       const bool live = m < p.M;
-      constexpr int kCols = MODE == kDenseGateUp ? BN / 2 : BN;
+      if (t.slot >= 0 && p.splits > 1) {
+        // a K slice's sums as they are: [slot][row of the tile][BN]
+        float* part = p.partial + ((size_t)t.slot * C::kTileM + r) * BN;
 #pragma unroll 1
-      for (int c = 32 * half; c < kCols; c += 64) {
-        float v[32], w[32];
-        tmem_ld_32x32b_x32(acc + c, v);
-        if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + BN / 2 + c, w);
-        tmem_wait_ld();
-        const int n = nt * kCols + c, left = p.N - n;  // a multiple of 8
-        if (!live) continue;
-        epilogue<X, MODE>(p, m, n, left, split, v, w);
+        for (int c = 32 * half; c < BN; c += 64) {
+          float v[32];
+          tmem_ld_32x32b_x32(acc + c, v);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) store8(part + c + j, v + j);
+          }
+          __syncwarp();  // the next tensor-memory load is the whole warp's
+        }
+      } else {
+        constexpr int kCols = MODE == kDenseGateUp ? BN / 2 : BN;
+#pragma unroll 1
+        for (int c = 32 * half; c < kCols; c += 64) {
+          float v[32], w[32];
+          tmem_ld_32x32b_x32(acc + c, v);
+          if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + BN / 2 + c, w);
+          tmem_wait_ld();
+          const int n = t.n * kCols + c;
+          if (live) epilogue<X, MODE, 32>(p, m, n, p.N - n, v, w);  // p.N - n: a multiple of 8
+          __syncwarp();
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -450,61 +468,90 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   if (warp == 1) tmem_dealloc_g<PAIR>(tmem, C::kTmemCols);
 }
 
-// Sum of the K slices in slice order, rounded once.  Eight columns per thread.
-template <typename X>
-__global__ void __launch_bounds__(256) dense_join_kernel(const float* partial, int splits, size_t count, X* out) {
+// The split tiles: the slices' sums in slice order, then the epilogue.  16 columns (of gate
+// and of up) per thread.
+template <typename X, int MODE>
+__global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__ DenseGemmParams p, int tile_rows, int bn) {
   pdl_wait();
   pdl_launch_dependents();
-  const size_t v = blockIdx.x * (size_t)256 + threadIdx.x;
-  if (v >= count / 8) return;
-  float acc[8];
-  Vec8<float> t;
-  t.load(partial, v);
-  t.get(acc);
-  for (int s = 1; s < splits; ++s) {
-    float f[8];
-    t.load(partial + s * count, v);
-    t.get(f);
+  const int cols = MODE == kDenseGateUp ? bn / 2 : bn, per_row = cols / 16;
+  const long long i = blockIdx.x * 256LL + threadIdx.x;
+  const int c = (int)(i % per_row) * 16;
+  const int r = (int)(i / per_row % tile_rows), tile = (int)(i / per_row / tile_rows);
+  if (p.full + tile >= p.tiles_m * p.tiles_n) return;
+  const Unit t = map_unit(p, p.full + tile * p.splits);
+  const int m = t.m * tile_rows + r, n = t.n * cols + c;
+  if (m >= p.M || n >= p.N) return;
+  float v[16], w[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += f[i];
+  for (int j = 0; j < 16; ++j) v[j] = w[j] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float* part = p.partial + ((size_t)(tile * p.splits + s) * tile_rows + r) * bn + c;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 16; j += 8) {
+      load8(f, part + j);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j + k] += f[k];
+      if constexpr (MODE == kDenseGateUp) {
+        load8(f, part + cols + j);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[j + k] += f[k];
+      }
+    }
   }
-  Vec8<X> o;
-  o.set(acc);
-  o.store(out, v);
+  epilogue<X, MODE, 16>(p, m, n, p.N - n, v, w);
 }
 
 // ------------------------------------------------------------------ host side
 struct Shape {
   int bn;
   bool pair;
-  int tiles_m, tiles_n, splits;
+  int tiles_m, tiles_n, full, splits;
 };
 
-// Tile shape.  Pairs of SMs on 256 x 256 tiles once there are rows and tiles for them;
-// one SM on 128 x 128 or 128 x 64 tiles below, where more and smaller tiles keep all SMs
-// streaming weights; K split (a plain store only) while whole tiles leave SMs idle.
+// Tile shape and split by estimated time, in cycles.  A unit's K group (64 values) takes
+// what its MMAs and its operand bytes need; a round of whole tiles takes all SMs, and the
+// tiles of a last, partial round may be cut along K so that its slices fill the SMs,
+// at the price of f32 partial sums written and read and one more launch.  The constants
+// are fitted to measured products (256 x 256 pair tiles run at 650 cycles a K group, a
+// block brings in about 50 bytes a cycle, HBM gives each SM 23).
 Shape pick_shape(int M, int N, int K, int mode) {
-  const int cols = mode == kDenseGateUp ? 2 * N : N;
-  Shape s{};
-  const long long pair_tiles = (long long)ceil_div(M, 256) * ceil_div(cols, 256);
-  if (M > 128 && pair_tiles >= 48) {
-    s.bn = 256;
-    s.pair = true;
-  } else {
-    s.bn = (long long)ceil_div(M, 128) * ceil_div(cols, 128) >= kMaxCtas ? 128 : 64;
+  const int sms = device_sms(), kg = ceil_div(K, 64), cols = mode == kDenseGateUp ? 2 * N : N;
+  const float hbm = ((float)M + (float)cols) * (float)K * 2.f / (23.f * (float)sms);
+  Shape best{};
+  float best_time = 0.f;
+  for (int config = 0; config < 3; ++config) {
+    Shape s{};
+    s.pair = config == 0;
+    s.bn = config == 0 ? 256 : config == 1 ? 128 : 64;
+    if (s.pair && M <= 128) continue;
+    const int tile_m = s.pair ? 256 : 128, workers = s.pair ? sms / 2 : sms;
+    s.tiles_m = ceil_div(M, tile_m);
+    s.tiles_n = ceil_div(cols, s.bn);
+    if (mode == kDenseGateUp) s.tiles_n = ceil_div(N, s.bn / 2);
+    const int rows = M < 128 ? M : 128;
+    const float bytes = (float)(rows + (s.pair ? 128 : s.bn)) * 128.f;
+    const float group = s.pair ? 650.f : bytes / 50.f > 2.2f * s.bn ? bytes / 50.f : 2.2f * s.bn;
+    const int tiles = s.tiles_m * s.tiles_n, rem = tiles % workers;
+    for (int splits = 1; splits <= kDenseMaxSplits && (splits == 1 || kg / splits >= 4); ++splits) {
+      s.splits = splits;
+      s.full = splits == 1 ? tiles : tiles - rem;
+      if (splits > 1 && rem == 0) break;
+      float time = (float)ceil_div(s.full, workers) * ((float)kg * group + 1000.f);
+      if (splits > 1) {
+        const float slice = (float)ceil_div(kg, splits) * group + 1500.f;
+        const float moved = (float)rem * splits * (float)(s.pair ? 256 : rows) * s.bn * 8.f;
+        time += (float)ceil_div(rem * splits, workers) * slice + moved / 2500.f + 5000.f;
+      }
+      if (time < hbm) time = hbm + 0.1f * time;  // (ties on the HBM bound go to the smaller work)
+      if (best_time == 0.f || time < best_time) {
+        best_time = time;
+        best = s;
+      }
+    }
   }
-  s.tiles_m = ceil_div(M, s.pair ? 256 : 128);
-  s.tiles_n = mode == kDenseGateUp ? ceil_div(N, s.bn / 2) : ceil_div(N, s.bn);
-  s.splits = 1;
-  if (mode == kDenseStore && !s.pair) {
-    const long long tiles = (long long)s.tiles_m * s.tiles_n;
-    const int kg = ceil_div(K, 64);
-    int want = (int)(2LL * kMaxCtas / tiles);
-    if (want > kg / 8) want = kg / 8;  // a slice keeps at least eight stages
-    if (want > 8) want = 8;
-    if (want > 1) s.splits = want;
-  }
-  return s;
+  return best;
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -577,7 +624,7 @@ cudaError_t launch_kernel(const DenseGemmParams& p, cudaStream_t stream) {
   int blocks = 0;
   e = resident_blocks(kern, C::kSmemBytes, PAIR, cached, &blocks);
   if (e != cudaSuccess) return e;
-  const long long need = (long long)p.tiles_m * p.tiles_n * p.splits * C::kCtas;
+  const long long need = (p.full + (long long)(p.tiles_m * p.tiles_n - p.full) * p.splits) * C::kCtas;
   if (need < blocks) blocks = (int)need;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
@@ -595,29 +642,31 @@ cudaError_t launch_kernel(const DenseGemmParams& p, cudaStream_t stream) {
 }
 
 template <typename X, int MODE>
-cudaError_t launch_shape(const DenseGemmParams& p, const Shape& s, cudaStream_t stream) {
-  if constexpr (MODE != kDensePartial)
-    if (s.pair) return launch_kernel<X, MODE, 256, true>(p, stream);
-  return s.bn == 128 ? launch_kernel<X, MODE, 128, false>(p, stream) : launch_kernel<X, MODE, 64, false>(p, stream);
+cudaError_t launch_mode(const DenseGemmParams& p, const Shape& s, cudaStream_t stream) {
+  const cudaError_t e = s.pair         ? launch_kernel<X, MODE, 256, true>(p, stream)
+                        : s.bn == 128 ? launch_kernel<X, MODE, 128, false>(p, stream)
+                                      : launch_kernel<X, MODE, 64, false>(p, stream);
+  if (e != cudaSuccess || s.splits == 1) return e;
+  const int tile_rows = s.pair ? 256 : 128;
+  const long long threads =
+      (long long)(s.tiles_m * s.tiles_n - s.full) * tile_rows * ((MODE == kDenseGateUp ? s.bn / 2 : s.bn) / 16);
+  return launch_pdl(dense_join_kernel<X, MODE>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, p, tile_rows,
+                    s.bn);
 }
 
 template <typename X>
-cudaError_t launch_mode(const DenseGemmParams& p, const Shape& s, int mode, cudaStream_t stream) {
-  if (mode == kDenseGateUp) return launch_shape<X, kDenseGateUp>(p, s, stream);
-  if (mode == kDenseGateUpGrad) return launch_shape<X, kDenseGateUpGrad>(p, s, stream);
-  if (s.splits == 1) return launch_shape<X, kDenseStore>(p, s, stream);
-  const cudaError_t e = launch_shape<X, kDensePartial>(p, s, stream);
-  if (e != cudaSuccess) return e;
-  const size_t count = (size_t)p.M * p.N;
-  return launch_pdl(dense_join_kernel<X>, dim3((unsigned)((count / 8 + 255) / 256)), dim3(256), 0, stream,
-                    (const float*)p.partial, p.splits, count, reinterpret_cast<X*>(p.out));
+cudaError_t launch_type(const DenseGemmParams& p, const Shape& s, int mode, cudaStream_t stream) {
+  if (mode == kDenseGateUp) return launch_mode<X, kDenseGateUp>(p, s, stream);
+  if (mode == kDenseGateUpGrad) return launch_mode<X, kDenseGateUpGrad>(p, s, stream);
+  return launch_mode<X, kDenseStore>(p, s, stream);
 }
 
 }  // namespace
 
 size_t dense_partial_bytes(int M, int N, int K, int mode) {
   const Shape s = pick_shape(M, N, K, mode);
-  return s.splits > 1 ? (size_t)s.splits * M * N * sizeof(float) : 0;
+  if (s.splits == 1) return 0;
+  return (size_t)(s.tiles_m * s.tiles_n - s.full) * s.splits * (s.pair ? 256 : 128) * s.bn * sizeof(float);
 }
 
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
@@ -627,13 +676,14 @@ int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOpera
   p.b_mn = b.mn_major;
   p.tiles_m = s.tiles_m;
   p.tiles_n = s.tiles_n;
+  p.full = s.full;
   p.splits = s.splits;
   p.kgroups = ceil_div(p.K, 64);
   p.wait_ns = gemm_wait_limit_ns();
   if (!operand_map(&p.tm_a, a, a.mn_major ? 64 : 128, dtype)) return MOE_ERR_CUDA;
   if (!operand_map(&p.tm_b, b, b.mn_major ? 64 : s.bn / 2, dtype)) return MOE_ERR_CUDA;
-  const cudaError_t e = dtype == kDtypeF16 ? launch_mode<__half>(p, s, mode, stream)
-                                           : launch_mode<__nv_bfloat16>(p, s, mode, stream);
+  const cudaError_t e = dtype == kDtypeF16 ? launch_type<__half>(p, s, mode, stream)
+                                           : launch_type<__nv_bfloat16>(p, s, mode, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
