@@ -465,10 +465,7 @@ __global__ void __launch_bounds__(512, 2)
     if (warps == 1) return t;
     if (lane == 0) buf[group * warps + warp] = t;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(per) : "memory");
-    t = lane < warps ? buf[group * warps + lane] : 0.f;  // at most 16 warps
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
+    return warp_sum_butterfly(lane < warps ? buf[group * warps + lane] : 0.f);
   };
   if (leader) {
     for (int i = 0; i < rows.stages; ++i) ptx::mbar_init(&full_bar[group][i], 1);

@@ -98,6 +98,22 @@ def test_widths_and_row_counts(T, H):
     both(make(T, H, torch.bfloat16, torch.bfloat16, "feature", seed=H), 1.0)
 
 
+@pytest.mark.parametrize("gate", ["none", "feature", "token", "full"])
+@pytest.mark.parametrize("T,H", [(2001, 2880), (1300, 4096), (10007, 264), (18301, 8), (9800, 512)])
+def test_many_rows(T, H, gate):
+    """Row counts at which the forward's persistent blocks take over (four rows for each
+    group of threads on the GPU)."""
+    stream = torch.float32 if H == 4096 else torch.bfloat16
+    both(make(T, H, torch.bfloat16, stream, gate, seed=T), 0.7)
+
+
+@pytest.mark.parametrize("T,H,dtype,stream", [(300, 8192, torch.bfloat16, torch.float32), (7, 6000, torch.float16, torch.float16),
+                                              (1200, 4104, torch.bfloat16, torch.bfloat16)])
+@pytest.mark.parametrize("gate", ["none", "feature", "full"])
+def test_rows_wider_than_a_blocks_registers(T, H, dtype, stream, gate):
+    both(make(T, H, dtype, stream, gate, seed=H), 0.7)
+
+
 @pytest.mark.parametrize("post,nxt,residual,gate", [(False, True, True, "none"), (False, True, True, "token"),
                                                     (True, False, True, "full"), (True, True, False, "feature"),
                                                     (False, False, True, "feature"), (False, False, True, "none"),
