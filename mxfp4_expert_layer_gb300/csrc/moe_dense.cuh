@@ -221,7 +221,8 @@ struct ThinParams {
   int T, K, n_out;          // n_out: output features (gated: half the rows)
   int tiles, ku;            // row tiles, K units (128 codes, or 32 16-bit values)
   int act;
-  int kw;                   // MXFP4: K slices (blocks of a cluster)
+  int early;                // 16-bit: the weights may be read before the dependency wait
+  int log_kw;               // MXFP4: log2 of the blocks of a cluster, which split K
   const uint8_t* row_exp;   // MXFP4: the rows' largest E8M0 bytes, tile order
   uint8_t* packed;          // MXFP4: workspace for x in fragment order
   float* x_scale;           // MXFP4: and, behind it, its tokens' scales

@@ -133,6 +133,7 @@ int moe_ffn_forward(const void* x, const void* w_gateup, const void* w_down, int
     d.n_out = H;
     d.tiles = ceil_div(H, kThinRows);
     d.ku = ceil_div(I, 32);
+    d.early = 1;
     d.out = out;
     return cuda_status(launch_thin16(d, dtype, false, s));
   }

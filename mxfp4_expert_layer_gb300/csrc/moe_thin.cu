@@ -6,9 +6,9 @@
 // At these sizes every weight byte is read once and used for a few tokens, so the kernels
 // are bound by HBM, and what matters is the bytes in flight and the instructions spent
 // per weight.  The products run on mma.sync (m16n8k16, f32 sums): 16 weight rows are one
-// operand, the other up to 8 tokens a column group.  The sum over K is free to take its terms in any order, so each lane's
-// 16-byte weight read is its own operand fragments, with x permuted to match: no
-// shuffles.  Sums are added in a fixed order everywhere.
+// operand, up to 8 tokens (a column group) the other.  The sum over K is free to take its
+// terms in any order, so each lane's 16-byte weight read is its own operand fragments, with
+// x permuted to match: no shuffles.  Sums are added in a fixed order everywhere.
 //
 // MXFP4: two codes become an f16 pair by one conversion instruction (exact); a group's
 // 32 products are summed by two MMAs and then scaled in f32 by the group's scale, kept
@@ -78,48 +78,43 @@ __device__ __forceinline__ uint4 load_weights(const void* p) {
   return v;
 }
 
-// Adds the eight warps' sums (fragment layout: register pair c < 2 is row g, c >= 2 row
-// g + 8, token 2 t + (c & 1)) in warp order and writes the block's outputs.
-template <int NT, int RT>
+// Adds the eight warps' sums of a tile (fragment layout: register pair c < 2 is row g,
+// c >= 2 row g + 8, token 2 t + (c & 1)) in warp order and writes the block's outputs.
+constexpr int kFinishStride = kThinRows + 4;
+template <int NT>
 __device__ __host__ constexpr int finish_bytes() {
-  return kThinWarps * NT * 8 * (RT * kThinRows + 4) * 4;
+  return kThinWarps * NT * 8 * kFinishStride * 4;
 }
-template <typename X, int NT, int RT, bool GATED, int ACT>
-__device__ __forceinline__ void finish(const ThinParams& p, const float (&total)[RT][NT][4], float* red, int tile0,
-                                       int t0, int nt) {
-  constexpr int kRows = RT * kThinRows, kStride = kRows + 4;
+template <typename X, int NT, bool GATED, int ACT>
+__device__ __forceinline__ void finish(const ThinParams& p, const float (&total)[NT][4], float* red, int tile) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        red[(warp * NT * 8 + n * 8 + 2 * t + (c & 1)) * kStride + rt * 16 + g + 8 * (c >> 1)] = total[rt][n][c];
+    for (int c = 0; c < 4; ++c)
+      red[(warp * NT * 8 + n * 8 + 2 * t + (c & 1)) * kFinishStride + g + 8 * (c >> 1)] = total[n][c];
   __syncthreads();
-  constexpr int kOut = GATED ? kRows / 2 : kRows;
+  constexpr int kOut = GATED ? kThinRows / 2 : kThinRows;
   X* out = reinterpret_cast<X*>(p.out);
-  for (int i = threadIdx.x; i < nt * kOut; i += kThinThreads) {
-    const int tok = i / kOut, o = i - tok * kOut;
-    const size_t row = (size_t)(t0 + tok);
+  for (int i = threadIdx.x; i < p.T * kOut; i += kThinThreads) {
+    const int tok = i / kOut, o = i % kOut, f = tile * kOut + o;
+    if (f >= p.n_out) continue;
+    const size_t row = (size_t)tok;
     auto sum = [&](int r) {
-      float v = red[tok * kStride + r];
+      float v = red[tok * kFinishStride + r];
 #pragma unroll
-      for (int w = 1; w < kThinWarps; ++w) v += red[(w * NT * 8 + tok) * kStride + r];
+      for (int w = 1; w < kThinWarps; ++w) v += red[(w * NT * 8 + tok) * kFinishStride + r];
       return v;
     };
     if constexpr (GATED) {
-      const int f = tile0 * 8 + o, r = (o >> 3) * 16 + (o & 7);
-      if (f >= p.n_out) continue;
-      const float gv = sum(r), uv = sum(r + 8);
+      const float gv = sum(o), uv = sum(o + 8);
       if (p.gateup) {
         p.gateup[row * 2 * p.n_out + f] = gv;
         p.gateup[row * 2 * p.n_out + p.n_out + f] = uv;
       }
       out[row * p.n_out + f] = static_cast<X>(act_f<ACT>(gv) * uv);
     } else {
-      const int f = tile0 * 16 + o;
-      if (f < p.n_out) out[row * p.n_out + f] = static_cast<X>(sum(o));
+      out[row * p.n_out + f] = static_cast<X>(sum(o));
     }
   }
 }
@@ -152,27 +147,30 @@ __device__ __forceinline__ float scale_to_f16(uint4& v, uint32_t emax) {
   v = make_uint4(w[0], w[1], w[2], w[3]);
   return pow2_int(-pw);
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t base, uint32_t off) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(base + off));
-  return v;
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float (&v)[4]) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
 }
 
 // ------------------------------------------------------------------ MXFP4 weights
 // A block's eight warps take a tile each and walk K together.  A pipeline stage is one or
 // two K units of the block's tiles (contiguous in the prepared weights: one bulk copy)
-// and, where x is not resident, the same units of x; the warps refill the stages in turn.  So the bytes in flight do not depend on registers or on how
-// far the arithmetic has got, and the 16-byte shared-memory reads are the fragments.
+// and, where x is not resident, the same units of x; the warps refill the stages in turn.
+// So the bytes in flight do not depend on registers or on how far the arithmetic has got,
+// and the 16-byte shared-memory reads are the fragments.
 // x, as f16, comes in one of two ways:
 //   resident (few tokens, short K): the block converts it itself, once; rows padded by 64
 //     bytes, so that two tokens' 64-byte pieces fall into different banks;
 //   packed: a launch before wrote it to the workspace in fragment order.
 // Blocks are persistent over row groups; where there are too few groups to fill the GPU,
-// a cluster of blocks splits K and adds its sums through distributed shared memory, in
-// rank order.
+// a cluster of blocks splits K and each block finishes its share of the tokens, from the
+// fragments that the others write into its shared memory, added in rank order.  (K split
+// between the warps of a block, with a copy per slice and stage, measured slower: one token
+// x 131072 x 4096 67.8 us against 53.2.)
 constexpr int kUnitBytes = kMatvecUnitBytes;
 constexpr int kGroupBytes = kMatvecGroup * kUnitBytes;  // one K unit of eight tiles
 constexpr uint64_t kMatvecWaitNs = 1000000000ull;       // a wait may take 1 s
+constexpr int kMatvecMaxSplit = 4;                      // blocks of a cluster
 constexpr int kResidentPieces = 64;                     // resident x: (token, unit) pairs, at most
 static_assert(kMatvecGroup == kThinWarps, "one tile per warp and group");
 
@@ -185,9 +183,9 @@ struct MatvecCfg {
   static constexpr int kStages = NT == 1 ? 3 : NT == 2 ? 5 : 6;
   static constexpr int kUnitTotal = kGroupBytes + (PACKED ? NT * 2048 : 0);
   static constexpr int kStageBytes = kUnits * kUnitTotal;
-  static constexpr int kStride = kMatvecGroup * kThinRows + 4;  // a token's sums, where a cluster adds them
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static_assert(NT * 8 * kStride * 4 <= kRingBytes, "the sums take the ring's memory");
+  static_assert((NT > kMatvecMaxSplit ? NT : kMatvecMaxSplit) * kThinWarps * 512 <= kRingBytes,
+                "a cluster's fragments take the ring's memory");
 };
 __host__ __device__ inline int resident_row_halves(int ku) { return ku * 128 + 32; }
 inline bool matvec_resident(int tokens, int ku) { return tokens <= 8 && tokens * ku <= kResidentPieces; }
@@ -279,11 +277,11 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
   __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
   __shared__ uint32_t s_max[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int S = p.kw, rank = blockIdx.x % S, groups = p.tiles / kMatvecGroup;
+  const int log_s = p.log_kw, S = 1 << log_s, rank = blockIdx.x & (S - 1), groups = p.tiles / kMatvecGroup;
   const int t0 = blockIdx.y * NT * 8, nt = min(p.T - t0, NT * 8);
-  const int k_begin = rank * p.ku / S, k_end = (rank + 1) * p.ku / S, steps = ceil_div(k_end - k_begin, C::kUnits);
-  const int grp_step = gridDim.x / S, grp0 = blockIdx.x / S;
-  const int all = grp0 < groups ? (groups - grp0 + grp_step - 1) / grp_step * steps : 0;  // stages of this block
+  const int k_begin = rank * p.ku >> log_s, k_units = ((rank + 1) * p.ku >> log_s) - k_begin;
+  const int steps = (k_units + C::kUnits - 1) / C::kUnits;  // stages of a group
+  const int grp_step = gridDim.x >> log_s, grp0 = blockIdx.x >> log_s;
   uint8_t* const xs = thin_smem + C::kRingBytes;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -294,31 +292,37 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
   }
   if (!PACKED && threadIdx.x < 8) s_max[threadIdx.x] = 0;
   __syncthreads();
-  // stage i of the block: its weights, and its units of x
-  auto issue_w = [&](int i) {
-    const int u = k_begin + i % steps * C::kUnits, n = min(C::kUnits, k_end - u);
-    uint64_t* bar = &full_bar[i % C::kStages];
-    ptx::mbar_arrive_expect_tx(bar, n * C::kUnitTotal);
-    ptx::bulk_load(thin_smem + i % C::kStages * C::kStageBytes,
-                   reinterpret_cast<const uint8_t*>(p.w) + ((size_t)(grp0 + i / steps * grp_step) * p.ku + u) * kGroupBytes,
-                   n * kGroupBytes, bar);
+  // step `at` of group grp into stage s: its weights, and its units of x
+  auto issue_w = [&](int s, int grp, int at) {
+    const int u = at * C::kUnits, n = min(C::kUnits, k_units - u);
+    ptx::mbar_arrive_expect_tx(&full_bar[s], n * C::kUnitTotal);
+    ptx::bulk_load(thin_smem + s * C::kStageBytes,
+                   reinterpret_cast<const uint8_t*>(p.w) + ((size_t)grp * p.ku + k_begin + u) * kGroupBytes, n * kGroupBytes,
+                   &full_bar[s]);
   };
-  auto issue_x = [&](int i) {
-    const int u = k_begin + i % steps * C::kUnits, n = min(C::kUnits, k_end - u);
-    ptx::bulk_load(thin_smem + i % C::kStages * C::kStageBytes + C::kUnits * kGroupBytes,
-                   p.packed + ((size_t)blockIdx.y * p.ku + u) * (NT * 2048), n * NT * 2048, &full_bar[i % C::kStages]);
+  auto issue_x = [&](int s, int at) {
+    const int u = at * C::kUnits, n = min(C::kUnits, k_units - u);
+    ptx::bulk_load(thin_smem + s * C::kStageBytes + C::kUnits * kGroupBytes,
+                   p.packed + ((size_t)blockIdx.y * p.ku + k_begin + u) * (NT * 2048), n * NT * 2048, &full_bar[s]);
+  };
+  // `by` steps on from step `at` of group grp (steps wrap into the block's next groups)
+  auto advance = [&](int& grp, int& at, int by) {
+    for (at += by; at >= steps; at -= steps) grp += grp_step;
+  };
+  auto first_stages = [&](auto f) {
+    int grp = grp0, at = 0;
+    for (int s = 0; s < C::kStages && grp < groups; ++s, advance(grp, at, 1)) f(s, grp, at);
   };
   // Weights of packed x's kernel may be read before the dependency wait: the launch before
   // it is the packing one, which began its work only when all earlier work had completed.
-  if (PACKED && threadIdx.x == 0)
-    for (int i = 0; i < C::kStages && i < all; ++i) issue_w(i);
+  if (PACKED && threadIdx.x == 0) first_stages([&](int s, int grp, int at) { issue_w(s, grp, at); });
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   if (threadIdx.x == 0)
-    for (int i = 0; i < C::kStages && i < all; ++i) {
-      if (PACKED) issue_x(i);
-      else issue_w(i);
-    }
+    first_stages([&](int s, int grp, int at) {
+      if (PACKED) issue_x(s, at);
+      else issue_w(s, grp, at);
+    });
   float down[2] = {1.f, 1.f};  // scales of x's tokens 2 t, 2 t + 1 (resident x)
   const int row_halves = resident_row_halves(p.ku);
   if constexpr (!PACKED) {
@@ -353,107 +357,99 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
   const uint8_t* const x_row = xs + (min(g, nt - 1) * row_halves + 8 * t) * 2;
   X* const out = reinterpret_cast<X*>(p.out);
 
-  int i = 0;
+  int s = 0, prev = C::kStages - 1, turn = 0;  // this step's stage, the one before, the warp that refills
+  uint32_t phase = 0;
   bool ok = true;
   for (int grp = grp0; grp < groups; grp += grp_step) {
     float total[NT][4] = {};
-    for (int u0 = k_begin; u0 < k_end; u0 += C::kUnits, ++i) {
-      const int s = i % C::kStages;
-      if (ok && !ptx::mbar_wait_bounded(&full_bar[s], (i / C::kStages) & 1, kMatvecWaitNs)) ok = false;
+    for (int at = 0; at < steps; ++at) {
+      if (ok && !ptx::mbar_wait_bounded(&full_bar[s], phase, kMatvecWaitNs)) ok = false;
       const uint8_t* st = thin_smem + s * C::kStageBytes;
 #pragma unroll
       for (int j = 0; j < C::kUnits; ++j) {
-        if (u0 + j >= k_end) break;
+        const int u = at * C::kUnits + j;
+        if (u >= k_units) break;
         unit_product<NT>(st + j * kGroupBytes + warp * kUnitBytes, total, [&](int blk, int n8) {
           if constexpr (PACKED)
             return *reinterpret_cast<const uint4*>(st + C::kUnits * kGroupBytes + ((j * 4 + blk) * NT + n8) * 512 + lane * 16);
           else
-            return *reinterpret_cast<const uint4*>(x_row + ((u0 + j) * 128 + 32 * blk) * 2);
+            return *reinterpret_cast<const uint4*>(x_row + ((k_begin + u) * 128 + 32 * blk) * 2);
         });
       }
       __syncwarp();
       if (lane == 0) {
         ptx::mbar_arrive(&empty_bar[s]);
         // refill the stage before this one, which the other warps have most likely left too
-        const int prev = i - 1, next = prev + C::kStages;
-        if (warp == i % kThinWarps && prev >= 0 && next < all) {
-          if (!ptx::mbar_wait_bounded(&empty_bar[prev % C::kStages], (prev / C::kStages) & 1, kMatvecWaitNs)) ok = false;
-          if (ok) {
-            issue_w(next);
-            if (PACKED) issue_x(next);
+        if (warp == turn && (grp != grp0 || at > 0)) {
+          int next = grp, to = at - 1;
+          advance(next, to, C::kStages);
+          if (next < groups) {
+            // (that stage's phase is this one's, unless the ring wrapped between them)
+            if (!ptx::mbar_wait_bounded(&empty_bar[prev], prev > s ? phase ^ 1 : phase, kMatvecWaitNs)) ok = false;
+            if (ok) {
+              issue_w(prev, next, to);
+              if (PACKED) issue_x(prev, to);
+            }
           }
         }
+      }
+      turn = (turn + 1) & (kThinWarps - 1);
+      prev = s;
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
       }
     }
     const int tile0 = grp * kMatvecGroup;
-    if (S == 1) {
-      // this warp's outputs straight from its fragments: row g and g + 8, tokens 2 t, 2 t + 1
-      const int tile = tile0 + warp, f = tile * (GATED ? 8 : 16) + g;
-      if (f >= p.n_out) continue;
-      const int f8 = GATED ? p.n_out + f : f + 8;  // the weight row of the second half
-      const bool low = GATED || f8 < p.n_out;
-      const float b0 = p.bias ? p.bias[f] : 0.f, b1 = p.bias && low ? p.bias[f8] : 0.f;
-      const float r0 = row_scale(p, tile * 16 + g), r1 = row_scale(p, tile * 16 + g + 8);
-#pragma unroll
-      for (int n8 = 0; n8 < NT; ++n8)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int tok = 8 * n8 + 2 * t + c;
-          if (tok >= nt) continue;
-          const size_t row = (size_t)(t0 + tok) * p.n_out;
-          const float q = PACKED ? __ldcg(p.x_scale + t0 + tok) : down[c];
-          const float v0 = fmaf(total[n8][c] * q, r0, b0), v1 = fmaf(total[n8][2 + c] * q, r1, b1);
-          if constexpr (GATED) {
-            out[row + f] = static_cast<X>(act_f<ACT>(v0) * v1);
-          } else {
-            out[row + f] = static_cast<X>(v0);
-            if (low) out[row + f8] = static_cast<X>(v1);
-          }
-        }
-    } else {
-      // (one group per cluster) the blocks' sums, [token][row], in the ring's memory: every
-      // copy has been consumed
-      __syncthreads();
-      float* red = reinterpret_cast<float*>(thin_smem);
-#pragma unroll
-      for (int n8 = 0; n8 < NT; ++n8)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          red[(n8 * 8 + 2 * t + (c & 1)) * C::kStride + warp * 16 + g + 8 * (c >> 1)] =
-              PACKED ? total[n8][c] : total[n8][c] * down[c & 1];
+    if (S > 1) {
+      // (one group per cluster) Each block finishes the column groups n8 = rank (mod S): the
+      // others send theirs to its ring, [n8 / S][sender][warp][lane], whose copies have all
+      // been consumed once its warps have arrived.
       ptx::cluster_arrive_release();
       ptx::cluster_wait_acquire();
-      // this block's share of the tiles
-      const int a = rank * kMatvecGroup / S, share = kMatvecGroup / S * (GATED ? 8 : 16);
-      const uint32_t red0 = ptx::smem_u32(red);
-      for (int o = threadIdx.x; o < nt * share; o += kThinThreads) {
-        const int tok = o / share, e = o - tok * share;
-        auto sum = [&](int r) {
-          float v = 0.f;
-          for (int s = 0; s < S; ++s) v += ld_cluster_f32(ptx::mapa_shared(red0, s), (tok * C::kStride + r) * 4);
-          if (PACKED) v *= __ldcg(p.x_scale + t0 + tok);
-          return v * row_scale(p, tile0 * 16 + r);
-        };
-        const size_t row = (size_t)(t0 + tok) * p.n_out;
-        const int f = (tile0 + a) * (GATED ? 8 : 16) + e;
-        if (f >= p.n_out) continue;
-        if constexpr (GATED) {
-          const int r = a * 16 + (e >> 3) * 16 + (e & 7);
-          float gv = sum(r), uv = sum(r + 8);
-          if (p.bias) {
-            gv += p.bias[f];
-            uv += p.bias[p.n_out + f];
+      const uint32_t slot = (warp * 32 + lane) * 16;
+#pragma unroll
+      for (int n8 = 0; n8 < NT; ++n8)
+        if ((n8 & (S - 1)) != rank)
+          st_cluster_f32x4(ptx::mapa_shared(ptx::smem_u32(thin_smem) + ((n8 >> log_s) * S + rank) * kThinWarps * 512 + slot,
+                                            n8 & (S - 1)), total[n8]);
+      ptx::cluster_arrive_release();
+      ptx::cluster_wait_acquire();
+#pragma unroll
+      for (int n8 = 0; n8 < NT; ++n8)
+        if ((n8 & (S - 1)) == rank)
+          for (int r = 0; r < S; ++r) {
+            if (r == rank) continue;
+            const float4 v = *reinterpret_cast<const float4*>(thin_smem + ((n8 >> log_s) * S + r) * kThinWarps * 512 + slot);
+            total[n8][0] += v.x;
+            total[n8][1] += v.y;
+            total[n8][2] += v.z;
+            total[n8][3] += v.w;
           }
-          out[row + f] = static_cast<X>(act_f<ACT>(gv) * uv);
+    }
+    // this warp's outputs straight from its fragments: row g and g + 8, tokens 2 t, 2 t + 1
+    const int tile = tile0 + warp, f = tile * (GATED ? 8 : 16) + g;
+    if (f >= p.n_out) continue;
+    const int f8 = GATED ? p.n_out + f : f + 8;  // the weight row of the second half
+    const bool low = GATED || f8 < p.n_out;
+    const float b0 = p.bias ? p.bias[f] : 0.f, b1 = p.bias && low ? p.bias[f8] : 0.f;
+    const float r0 = row_scale(p, tile * 16 + g), r1 = row_scale(p, tile * 16 + g + 8);
+#pragma unroll
+    for (int n8 = 0; n8 < NT; ++n8)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int tok = 8 * n8 + 2 * t + c;
+        if (tok >= nt || (n8 & (S - 1)) != rank) continue;
+        const size_t row = (size_t)(t0 + tok) * p.n_out;
+        const float q = PACKED ? __ldcg(p.x_scale + t0 + tok) : down[c];
+        const float v0 = fmaf(total[n8][c] * q, r0, b0), v1 = fmaf(total[n8][2 + c] * q, r1, b1);
+        if constexpr (GATED) {
+          out[row + f] = static_cast<X>(act_f<ACT>(v0) * v1);
         } else {
-          float v = sum(a * 16 + e);
-          if (p.bias) v += p.bias[f];
-          out[row + f] = static_cast<X>(v);
+          out[row + f] = static_cast<X>(v0);
+          if (low) out[row + f8] = static_cast<X>(v1);
         }
       }
-      ptx::cluster_arrive_release();  // the peers have read this block's sums
-      ptx::cluster_wait_acquire();
-    }
   }
   // a copy waited for in vain may still land: report, and stay until it surely has
   if (!ok) {
@@ -526,66 +522,65 @@ __global__ void matvec_prepare_kernel(MatvecPrepareParams p) {
 }
 
 // ------------------------------------------------------------------ 16-bit weights
-template <typename X, int NT, int RT, bool GATED, int ACT>
-__global__ void __launch_bounds__(kThinThreads) thin16_kernel(const __grid_constant__ ThinParams p) {
-  constexpr int kUnits = RT == 4 ? 2 : RT == 2 ? 4 : 8;  // 32-value units per chunk: 8 unit tiles in flight
+// One tile of 16 rows per block; its eight warps split K, each loading eight units of 32
+// values (16 bytes a lane and row) at a time straight to registers, so that two blocks per
+// SM have 128 KB in flight.  Two or four tiles per block, which share the x fragments,
+// measured slower at every size (16 tokens, 4096 x 14336: 71 and 76 us against 70; one
+// token 57 and 70 against 55, 0.96 of the measured copy rate), and so did three and four
+// blocks per SM with fewer units each.
+template <typename X, int NT, bool GATED, int ACT>
+__global__ void __launch_bounds__(kThinThreads, 2) thin16_kernel(const __grid_constant__ ThinParams p) {
+  constexpr int kUnits = 8;
   extern __shared__ __align__(128) uint8_t thin_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tile0 = blockIdx.x * RT, t0 = blockIdx.y * kThinTokens;
-  const int nt = min(p.T - t0, NT * 8);
+  const int tile = blockIdx.x;
   const int u_end = (int)((long long)(warp + 1) * p.ku / kThinWarps);
   int u = (int)((long long)warp * p.ku / kThinWarps);
-  // the two weight rows of this lane in each tile (rows past the matrix read the last row
-  // and are dropped at the end)
-  const uint16_t* w = reinterpret_cast<const uint16_t*>(p.w);
-  const uint16_t* rows[RT][2];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if constexpr (GATED) {
-      const int f = min((tile0 + rt) * 8 + g, p.n_out - 1);
-      rows[rt][0] = w + (size_t)f * p.K;
-      rows[rt][1] = w + (size_t)(p.n_out + f) * p.K;
-    } else {
-      const int f = (tile0 + rt) * 16 + g;
-      rows[rt][0] = w + (size_t)min(f, p.n_out - 1) * p.K;
-      rows[rt][1] = w + (size_t)min(f + 8, p.n_out - 1) * p.K;
-    }
-  }
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + (size_t)t0 * p.K;
-  float total[RT][NT][4] = {};
+  // the two weight rows of this lane (rows past the matrix read the last row and are
+  // dropped at the end)
+  const int f = tile * (GATED ? 8 : 16) + g, last = p.n_out - 1;
+  const uint16_t* w = reinterpret_cast<const uint16_t*>(p.w) + 8 * t;
+  const uint16_t* row0 = w + (size_t)min(f, last) * p.K;
+  const uint16_t* row1 = w + (size_t)(GATED ? p.n_out + min(f, last) : min(f + 8, last)) * p.K;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (; u < u_end; u += kUnits) {
-    uint4 wr[RT][kUnits][2];
+  uint4 wr[kUnits][2];
+  auto load = [&](int from) {
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) {
-      const int k = (u + j) * 32 + 8 * t;
-      const bool live = u + j < u_end && k < p.K;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        wr[rt][j][0] = live ? load_weights(rows[rt][0] + k) : zero;
-        wr[rt][j][1] = live ? load_weights(rows[rt][1] + k) : zero;
-      }
+      const bool live = from + j < u_end && (from + j) * 32 + 8 * t < p.K;
+      wr[j][0] = live ? load_weights(row0 + (from + j) * 32) : zero;
+      wr[j][1] = live ? load_weights(row1 + (from + j) * 32) : zero;
     }
+  };
+  if (p.early) {  // the weights, where the launch before is one of the same call
+    load(u);
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+  } else {
+    ptx::pdl_wait();
+    ptx::pdl_launch_dependents();
+    load(u);
+  }
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + 8 * t;
+  float total[NT][4] = {};
+  while (true) {
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) {
-      const int k = (u + j) * 32 + 8 * t;
-      const bool live = u + j < u_end && k < p.K;
+      const bool live = u + j < u_end && (u + j) * 32 + 8 * t < p.K;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 xf =
-            live && g + 8 * n < nt ? __ldcg(reinterpret_cast<const uint4*>(x + (size_t)(g + 8 * n) * p.K + k)) : zero;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint4 a = wr[rt][j][0], b = wr[rt][j][1];
-          mma16816<X>(total[rt][n], a.x, b.x, a.y, b.y, xf.x, xf.y);
-          mma16816<X>(total[rt][n], a.z, b.z, a.w, b.w, xf.z, xf.w);
-        }
+            live && g + 8 * n < p.T ? __ldcg(reinterpret_cast<const uint4*>(x + (size_t)(g + 8 * n) * p.K + (u + j) * 32)) : zero;
+        const uint4 a = wr[j][0], b = wr[j][1];
+        mma16816<X>(total[n], a.x, b.x, a.y, b.y, xf.x, xf.y);
+        mma16816<X>(total[n], a.z, b.z, a.w, b.w, xf.z, xf.w);
       }
     }
+    u += kUnits;
+    if (u >= u_end) break;
+    load(u);
   }
-  finish<X, NT, RT, GATED, ACT>(p, total, reinterpret_cast<float*>(thin_smem), tile0, t0, nt);
+  finish<X, NT, GATED, ACT>(p, total, reinterpret_cast<float*>(thin_smem), tile);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -601,9 +596,11 @@ cudaError_t launch_matvec_t(ThinParams p, cudaStream_t stream) {
   }
   // clusters along K while whole groups leave resident blocks idle and a block keeps two units
   const int groups = p.tiles / kMatvecGroup, resident = C::kPerSm * device_sms();
-  p.kw = 1;
-  while (p.kw < 8 && 2 * groups * groups_t * p.kw <= resident && p.ku >= 4 * p.kw) p.kw *= 2;
-  const int blocks = p.kw > 1 || groups * groups_t < resident ? groups * p.kw : max(1, resident / groups_t);
+  p.log_kw = 0;
+  while ((2 << p.log_kw) <= kMatvecMaxSplit && 2 * groups * groups_t << p.log_kw <= resident && p.ku >= 4 << p.log_kw)
+    ++p.log_kw;
+  const int split = 1 << p.log_kw;
+  const int blocks = split > 1 || groups * groups_t < resident ? groups * split : max(1, resident / groups_t);
   const int smem = C::kRingBytes + (PACKED ? 0 : p.T * resident_row_halves(p.ku) * 2);
   auto kern = matvec_kernel<X, NT, PACKED, GATED, ACT>;
   static SmemOptIn opt_in;
@@ -618,9 +615,9 @@ cudaError_t launch_matvec_t(ThinParams p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {(unsigned)p.kw, 1, 1};
+  attr[1].val.clusterDim = {(unsigned)split, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = p.kw > 1 ? 2 : 1;
+  cfg.numAttrs = split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -633,30 +630,15 @@ cudaError_t launch_matvec_nt(const ThinParams& p, cudaStream_t stream) {
   return launch_matvec_t<X, 4, true, GATED, ACT>(p, stream);
 }
 
-template <typename X, int NT, int RT, bool GATED, int ACT>
-cudaError_t launch_thin16_t(const ThinParams& p, cudaStream_t stream) {
-  auto kern = thin16_kernel<X, NT, RT, GATED, ACT>;
-  static SmemOptIn opt_in;
-  const cudaError_t e = opt_in.ensure(kern, finish_bytes<NT, RT>());
-  if (e != cudaSuccess) return e;
-  const dim3 grid(ceil_div(p.tiles, RT), ceil_div(p.T, kThinTokens));
-  return launch_pdl(kern, grid, dim3(kThinThreads), finish_bytes<NT, RT>(), stream, p);
-}
-
-// Row tiles per block: as many (up to four) as leave two blocks for every SM -- more
-// tiles share each x fragment, fewer leave SMs without work.
 template <typename X, int NT, bool GATED, int ACT>
-cudaError_t launch_thin16_rt(const ThinParams& p, cudaStream_t stream) {
-  const int want = 2 * kMaxCtas;
-  if (ceil_div(p.tiles, 4) >= want) return launch_thin16_t<X, NT, 4, GATED, ACT>(p, stream);
-  if (ceil_div(p.tiles, 2) >= want) return launch_thin16_t<X, NT, 2, GATED, ACT>(p, stream);
-  return launch_thin16_t<X, NT, 1, GATED, ACT>(p, stream);
+cudaError_t launch_thin16_t(const ThinParams& p, cudaStream_t stream) {
+  return launch_pdl(thin16_kernel<X, NT, GATED, ACT>, dim3(p.tiles), dim3(kThinThreads), finish_bytes<NT>(), stream, p);
 }
 
 template <bool MX, typename X, bool GATED, int ACT>
 cudaError_t launch_nt(const ThinParams& p, cudaStream_t stream) {
   if constexpr (MX) return launch_matvec_nt<X, GATED, ACT>(p, stream);
-  return p.T <= 8 ? launch_thin16_rt<X, 1, GATED, ACT>(p, stream) : launch_thin16_rt<X, 2, GATED, ACT>(p, stream);
+  return p.T <= 8 ? launch_thin16_t<X, 1, GATED, ACT>(p, stream) : launch_thin16_t<X, 2, GATED, ACT>(p, stream);
 }
 
 template <bool MX, typename X>
