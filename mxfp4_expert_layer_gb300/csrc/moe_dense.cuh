@@ -247,6 +247,7 @@ struct DenseGemmParams {
   CUtensorMap tm_a, tm_b;
   int M, N, K;              // N: output columns (gate/up: features, half of B's rows)
   int a_mn, b_mn;           // operand stored with M (N) contiguous
+  int bn;                   // columns of a tile
   int tiles_m, tiles_n;
   int full, splits, kgroups;  // tiles after the first `full` are cut into `splits` slices of K (groups of 64)
   int act;
@@ -263,7 +264,7 @@ struct DenseOperand {
 };
 // One product with the tile shape chosen by size; `partial` (f32) holds
 // dense_partial_bytes() bytes and is used when K is split.
-size_t dense_partial_bytes(int M, int N, int K, int mode);
+size_t dense_partial_bytes(int M, int N, int K, int mode, bool b_mn);
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream);
 

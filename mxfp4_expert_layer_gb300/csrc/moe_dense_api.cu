@@ -66,7 +66,7 @@ FfnLayout ffn_layout(int T, int H, int I, bool backward) {
   L.h = take((size_t)T * I * 2);
   size_t part = 0;
   auto need = [&](int M, int N, int K, int mode) {
-    const size_t b = dense_partial_bytes(M, N, K, mode);
+    const size_t b = dense_partial_bytes(M, N, K, mode, backward);  // (the backward's B are all MN-major)
     if (b > part) part = b;
   };
   if (backward) {

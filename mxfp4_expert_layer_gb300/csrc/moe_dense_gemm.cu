@@ -7,15 +7,18 @@
 // an MN-major one (both are forms of the same swizzled shared-memory tile), so nothing
 // is transposed in memory.
 //
-// One persistent block per SM.  Warp 0 issues the TMA loads into a ring of stages of 64
-// K values, warp 1 the MMAs into one of two accumulators in tensor memory, warps 2-9 run
-// the epilogue of one tile while the next one's MMAs proceed.  Large products run on
-// pairs of SMs (cta_group::2): the pair computes a 256 x BN tile, each SM loading its
+// One persistent block per SM.  Warps 0 and 10 issue the TMA loads of A and of B into a
+// ring of stages, warp 1 the MMAs into one of two accumulators in tensor memory, warps
+// 2-9 run the epilogue of one tile while the next one's MMAs proceed.  Large products run
+// on pairs of SMs (cta_group::2): the pair computes a tile of 256 rows, each SM loading its
 // own 128 rows of A and half of B, so the bytes an SM must bring in per MMA are halved
 // against a 128-row tile of one SM; the first block of the pair issues the MMAs for both.
+// What bounds a large product is the MMAs: 540 cycles a K group of 64 of a 256 x 256 tile
+// against their 512 (2048 tokens, 4096 x 14336, forward: 367 us, 1.97 PFLOP/s).
 // Sums are f32; g and u are saved in f32 so that the backward's derivatives carry no
 // rounding but their own; h, dg and du are rounded to 16 bits because the next
 // product's tensor-core operands have that type.
+#include <cmath>
 #include "moe_dense.cuh"
 #include "sm100_ptx.cuh"
 
@@ -26,7 +29,7 @@ using namespace ptx;
 namespace {
 
 constexpr int kEpiWarps = 8;                    // two per tensor-memory lane quarter
-constexpr int kDenseThreads = 64 + 32 * kEpiWarps;
+constexpr int kDenseThreads = 96 + 32 * kEpiWarps;
 constexpr uint64_t kDrainLimit = 1000000000ull;  // ns for MMAs already issued (1 s)
 constexpr uint64_t kLandingNs = 20000000ull;     // ns after a time-out in which every issued copy has landed (20 ms)
 
@@ -51,44 +54,62 @@ __device__ __forceinline__ void tmem_dealloc_g(uint32_t taddr, uint32_t ncols) {
   else
     tmem_dealloc(taddr, ncols);
 }
+// Forms that a warp runs in step with one elected lane issuing.  The election is inside
+// each: with the loop in one lane's branch, or a predicate of the lane's number, a stage's
+// instructions took longer to issue than its MMAs to run (a K group of a 256 x 256 pair
+// tile, one warp for all loads: 700 and 640 cycles; elected 560).
+#define MOE_ELECTED "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p "
 // 2-D tiled load; in a pair the barrier may be the peer's (a cluster address).
 template <bool PAIR>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1) {
   if constexpr (PAIR)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-        "[%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-}
-template <bool PAIR>
-__device__ __forceinline__ void mma_f16_g(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile("{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, P;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+    asm volatile(MOE_ELECTED
+                 "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+                 "%4}], [%2];\n\t}" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
                  : "memory");
   else
-    mma_bf16(d, a, b, idesc, accumulate);
+    asm volatile(MOE_ELECTED
+                 "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+                 "[%2];\n\t}" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+                 : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %4, 0;\n\telect.sync _|p, 0xffffffff;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 // Arrive on `bar` -- in a pair on both blocks' barrier of that offset -- when the MMAs
 // issued so far are done.
 template <bool PAIR>
-__device__ __forceinline__ void commit_g(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar) {
   if constexpr (PAIR)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
+    asm volatile(MOE_ELECTED
+                 "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
   else
-    mma_commit(bar);
+    asm volatile(MOE_ELECTED "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+#undef MOE_ELECTED
+// A bounded wait of a whole warp, in step; the answer is the same in every lane.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const bool ok = mbar_wait_step(bar, parity, limit_ns);
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -168,12 +189,14 @@ template <int BN, bool PAIR>
 struct DenseCfg {
   static constexpr int kCtas = PAIR ? 2 : 1;
   static constexpr int kTileM = 128 * kCtas;
-  static constexpr int kBRows = BN / kCtas;               // rows of B in this block's shared memory
-  static constexpr int kABytes = 128 * 128, kBBytes = kBRows * 128;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStageBytes > 8 ? 8 : 196608 / kStageBytes;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-  static constexpr uint32_t kTx = (uint32_t)kStageBytes * kCtas;  // the pair's copies all count on one barrier
+  static constexpr int kABytes = 128 * 128, kBBytes = BN / kCtas * 128;  // of B in this block's shared memory
+  static constexpr int kGroupBytes = kABytes + kBBytes;  // of one K group (64 values)
+  // K groups per stage: a stage's waits and commits cost 440 cycles, more than the MMAs of a
+  // small tile's group (2048 tokens in 64-column tiles: 1215 us by one, 921 by two); a pair's
+  // tiles need the finer ring more (1001 tokens x 2880 x 2880: 44.0 us by one, 47.5 by two)
+  static constexpr int kGroups = PAIR ? 1 : 2;
+  static constexpr int kStages = 196608 / (kGroups * kGroupBytes);
+  static constexpr int kSmemBytes = kStages * kGroups * kGroupBytes + 1024;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory columns");
 };
@@ -280,6 +303,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int bn = PAIR ? p.bn : BN;  // columns of a tile
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -309,92 +333,117 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   const int units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   const int first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full_bar), 0) : smem_u32(full_bar);
-      int g = 0;
-      bool ok = true;
-      for (int u = first; u < units && ok; u += step) {
-        const Unit w = map_unit(p, u);
-        const int m0 = w.m * C::kTileM + (int)rank * 128, nt = w.n;
-        for (int kk = w.k0; kk < w.k1; ++kk, ++g) {
-          const int s = g % C::kStages;
-          if (!mbar_wait_bounded(&empty_bar[s], ((g / C::kStages) & 1) ^ 1, p.wait_ns)) {
-            atomicOr(&g_dense_status, kStatusTimeoutProducer);
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], C::kTx);
-          const uint32_t bar = full0 + 8 * s, a = smem_u32(smem + s * C::kStageBytes), b = a + C::kABytes;
-          if (p.a_mn) {
+  if (warp == 0 || warp == 2 + kEpiWarps) {
+    // ------------------------------------------------------------ TMA producers
+    // (whole warps, in step) one of A, one of B: issuing a load takes about 125 cycles and
+    // a stage's wait 190, so one warp for both could not keep up with the MMAs.
+    // The pair's copies all count on one barrier.
+    const bool of_b = warp != 0;
+    const int b_cols = bn / C::kCtas;
+    const uint32_t tx = (uint32_t)(C::kABytes + b_cols * 128) * C::kCtas;
+    const uint32_t full0 = PAIR ? mapa_shared(smem_u32(full_bar), 0) : smem_u32(full_bar);
+    const uint32_t base = smem_u32(smem) + (of_b ? C::kABytes : 0);
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = first; u < units && ok; u += step) {
+      const Unit w = map_unit(p, u);
+      const int m0 = w.m * C::kTileM + (int)rank * 128, nt = w.n;
+      for (int k0 = w.k0; k0 < w.k1; k0 += C::kGroups) {
+        if (!wait_warp(&empty_bar[s], phase ^ 1, p.wait_ns)) {
+          if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutProducer);
+          ok = false;
+          break;
+        }
+        const int n = min(C::kGroups, w.k1 - k0);
+        const uint32_t bar = full0 + 8 * s;
+        if (!of_b) mbar_arrive_expect_tx_if(lane == 0 && rank == 0, &full_bar[s], tx * n);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tma_load_2d<PAIR>(a + c * 8192, &p.tm_a, bar, m0 + 64 * c, kk * 64);
+        for (int j = 0; j < C::kGroups; ++j) {
+          if (j >= n) break;
+          const int k = (k0 + j) * 64;
+          const uint32_t dst = base + (s * C::kGroups + j) * C::kGroupBytes;
+          if (!of_b) {
+            if (p.a_mn) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) tma_load_2d<PAIR>(dst + c * 8192, &p.tm_a, bar, m0 + 64 * c, k);
+            } else {
+              tma_load_2d<PAIR>(dst, &p.tm_a, bar, k, m0);
+            }
+          } else if (p.b_mn) {
+            const int n0 = nt * bn + (int)rank * b_cols;
+            for (int c = 0; c < b_cols / 64; ++c) tma_load_2d<PAIR>(dst + c * 8192, &p.tm_b, bar, n0 + 64 * c, k);
           } else {
-            tma_load_2d<PAIR>(a, &p.tm_a, bar, kk * 64, m0);
-          }
-          if (p.b_mn) {
-            const int n0 = nt * BN + (int)rank * C::kBRows;
+            // gate then up features; or this block's columns in one box
 #pragma unroll
-            for (int c = 0; c < C::kBRows / 64; ++c) tma_load_2d<PAIR>(b + c * 8192, &p.tm_b, bar, n0 + 64 * c, kk * 64);
-          } else {
-            // boxes of BN / 2 rows: gate then up features, or the two halves of the columns
-#pragma unroll
-            for (int c = 0; c < 2 / C::kCtas; ++c) {
-              const int half = PAIR ? (int)rank : c;
-              const int row = MODE == kDenseGateUp ? half * p.N + nt * (BN / 2) : nt * BN + half * (BN / 2);
-              tma_load_2d<PAIR>(b + c * (BN / 2) * 128, &p.tm_b, bar, kk * 64, row);
+            for (int c = 0; c < (MODE == kDenseGateUp ? 2 / C::kCtas : 1); ++c) {
+              const int row =
+                  MODE == kDenseGateUp ? (PAIR ? (int)rank : c) * p.N + nt * (bn / 2) : nt * bn + (int)rank * b_cols;
+              tma_load_2d<PAIR>(dst + c * (bn / 2) * 128, &p.tm_b, bar, k, row);
             }
           }
+        }
+        if (++s == C::kStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (rank == 0 && lane == 0) {
+    // (the whole warp, in step)
+    if (rank == 0) {
       constexpr uint32_t kFmt = std::is_same<X, __half>::value ? 0u : 1u;  // operand format: f16 0, bf16 1
       const uint32_t idesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
-                             ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(C::kTileM >> 4) << 24);
+                             ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(C::kTileM >> 4) << 24);
       // K major: rows of 128 bytes in groups of 8 (1024 bytes), 32 bytes per K = 16 step.
       // MN major: 64 K rows of 128 bytes (64 values) per 8192-byte chunk, 8 K rows per
       // 1024 bytes, 2048 bytes per K = 16 step.
-      const uint32_t a_lbo = p.a_mn ? 8192 : 16, b_lbo = p.b_mn ? 8192 : 16;
       const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;  // in 16 bytes
-      const uint32_t base = smem_u32(smem);
-      int g = 0, i = 0;
+      const uint64_t a_desc = smem_desc(smem_u32(smem), p.a_mn ? 8192 : 16, 1024, 2);
+      const uint64_t b_desc = smem_desc(smem_u32(smem) + C::kABytes, p.b_mn ? 8192 : 16, 1024, 2);
+      int s = 0, i = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int u = first; u < units && ok; u += step, ++i) {
         const Unit w = map_unit(p, u);
         const int b = i & 1;
-        const bool free = PAIR ? mbar_wait_cluster_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns)
-                               : mbar_wait_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
+        const bool free = PAIR ? __all_sync(0xffffffffu, mbar_wait_cluster_step(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns))
+                               : wait_warp(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
         if (!free) {
-          atomicOr(&g_dense_status, kStatusTimeoutMain);
+          if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutMain);
           break;
         }
         tc_fence_after();
         const uint32_t acc = tmem + b * BN;
-        for (int kk = w.k0; kk < w.k1; ++kk, ++g) {
-          const int s = g % C::kStages;
-          if (!mbar_wait_bounded(&full_bar[s], (g / C::kStages) & 1, p.wait_ns)) {
-            atomicOr(&g_dense_status, kStatusTimeoutMain);
+        for (int k0 = w.k0; k0 < w.k1; k0 += C::kGroups) {
+          if (!wait_warp(&full_bar[s], phase, p.wait_ns)) {
+            if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutMain);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = smem_desc(base + s * C::kStageBytes, a_lbo, 1024, 2);
-          const uint64_t bd = smem_desc(base + s * C::kStageBytes + C::kABytes, b_lbo, 1024, 2);
+          const int n = min(C::kGroups, w.k1 - k0);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16_g<PAIR>(acc, ad + (uint64_t)(a_step * ks), bd + (uint64_t)(b_step * ks), idesc,
-                            kk > w.k0 || ks > 0 ? 1u : 0u);
-          commit_g<PAIR>(&empty_bar[s]);
+          for (int j = 0; j < C::kGroups; ++j) {
+            if (j >= n) break;
+            const uint64_t at = (uint64_t)((s * C::kGroups + j) * (C::kGroupBytes / 16));
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_f16<PAIR>(acc, a_desc + at + (uint64_t)(a_step * ks), b_desc + at + (uint64_t)(b_step * ks), idesc,
+                            k0 > w.k0 || j > 0 || ks > 0 ? 1u : 0u);
+          }
+          commit<PAIR>(&empty_bar[s]);
+          if (++s == C::kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) commit_g<PAIR>(&accf_bar[b]);
+        if (ok) commit<PAIR>(&accf_bar[b]);
       }
       // all tensor-core work is done before the tensor memory is freed
-      commit_g<PAIR>(&drain_bar);
-      mbar_wait_bounded(&drain_bar, 0, kDrainLimit);
+      commit<PAIR>(&drain_bar);
+      wait_warp(&drain_bar, 0, kDrainLimit);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -403,7 +452,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     for (int u = first; u < units; u += step, ++i) {
       const Unit t = map_unit(p, u);
       const int b = i & 1;
-      if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
+      if (!mbar_wait_step(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
         break;
       }
@@ -413,10 +462,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       const int r = (int)rank * 128 + q * 32 + lane, m = t.m * C::kTileM + r;  // row in the tile, in the matrix
       const bool live = m < p.M;
       if (t.slot >= 0 && p.splits > 1) {
-        // a K slice's sums as they are: [slot][row of the tile][BN]
-        float* part = p.partial + ((size_t)t.slot * C::kTileM + r) * BN;
+        // a K slice's sums as they are: [slot][row of the tile][bn]
+        float* part = p.partial + ((size_t)t.slot * C::kTileM + r) * bn;
 #pragma unroll 1
-        for (int c = 32 * half; c < BN; c += 64) {
+        for (int c = 32 * half; c < bn; c += 64) {
           float v[32];
           tmem_ld_32x32b_x32(acc + c, v);
           tmem_wait_ld();
@@ -427,15 +476,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
           __syncwarp();  // the next tensor-memory load is the whole warp's
         }
       } else {
-        constexpr int kCols = MODE == kDenseGateUp ? BN / 2 : BN;
+        const int cols = MODE == kDenseGateUp ? bn / 2 : bn;
 #pragma unroll 1
-        for (int c = 32 * half; c < kCols; c += 64) {
+        for (int c = 32 * half; c < cols; c += 64) {
           float v[32], w[32];
           tmem_ld_32x32b_x32(acc + c, v);
-          if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + BN / 2 + c, w);
+          if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + bn / 2 + c, w);
           tmem_wait_ld();
-          const int n = t.n * kCols + c;
-          if (live) epilogue<X, MODE, 32>(p, m, n, p.N - n, v, w);  // p.N - n: a multiple of 8
+          const int n = t.n * cols + c, left = min(p.N - n, cols - c);  // a multiple of 8
+          if (live) epilogue<X, MODE, 32>(p, m, n, left, v, w);
           __syncwarp();
         }
       }
@@ -511,28 +560,29 @@ struct Shape {
 };
 
 // Tile shape and split by estimated time, in cycles.  A unit's K group (64 values) takes
-// what its MMAs and its operand bytes need; a round of whole tiles takes all SMs, and the
-// tiles of a last, partial round may be cut along K so that its slices fill the SMs,
-// at the price of f32 partial sums written and read and one more launch.  The constants
-// are fitted to measured products (256 x 256 pair tiles run at 650 cycles a K group, a
-// block brings in about 50 bytes a cycle, HBM gives each SM 23).
-Shape pick_shape(int M, int N, int K, int mode) {
-  const int sms = device_sms(), kg = ceil_div(K, 64), cols = mode == kDenseGateUp ? 2 * N : N;
+// what its MMAs, its operand bytes and the issuing of both need; a round of whole tiles
+// takes all SMs, and the tiles of a last, partial round may be cut along K so that its
+// slices fill the SMs, at the price of f32 partial sums written and read and one more
+// launch.  The constants are fitted to measured products: a 256-column pair tile takes 540
+// cycles a K group, one of 192 columns and less 440 (issuing), one-SM tiles of 128 and 64
+// columns 530 and 335; HBM gives each SM 23 bytes a cycle.  Widths between the powers of two
+// (2048 tokens x 4096 x 14336: 367 us with them, 375 without) are for K-major B only: an
+// MN-major one comes in whole chunks of 64 columns.
+Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
+  const int kg = ceil_div(K, 64), cols = mode == kDenseGateUp ? 2 * N : N;
   const float hbm = ((float)M + (float)cols) * (float)K * 2.f / (23.f * (float)sms);
   Shape best{};
   float best_time = 0.f;
-  for (int config = 0; config < 3; ++config) {
+  for (int config = 0; config < 7; ++config) {
     Shape s{};
-    s.pair = config == 0;
-    s.bn = config == 0 ? 256 : config == 1 ? 128 : 64;
-    if (s.pair && M <= 128) continue;
+    s.pair = config < 5;
+    s.bn = s.pair ? 256 - 32 * config : config == 5 ? 128 : 64;
+    if (s.pair && (M <= 128 || (b_mn && s.bn % 128))) continue;
     const int tile_m = s.pair ? 256 : 128, workers = s.pair ? sms / 2 : sms;
     s.tiles_m = ceil_div(M, tile_m);
-    s.tiles_n = ceil_div(cols, s.bn);
-    if (mode == kDenseGateUp) s.tiles_n = ceil_div(N, s.bn / 2);
+    s.tiles_n = mode == kDenseGateUp ? ceil_div(N, s.bn / 2) : ceil_div(cols, s.bn);
     const int rows = M < 128 ? M : 128;
-    const float bytes = (float)(rows + (s.pair ? 128 : s.bn)) * 128.f;
-    const float group = s.pair ? 650.f : bytes / 50.f > 2.2f * s.bn ? bytes / 50.f : 2.2f * s.bn;
+    const float group = s.pair ? fmaxf(2.12f * s.bn, 440.f) : s.bn == 128 ? 530.f : 335.f;
     const int tiles = s.tiles_m * s.tiles_n, rem = tiles % workers;
     for (int splits = 1; splits <= kDenseMaxSplits && (splits == 1 || kg / splits >= 4); ++splits) {
       s.splits = splits;
@@ -552,6 +602,19 @@ Shape pick_shape(int M, int N, int K, int mode) {
     }
   }
   return best;
+}
+// The estimate is a function of the sizes alone; the last ones are kept per thread, since a
+// small product's launch would wait for its 3 us otherwise.
+Shape pick_shape(int M, int N, int K, int mode, bool b_mn) {
+  struct Entry {
+    int M, N, K, key;
+    Shape s;
+  };
+  static thread_local Entry kept[16] = {};
+  const int sms = device_sms(), key = sms * 8 + mode * 2 + b_mn;
+  Entry& e = kept[((unsigned)M * 31u + (unsigned)N * 7u + (unsigned)K * 3u + (unsigned)key) * 2654435761u >> 28];
+  if (e.M != M || e.N != N || e.K != K || e.key != key) e = {M, N, K, key, estimate_shape(M, N, K, mode, b_mn, sms)};
+  return e.s;
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -663,17 +726,18 @@ cudaError_t launch_type(const DenseGemmParams& p, const Shape& s, int mode, cuda
 
 }  // namespace
 
-size_t dense_partial_bytes(int M, int N, int K, int mode) {
-  const Shape s = pick_shape(M, N, K, mode);
+size_t dense_partial_bytes(int M, int N, int K, int mode, bool b_mn) {
+  const Shape s = pick_shape(M, N, K, mode, b_mn);
   if (s.splits == 1) return 0;
   return (size_t)(s.tiles_m * s.tiles_n - s.full) * s.splits * (s.pair ? 256 : 128) * s.bn * sizeof(float);
 }
 
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream) {
-  const Shape s = pick_shape(p.M, p.N, p.K, mode);
+  const Shape s = pick_shape(p.M, p.N, p.K, mode, b.mn_major);
   p.a_mn = a.mn_major;
   p.b_mn = b.mn_major;
+  p.bn = s.bn;
   p.tiles_m = s.tiles_m;
   p.tiles_n = s.tiles_n;
   p.full = s.full;
@@ -681,7 +745,7 @@ int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOpera
   p.kgroups = ceil_div(p.K, 64);
   p.wait_ns = gemm_wait_limit_ns();
   if (!operand_map(&p.tm_a, a, a.mn_major ? 64 : 128, dtype)) return MOE_ERR_CUDA;
-  if (!operand_map(&p.tm_b, b, b.mn_major ? 64 : s.bn / 2, dtype)) return MOE_ERR_CUDA;
+  if (!operand_map(&p.tm_b, b, b.mn_major ? 64 : s.pair || mode == kDenseGateUp ? s.bn / 2 : s.bn, dtype)) return MOE_ERR_CUDA;
   const cudaError_t e = dtype == kDtypeF16 ? launch_type<__half>(p, s, mode, stream)
                                            : launch_type<__nv_bfloat16>(p, s, mode, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
