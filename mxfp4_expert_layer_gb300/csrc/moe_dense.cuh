@@ -241,17 +241,24 @@ uint32_t* dense_status_word();
 constexpr int kDenseStore = 0;       // C in the operands' type
 constexpr int kDenseGateUp = 1;      // B rows: gate, then up; h = act(g) u, and g, u in f32 when asked for
 constexpr int kDenseGateUpGrad = 2;  // C = dh: dg, du from the saved g, u; and h again
+constexpr int kDenseProducts = 3;    // several products, each as kDenseStore
 constexpr int kDenseMaxSplits = 16;
 
-struct DenseGemmParams {
+// One product: C [M, N] = A B^T.
+struct DenseProblem {
   CUtensorMap tm_a, tm_b;
   int M, N, K;              // N: output columns (gate/up: features, half of B's rows)
   int a_mn, b_mn;           // operand stored with M (N) contiguous
-  int bn;                   // columns of a tile
-  int tiles_m, tiles_n;
-  int full, splits, kgroups;  // tiles after the first `full` are cut into `splits` slices of K (groups of 64)
-  int act;
+  int tiles_m, tiles_n, kgroups;  // K groups of 64
   void* out;                // 16-bit [M, N]; gate/up grad: dgu [M, 2 N]
+};
+constexpr int kDenseGroup = 3;  // products of one launch
+struct DenseGemmParams {
+  DenseProblem g[kDenseGroup];
+  int bn;                   // columns of a tile
+  int full, splits;         // tiles after the first `full` are cut into `splits` slices of K
+  int group, long_n, lead;  // several products: how many, those of the long class, and the lead (see below)
+  int act;
   void* out_h;              // gate/up grad: h [M, N]
   float* gateup;            // f32 [M, 2 N]: written by gate/up (or null), read by its gradient
   float* partial;           // f32 [slices][tile rows][tile columns]
@@ -267,5 +274,9 @@ struct DenseOperand {
 size_t dense_partial_bytes(int M, int N, int K, int mode, bool b_mn);
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream);
+// Up to kDenseGroup plain products (g[i].M, N, K, out set) whose K takes at most two values,
+// in one launch where that is estimated to be faster.
+int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const DenseOperand* b, int dtype,
+                          cudaStream_t stream);
 
 }  // namespace moe

@@ -138,16 +138,16 @@ int moe_ffn_forward(const void* x, const void* w_gateup, const void* w_down, int
     return cuda_status(launch_thin16(d, dtype, false, s));
   }
   DenseGemmParams g{};
-  g.M = T; g.N = I; g.K = H;
+  g.g[0].M = T; g.g[0].N = I; g.g[0].K = H;
+  g.g[0].out = h;
   g.act = act;
-  g.out = h;
   g.gateup = gateup_out;
   g.partial = ws_ptr<float>(workspace, L.partial);
   st = launch_dense_gemm(g, {x, T, H, 0}, {w_gateup, 2 * I, H, 0}, kDenseGateUp, dtype, s);
   if (st != MOE_OK) return st;
   DenseGemmParams d{};
-  d.M = T; d.N = H; d.K = I;
-  d.out = out;
+  d.g[0].M = T; d.g[0].N = H; d.g[0].K = I;
+  d.g[0].out = out;
   d.partial = ws_ptr<float>(workspace, L.partial);
   return launch_dense_gemm(d, {h, T, I, 0}, {w_down, H, I, 0}, kDenseStore, dtype, s);
 }
@@ -170,25 +170,29 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
   void* dgu = ws_ptr<uint8_t>(workspace, L.dgu);
   float* partial = ws_ptr<float>(workspace, L.partial);
   DenseGemmParams p{};  // dh = d_out W_down, and from it dg, du, h
-  p.M = T; p.N = I; p.K = H;
+  p.g[0].M = T; p.g[0].N = I; p.g[0].K = H;
+  p.g[0].out = dgu;
   p.act = act;
-  p.out = dgu;
   p.out_h = h;
   p.gateup = const_cast<float*>(gateup);
   p.partial = partial;
   st = launch_dense_gemm(p, {d_out, T, H, 0}, {w_down, H, I, 1}, kDenseGateUpGrad, dtype, s);
   if (st != MOE_OK) return st;
-  auto product = [&](int M, int N, int K, const DenseOperand& a, const DenseOperand& b, void* out) {
-    DenseGemmParams q{};
-    q.M = M; q.N = N; q.K = K;
-    q.out = out;
-    q.partial = partial;
-    return launch_dense_gemm(q, a, b, kDenseStore, dtype, s);
+  DenseGemmParams q{};  // what of it is asked for: dx = dgu W_gateup, dW_gateup = dgu^T x, dW_down = dout^T h
+  q.partial = partial;
+  DenseOperand a[kDenseGroup], b[kDenseGroup];
+  int n = 0;
+  auto product = [&](int M, int N, int K, const DenseOperand& am, const DenseOperand& bm, void* out) {
+    if (!out) return;
+    q.g[n].M = M; q.g[n].N = N; q.g[n].K = K;
+    q.g[n].out = out;
+    a[n] = am;
+    b[n++] = bm;
   };
-  if (d_x && (st = product(T, H, 2 * I, {dgu, T, 2 * I, 0}, {w_gateup, 2 * I, H, 1}, d_x)) != MOE_OK) return st;
-  if (d_w_gateup && (st = product(2 * I, H, T, {dgu, T, 2 * I, 1}, {x, T, H, 1}, d_w_gateup)) != MOE_OK) return st;
-  if (d_w_down && (st = product(H, I, T, {d_out, T, H, 1}, {h, T, I, 1}, d_w_down)) != MOE_OK) return st;
-  return MOE_OK;
+  product(T, H, 2 * I, {dgu, T, 2 * I, 0}, {w_gateup, 2 * I, H, 1}, d_x);
+  product(2 * I, H, T, {dgu, T, 2 * I, 1}, {x, T, H, 1}, d_w_gateup);
+  product(H, I, T, {d_out, T, H, 1}, {h, T, I, 1}, d_w_down);
+  return launch_dense_products(q, n, a, b, dtype, s);
 }
 
 int moe_dense_status(int* status, moe_stream_t stream) {

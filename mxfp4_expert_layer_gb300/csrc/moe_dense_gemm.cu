@@ -19,6 +19,7 @@
 // rounding but their own; h, dg and du are rounded to 16 bits because the next
 // product's tensor-core operands have that type.
 #include <cmath>
+#include <utility>
 #include "moe_dense.cuh"
 #include "sm100_ptx.cuh"
 
@@ -207,46 +208,112 @@ struct DenseCfg {
 // time share both operands through L2.
 constexpr int kRasterM = 8;
 struct Unit {
-  int m, n, slot, k0, k1;  // slot: place of the slice's partial sums, or -1
+  int g, m, n, slot, k0, k1;  // product; slot: place of the slice's partial sums, or -1
 };
+__device__ __forceinline__ void map_tile(const DenseProblem& g, int u, Unit& r) {
+  const int first = u / (kRasterM * g.tiles_n) * kRasterM;
+  const int rows = min(kRasterM, g.tiles_m - first);
+  const int within = u - first * g.tiles_n;
+  r.n = within / rows;
+  r.m = first + within - r.n * rows;
+}
 __device__ __forceinline__ Unit map_unit(const DenseGemmParams& p, int u) {
   Unit r;
+  r.g = 0;
   r.slot = u - p.full;
   r.k0 = 0;
-  r.k1 = p.kgroups;
+  r.k1 = p.g[0].kgroups;
   if (r.slot < 0) {
     r.slot = -1;
   } else if (p.splits > 1) {
     const int split = r.slot % p.splits;
     u = p.full + r.slot / p.splits;
-    r.k0 = (int)((long long)split * p.kgroups / p.splits);
-    r.k1 = (int)((long long)(split + 1) * p.kgroups / p.splits);
+    r.k0 = (int)((long long)split * p.g[0].kgroups / p.splits);
+    r.k1 = (int)((long long)(split + 1) * p.g[0].kgroups / p.splits);
   }
-  const int first = u / (kRasterM * p.tiles_n) * kRasterM;
-  const int rows = min(kRasterM, p.tiles_m - first);
-  const int within = u - first * p.tiles_n;
-  r.n = within / rows;
-  r.m = first + within - r.n * rows;
+  map_tile(p.g[0], u, r);
   return r;
 }
+
+// The units of one worker (a block, or a pair): every `workers`-th.  Several products: the
+// tiles of the long class (the larger K) in turn; then, while the workers that got one more
+// of those are still at it, each of the others takes `lead` tiles of the short class; then
+// all take the rest of it in turn, the earlier ones first.  So the products end together,
+// where each by itself would leave part of its last round's SMs idle.
+template <bool GROUP>
+struct Units {
+  const DenseGemmParams& p;
+  const int worker, workers;
+  int u, end, step, phase;
+  int n_long, n_short, more, head;  // tiles of the classes; workers with one more long tile; tiles taken in the lead
+  __device__ __forceinline__ Units(const DenseGemmParams& q, int w, int ws) : p(q), worker(w), workers(ws), phase(0) {
+    u = worker;
+    step = workers;
+    if constexpr (GROUP) {
+      n_long = n_short = 0;
+      for (int i = 0; i < p.group; ++i) (i < p.long_n ? n_long : n_short) += p.g[i].tiles_m * p.g[i].tiles_n;
+      more = n_long % workers;
+      head = more > 0 ? min(n_short, (workers - more) * p.lead) : 0;
+      end = n_long;
+      settle();
+    } else {
+      end = p.full + (p.g[0].tiles_m * p.g[0].tiles_n - p.full) * p.splits;
+    }
+  }
+  __device__ __forceinline__ void settle() {
+    while (u >= end && phase < 2) {
+      if (++phase == 1) {
+        u = worker >= more ? worker - more : head;
+        end = head;
+        step = workers - more;
+      } else if (n_short > 0) {
+        const bool late_first = (long long)p.lead * p.g[p.long_n].kgroups > p.g[0].kgroups;
+        u = head + (late_first || more == 0 ? worker : worker >= more ? worker - more : worker + workers - more);
+        end = n_short;
+        step = workers;
+      }
+    }
+  }
+  __device__ __forceinline__ bool on() const { return u < end; }
+  __device__ __forceinline__ void next() {
+    u += step;
+    if constexpr (GROUP) settle();
+  }
+  __device__ __forceinline__ Unit get() const {
+    if constexpr (GROUP) {
+      Unit r;
+      int at = u;
+      r.g = phase == 0 ? 0 : p.long_n;
+      for (; at >= p.g[r.g].tiles_m * p.g[r.g].tiles_n; ++r.g) at -= p.g[r.g].tiles_m * p.g[r.g].tiles_n;
+      r.slot = -1;
+      r.k0 = 0;
+      r.k1 = p.g[r.g].kgroups;
+      map_tile(p.g[r.g], at, r);
+      return r;
+    } else {
+      return map_unit(p, u);
+    }
+  }
+};
 
 // What happens to the sums of W columns of a row (`left` of them inside the matrix, in
 // eights): v, and for gate/up w the up sums.
 template <typename X, int MODE, int W>
-__device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n, int left, float (&v)[W], float (&w)[W]) {
-  X* out = reinterpret_cast<X*>(p.out);
-  if constexpr (MODE == kDenseStore) {
+__device__ __forceinline__ void epilogue(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left, float (&v)[W],
+                                         float (&w)[W]) {
+  X* out = reinterpret_cast<X*>(c.out);
+  if constexpr (MODE == kDenseStore || MODE == kDenseProducts) {
 #pragma unroll
     for (int j = 0; j < W; j += 16)
-      if (j < left) store16(out + (size_t)m * p.N + n + j, v + j, left - j);
+      if (j < left) store16(out + (size_t)m * c.N + n + j, v + j, left - j);
   } else if constexpr (MODE == kDenseGateUp) {
     if (p.gateup) {
-      float* gu = p.gateup + (size_t)m * 2 * p.N + n;
+      float* gu = p.gateup + (size_t)m * 2 * c.N + n;
 #pragma unroll
       for (int j = 0; j < W; j += 8)
         if (j < left) {
           store8(gu + j, v + j);
-          store8(gu + p.N + j, w + j);
+          store8(gu + c.N + j, w + j);
         }
     }
     if (p.act == kActSilu) {
@@ -258,17 +325,17 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n,
     }
 #pragma unroll
     for (int j = 0; j < W; j += 16)
-      if (j < left) store16(out + (size_t)m * p.N + n + j, v + j, left - j);
+      if (j < left) store16(out + (size_t)m * c.N + n + j, v + j, left - j);
   } else {
-    X* dg = out + (size_t)m * 2 * p.N + n;
-    X* hh = reinterpret_cast<X*>(p.out_h) + (size_t)m * p.N + n;
-    const float* gu = p.gateup + (size_t)m * 2 * p.N + n;
+    X* dg = out + (size_t)m * 2 * c.N + n;
+    X* hh = reinterpret_cast<X*>(p.out_h) + (size_t)m * c.N + n;
+    const float* gu = p.gateup + (size_t)m * 2 * c.N + n;
     float g[W / 8][8], u[W / 8][8];
 #pragma unroll
     for (int j = 0; j < W; j += 8)
       if (j < left) {
         load8(g[j / 8], gu + j);
-        load8(u[j / 8], gu + p.N + j);
+        load8(u[j / 8], gu + c.N + j);
       }
     auto grad = [&](auto tag) {  // g, u, dh -> dg, du, h in place
 #pragma unroll
@@ -288,7 +355,7 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n,
     for (int j = 0; j < W; j += 16)
       if (j < left) {
         store16(dg + j, &g[j / 8][0], left - j);
-        store16(dg + p.N + j, &u[j / 8][0], left - j);
+        store16(dg + c.N + j, &u[j / 8][0], left - j);
         store16(hh + j, v + j, left - j);
       }
   }
@@ -297,6 +364,7 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, int m, int n,
 template <typename X, int MODE, int BN, bool PAIR>
 __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __grid_constant__ DenseGemmParams p) {
   using C = DenseCfg<BN, PAIR>;
+  constexpr bool kMany = MODE == kDenseProducts;
   extern __shared__ uint8_t dense_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dense_smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages], accf_bar[2], acce_bar[2], drain_bar;
@@ -315,8 +383,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     }
     mbar_init(&drain_bar, 1);
     fence_mbar_init();
-    tma_prefetch_desc(&p.tm_a);
-    tma_prefetch_desc(&p.tm_b);
+    for (int i = 0; i < (kMany ? p.group : 1); ++i) {
+      tma_prefetch_desc(&p.g[i].tm_a);
+      tma_prefetch_desc(&p.g[i].tm_b);
+    }
   }
   if (warp == 1) tmem_alloc_g<PAIR>(&tmem_slot, C::kTmemCols);
   tc_fence_before();
@@ -330,8 +400,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   pdl_wait();
   pdl_launch_dependents();
 
-  const int units = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
-  const int first = blockIdx.x / C::kCtas, step = gridDim.x / C::kCtas;
+  Units<kMany> it(p, blockIdx.x / C::kCtas, gridDim.x / C::kCtas);
 
   if (warp == 0 || warp == 2 + kEpiWarps) {
     // ------------------------------------------------------------ TMA producers
@@ -346,8 +415,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int u = first; u < units && ok; u += step) {
-      const Unit w = map_unit(p, u);
+    for (; it.on() && ok; it.next()) {
+      const Unit w = it.get();
+      const DenseProblem& g = p.g[kMany ? w.g : 0];
       const int m0 = w.m * C::kTileM + (int)rank * 128, nt = w.n;
       for (int k0 = w.k0; k0 < w.k1; k0 += C::kGroups) {
         if (!wait_warp(&empty_bar[s], phase ^ 1, p.wait_ns)) {
@@ -364,22 +434,22 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
           const int k = (k0 + j) * 64;
           const uint32_t dst = base + (s * C::kGroups + j) * C::kGroupBytes;
           if (!of_b) {
-            if (p.a_mn) {
+            if (g.a_mn) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) tma_load_2d<PAIR>(dst + c * 8192, &p.tm_a, bar, m0 + 64 * c, k);
+              for (int c = 0; c < 2; ++c) tma_load_2d<PAIR>(dst + c * 8192, &g.tm_a, bar, m0 + 64 * c, k);
             } else {
-              tma_load_2d<PAIR>(dst, &p.tm_a, bar, k, m0);
+              tma_load_2d<PAIR>(dst, &g.tm_a, bar, k, m0);
             }
-          } else if (p.b_mn) {
+          } else if (g.b_mn) {
             const int n0 = nt * bn + (int)rank * b_cols;
-            for (int c = 0; c < b_cols / 64; ++c) tma_load_2d<PAIR>(dst + c * 8192, &p.tm_b, bar, n0 + 64 * c, k);
+            for (int c = 0; c < b_cols / 64; ++c) tma_load_2d<PAIR>(dst + c * 8192, &g.tm_b, bar, n0 + 64 * c, k);
           } else {
             // gate then up features; or this block's columns in one box
 #pragma unroll
             for (int c = 0; c < (MODE == kDenseGateUp ? 2 / C::kCtas : 1); ++c) {
               const int row =
-                  MODE == kDenseGateUp ? (PAIR ? (int)rank : c) * p.N + nt * (bn / 2) : nt * bn + (int)rank * b_cols;
-              tma_load_2d<PAIR>(dst + c * (bn / 2) * 128, &p.tm_b, bar, k, row);
+                  MODE == kDenseGateUp ? (PAIR ? (int)rank : c) * g.N + nt * (bn / 2) : nt * bn + (int)rank * b_cols;
+              tma_load_2d<PAIR>(dst + c * (bn / 2) * 128, &g.tm_b, bar, k, row);
             }
           }
         }
@@ -394,19 +464,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     // (the whole warp, in step)
     if (rank == 0) {
       constexpr uint32_t kFmt = std::is_same<X, __half>::value ? 0u : 1u;  // operand format: f16 0, bf16 1
-      const uint32_t idesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
-                             ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(C::kTileM >> 4) << 24);
-      // K major: rows of 128 bytes in groups of 8 (1024 bytes), 32 bytes per K = 16 step.
-      // MN major: 64 K rows of 128 bytes (64 values) per 8192-byte chunk, 8 K rows per
-      // 1024 bytes, 2048 bytes per K = 16 step.
-      const uint32_t a_step = p.a_mn ? 128 : 2, b_step = p.b_mn ? 128 : 2;  // in 16 bytes
-      const uint64_t a_desc = smem_desc(smem_u32(smem), p.a_mn ? 8192 : 16, 1024, 2);
-      const uint64_t b_desc = smem_desc(smem_u32(smem) + C::kABytes, p.b_mn ? 8192 : 16, 1024, 2);
       int s = 0, i = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = first; u < units && ok; u += step, ++i) {
-        const Unit w = map_unit(p, u);
+      for (; it.on() && ok; it.next(), ++i) {
+        const Unit w = it.get();
+        const DenseProblem& g = p.g[kMany ? w.g : 0];
+        const uint32_t idesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)g.a_mn << 15) | ((uint32_t)g.b_mn << 16) |
+                               ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(C::kTileM >> 4) << 24);
+        // K major: rows of 128 bytes in groups of 8 (1024 bytes), 32 bytes per K = 16 step.
+        // MN major: 64 K rows of 128 bytes (64 values) per 8192-byte chunk, 8 K rows per
+        // 1024 bytes, 2048 bytes per K = 16 step.
+        const uint32_t a_step = g.a_mn ? 128 : 2, b_step = g.b_mn ? 128 : 2;  // in 16 bytes
+        const uint64_t a_desc = smem_desc(smem_u32(smem), g.a_mn ? 8192 : 16, 1024, 2);
+        const uint64_t b_desc = smem_desc(smem_u32(smem) + C::kABytes, g.b_mn ? 8192 : 16, 1024, 2);
         const int b = i & 1;
         const bool free = PAIR ? __all_sync(0xffffffffu, mbar_wait_cluster_step(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns))
                                : wait_warp(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
@@ -449,8 +520,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lane quarter; which 32-column chunks
     int i = 0;
-    for (int u = first; u < units; u += step, ++i) {
-      const Unit t = map_unit(p, u);
+    for (; it.on(); it.next(), ++i) {
+      const Unit t = it.get();
+      const DenseProblem& g = p.g[kMany ? t.g : 0];
       const int b = i & 1;
       if (!mbar_wait_step(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
@@ -460,8 +532,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * BN;
       const int r = (int)rank * 128 + q * 32 + lane, m = t.m * C::kTileM + r;  // row in the tile, in the matrix
-      const bool live = m < p.M;
-      if (t.slot >= 0 && p.splits > 1) {
+      const bool live = m < g.M;
+      if (!kMany && t.slot >= 0 && p.splits > 1) {
         // a K slice's sums as they are: [slot][row of the tile][bn]
         float* part = p.partial + ((size_t)t.slot * C::kTileM + r) * bn;
 #pragma unroll 1
@@ -483,8 +555,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
           tmem_ld_32x32b_x32(acc + c, v);
           if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + bn / 2 + c, w);
           tmem_wait_ld();
-          const int n = t.n * cols + c, left = min(p.N - n, cols - c);  // a multiple of 8
-          if (live) epilogue<X, MODE, 32>(p, m, n, left, v, w);
+          const int n = t.n * cols + c, left = min(g.N - n, cols - c);  // a multiple of 8
+          if (live) epilogue<X, MODE, 32>(p, g, m, n, left, v, w);
           __syncwarp();
         }
       }
@@ -527,10 +599,11 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__
   const long long i = blockIdx.x * 256LL + threadIdx.x;
   const int c = (int)(i % per_row) * 16;
   const int r = (int)(i / per_row % tile_rows), tile = (int)(i / per_row / tile_rows);
-  if (p.full + tile >= p.tiles_m * p.tiles_n) return;
+  const DenseProblem& g = p.g[0];
+  if (p.full + tile >= g.tiles_m * g.tiles_n) return;
   const Unit t = map_unit(p, p.full + tile * p.splits);
   const int m = t.m * tile_rows + r, n = t.n * cols + c;
-  if (m >= p.M || n >= p.N) return;
+  if (m >= g.M || n >= g.N) return;
   float v[16], w[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = w[j] = 0.f;
@@ -549,7 +622,7 @@ __global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__
       }
     }
   }
-  epilogue<X, MODE, 16>(p, m, n, p.N - n, v, w);
+  epilogue<X, MODE, 16>(p, g, m, n, g.N - n, v, w);
 }
 
 // ------------------------------------------------------------------ host side
@@ -557,6 +630,7 @@ struct Shape {
   int bn;
   bool pair;
   int tiles_m, tiles_n, full, splits;
+  float time;  // estimated cycles
 };
 
 // Tile shape and split by estimated time, in cycles.  A unit's K group (64 values) takes
@@ -598,6 +672,7 @@ Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
       if (best_time == 0.f || time < best_time) {
         best_time = time;
         best = s;
+        best.time = time;
       }
     }
   }
@@ -677,7 +752,7 @@ cudaError_t resident_blocks(Kern kern, int smem, bool pair, std::atomic<int> (&c
 }
 
 template <typename X, int MODE, int BN, bool PAIR>
-cudaError_t launch_kernel(const DenseGemmParams& p, cudaStream_t stream) {
+cudaError_t launch_kernel(const DenseGemmParams& p, long long units, cudaStream_t stream) {
   using C = DenseCfg<BN, PAIR>;
   auto kern = dense_gemm_kernel<X, MODE, BN, PAIR>;
   static SmemOptIn opt_in;
@@ -687,8 +762,7 @@ cudaError_t launch_kernel(const DenseGemmParams& p, cudaStream_t stream) {
   int blocks = 0;
   e = resident_blocks(kern, C::kSmemBytes, PAIR, cached, &blocks);
   if (e != cudaSuccess) return e;
-  const long long need = (p.full + (long long)(p.tiles_m * p.tiles_n - p.full) * p.splits) * C::kCtas;
-  if (need < blocks) blocks = (int)need;
+  if (units * C::kCtas < blocks) blocks = (int)units * C::kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kDenseThreads);
@@ -706,9 +780,10 @@ cudaError_t launch_kernel(const DenseGemmParams& p, cudaStream_t stream) {
 
 template <typename X, int MODE>
 cudaError_t launch_mode(const DenseGemmParams& p, const Shape& s, cudaStream_t stream) {
-  const cudaError_t e = s.pair         ? launch_kernel<X, MODE, 256, true>(p, stream)
-                        : s.bn == 128 ? launch_kernel<X, MODE, 128, false>(p, stream)
-                                      : launch_kernel<X, MODE, 64, false>(p, stream);
+  const long long units = s.full + (long long)(s.tiles_m * s.tiles_n - s.full) * s.splits;
+  const cudaError_t e = s.pair         ? launch_kernel<X, MODE, 256, true>(p, units, stream)
+                        : s.bn == 128 ? launch_kernel<X, MODE, 128, false>(p, units, stream)
+                                      : launch_kernel<X, MODE, 64, false>(p, units, stream);
   if (e != cudaSuccess || s.splits == 1) return e;
   const int tile_rows = s.pair ? 256 : 128;
   const long long threads =
@@ -732,22 +807,76 @@ size_t dense_partial_bytes(int M, int N, int K, int mode, bool b_mn) {
   return (size_t)(s.tiles_m * s.tiles_n - s.full) * s.splits * (s.pair ? 256 : 128) * s.bn * sizeof(float);
 }
 
+// A product's operands and tiles into its place.
+bool set_problem(DenseProblem& g, const DenseOperand& a, const DenseOperand& b, int b_box, int tiles_m, int tiles_n,
+                 int dtype) {
+  g.a_mn = a.mn_major;
+  g.b_mn = b.mn_major;
+  g.tiles_m = tiles_m;
+  g.tiles_n = tiles_n;
+  g.kgroups = ceil_div(g.K, 64);
+  return operand_map(&g.tm_a, a, a.mn_major ? 64 : 128, dtype) && operand_map(&g.tm_b, b, b.mn_major ? 64 : b_box, dtype);
+}
+
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream) {
-  const Shape s = pick_shape(p.M, p.N, p.K, mode, b.mn_major);
-  p.a_mn = a.mn_major;
-  p.b_mn = b.mn_major;
+  DenseProblem& g = p.g[0];
+  const Shape s = pick_shape(g.M, g.N, g.K, mode, b.mn_major);
   p.bn = s.bn;
-  p.tiles_m = s.tiles_m;
-  p.tiles_n = s.tiles_n;
   p.full = s.full;
   p.splits = s.splits;
-  p.kgroups = ceil_div(p.K, 64);
   p.wait_ns = gemm_wait_limit_ns();
-  if (!operand_map(&p.tm_a, a, a.mn_major ? 64 : 128, dtype)) return MOE_ERR_CUDA;
-  if (!operand_map(&p.tm_b, b, b.mn_major ? 64 : s.pair || mode == kDenseGateUp ? s.bn / 2 : s.bn, dtype)) return MOE_ERR_CUDA;
+  if (!set_problem(g, a, b, s.pair || mode == kDenseGateUp ? s.bn / 2 : s.bn, s.tiles_m, s.tiles_n, dtype))
+    return MOE_ERR_CUDA;
   const cudaError_t e = dtype == kDtypeF16 ? launch_type<__half>(p, s, mode, stream)
                                            : launch_type<__nv_bfloat16>(p, s, mode, stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const DenseOperand* b, int dtype,
+                          cudaStream_t stream) {
+  // the class of the larger K first
+  int order[kDenseGroup] = {0, 1, 2};
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && p.g[order[j]].K > p.g[order[j - 1]].K; --j) std::swap(order[j], order[j - 1]);
+  DenseGemmParams q = p;
+  q.group = n;
+  q.long_n = 0;
+  q.bn = 256;
+  q.splits = 1;
+  q.wait_ns = gemm_wait_limit_ns();
+  const int workers = device_sms() / 2;
+  long long tiles[2] = {0, 0};  // of the long and of the short class
+  float apart = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const DenseProblem& g = p.g[order[i]];
+    const bool is_long = g.K == p.g[order[0]].K;
+    q.long_n += is_long;
+    tiles[is_long ? 0 : 1] += (long long)ceil_div(g.M, 256) * ceil_div(g.N, 256);
+    apart += pick_shape(g.M, g.N, g.K, kDenseStore, b[order[i]].mn_major).time;
+  }
+  // estimated as in pick_shape; every launch has a start and an end of about 5000 cycles
+  const float len[2] = {ceil_div(p.g[order[0]].K, 64) * 540.f, ceil_div(p.g[order[n - 1]].K, 64) * 540.f};
+  q.lead = q.long_n < n ? (int)(len[0] / len[1] + 0.5f) : 0;
+  const float work = (float)tiles[0] * len[0] + (q.long_n < n ? (float)tiles[1] * len[1] : 0.f);
+  const float together = work / (float)workers + 0.5f * len[q.long_n < n ? 1 : 0] + 1000.f;
+  if (n < 2 || together > apart + 5000.f * (float)(n - 1)) {
+    for (int i = 0; i < n; ++i) {
+      DenseGemmParams one = p;
+      one.g[0] = p.g[i];
+      const int st = launch_dense_gemm(one, a[i], b[i], kDenseStore, dtype, stream);
+      if (st != MOE_OK) return st;
+    }
+    return MOE_OK;
+  }
+  for (int i = 0; i < n; ++i) {
+    q.g[i] = p.g[order[i]];
+    if (!set_problem(q.g[i], a[order[i]], b[order[i]], 128, ceil_div(q.g[i].M, 256), ceil_div(q.g[i].N, 256), dtype))
+      return MOE_ERR_CUDA;
+  }
+  const cudaError_t e = dtype == kDtypeF16
+                            ? launch_kernel<__half, kDenseProducts, 256, true>(q, tiles[0] + tiles[1], stream)
+                            : launch_kernel<__nv_bfloat16, kDenseProducts, 256, true>(q, tiles[0] + tiles[1], stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
