@@ -109,7 +109,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 #undef MOE_ELECTED
 // A bounded wait of a whole warp, in step; the answer is the same in every lane.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  const bool ok = mbar_wait_step(bar, parity, limit_ns);
+  const bool ok = mbar_wait_bounded(bar, parity, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
         const uint64_t a_desc = smem_desc(smem_u32(smem), g.a_mn ? 8192 : 16, 1024, 2);
         const uint64_t b_desc = smem_desc(smem_u32(smem) + C::kABytes, g.b_mn ? 8192 : 16, 1024, 2);
         const int b = i & 1;
-        const bool free = PAIR ? __all_sync(0xffffffffu, mbar_wait_cluster_step(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns))
+        const bool free = PAIR ? __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns))
                                : wait_warp(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
         if (!free) {
           if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutMain);
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       const Unit t = it.get();
       const DenseProblem& g = p.g[kMany ? t.g : 0];
       const int b = i & 1;
-      if (!mbar_wait_step(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
+      if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
         break;
       }

@@ -104,18 +104,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
-// mbar_wait_bounded for waits that are a step of a pipeline: the global timer is read only
-// after four suspended polls, for reading it takes longer than such a wait usually does.
-__device__ __forceinline__ bool mbar_wait_step(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  if (limit_ns >= 2000ull) {
-    if (mbar_try_wait(bar, parity)) return true;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i)
-      if (mbar_try_wait_suspend(bar, parity, limit_ns < 20000ull ? (uint32_t)limit_ns : 20000u)) return true;
-  }
-  return mbar_wait_bounded(bar, parity, limit_ns);
-}
-
 // ------------------------------------------------------------------ cluster
 // Split cluster barrier: arrive (release) early, wait (acquire) just before the
 // first access to a peer's shared memory.  Every thread of every CTA calls both once.
@@ -173,14 +161,6 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_
     if (mbar_try_wait_cluster(bar, parity)) return true;
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
-}
-
-// The same with the timer read late, as in mbar_wait_step.
-__device__ __forceinline__ bool mbar_wait_cluster_step(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i)
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-  return mbar_wait_cluster_bounded(bar, parity, limit_ns);
 }
 
 // ------------------------------------------------------------------ dependent launch
