@@ -129,6 +129,7 @@ double number(PyObject* o) {
 int integer(PyObject* o) {
   const long v = PyLong_AsLong(o);
   if (v == -1 && PyErr_Occurred()) throw Raised{};
+  if (v < INT32_MIN || v > INT32_MAX) value_error("an integer beyond 32 bits");
   return static_cast<int>(v);
 }
 bool arguments(Py_ssize_t got, Py_ssize_t want) {
