@@ -144,7 +144,7 @@ __device__ __forceinline__ void store_sector(void* p, const Sector& s) {
                "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
                : "memory");
 }
-__device__ __forceinline__ void load_sector(float (&f)[8], const float* p) {
+__device__ __forceinline__ void load_sector(float* f, const float* p) {
   asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
                : "l"(p));
@@ -175,13 +175,16 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
-__device__ __forceinline__ void load8(float (&f)[8], const float* p) {
+__device__ __forceinline__ void load8(float* f, const float* p) {
   if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
     load_sector(f, p);
   } else {
     Vec8<float> t;
     t.load(p, 0);
-    t.get(f);
+    float v[8];
+    t.get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v[i];
   }
 }
 
@@ -296,6 +299,47 @@ struct Units {
   }
 };
 
+// g and u of W columns of a row.
+template <int W>
+__device__ __forceinline__ void load_gateup(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left,
+                                            float (&g)[W], float (&u)[W]) {
+  const float* gu = p.gateup + (size_t)m * 2 * c.N + n;
+#pragma unroll
+  for (int j = 0; j < W; j += 8)
+    if (j < left) {
+      load8(&g[j], gu + j);
+      load8(&u[j], gu + c.N + j);
+    }
+}
+// dh, g, u -> dg, du, h.
+template <typename X, int W>
+__device__ __forceinline__ void epilogue_grad(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left,
+                                              float (&v)[W], float (&g)[W], float (&u)[W]) {
+  X* dg = reinterpret_cast<X*>(c.out) + (size_t)m * 2 * c.N + n;
+  X* hh = reinterpret_cast<X*>(p.out_h) + (size_t)m * c.N + n;
+  auto grad = [&](auto tag) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      float slope;
+      const float gj = g[j], uj = u[j], a = act_f<decltype(tag)::value>(gj, slope);
+      g[j] = v[j] * uj * slope;
+      u[j] = v[j] * a;
+      v[j] = a * uj;
+    }
+  };
+  if (p.act == kActSilu)
+    grad(std::integral_constant<int, kActSilu>{});
+  else
+    grad(std::integral_constant<int, kActGelu>{});
+#pragma unroll
+  for (int j = 0; j < W; j += 16)
+    if (j < left) {
+      store16(dg + j, &g[j], left - j);
+      store16(dg + c.N + j, &u[j], left - j);
+      store16(hh + j, v + j, left - j);
+    }
+}
+
 // What happens to the sums of W columns of a row (`left` of them inside the matrix, in
 // eights): v, and for gate/up w the up sums.
 template <typename X, int MODE, int W>
@@ -327,37 +371,9 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, const DensePr
     for (int j = 0; j < W; j += 16)
       if (j < left) store16(out + (size_t)m * c.N + n + j, v + j, left - j);
   } else {
-    X* dg = out + (size_t)m * 2 * c.N + n;
-    X* hh = reinterpret_cast<X*>(p.out_h) + (size_t)m * c.N + n;
-    const float* gu = p.gateup + (size_t)m * 2 * c.N + n;
-    float g[W / 8][8], u[W / 8][8];
-#pragma unroll
-    for (int j = 0; j < W; j += 8)
-      if (j < left) {
-        load8(g[j / 8], gu + j);
-        load8(u[j / 8], gu + c.N + j);
-      }
-    auto grad = [&](auto tag) {  // g, u, dh -> dg, du, h in place
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        float slope;
-        const float gj = g[j / 8][j % 8], uj = u[j / 8][j % 8], a = act_f<decltype(tag)::value>(gj, slope);
-        g[j / 8][j % 8] = v[j] * uj * slope;
-        u[j / 8][j % 8] = v[j] * a;
-        v[j] = a * uj;
-      }
-    };
-    if (p.act == kActSilu)
-      grad(std::integral_constant<int, kActSilu>{});
-    else
-      grad(std::integral_constant<int, kActGelu>{});
-#pragma unroll
-    for (int j = 0; j < W; j += 16)
-      if (j < left) {
-        store16(dg + j, &g[j / 8][0], left - j);
-        store16(dg + c.N + j, &u[j / 8][0], left - j);
-        store16(hh + j, v + j, left - j);
-      }
+    float g[W], u[W];
+    load_gateup(p, c, m, n, left, g, u);
+    epilogue_grad<X>(p, c, m, n, left, v, g, u);
   }
 }
 
@@ -524,6 +540,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       const Unit t = it.get();
       const DenseProblem& g = p.g[kMany ? t.g : 0];
       const int b = i & 1;
+      const int r = (int)rank * 128 + q * 32 + lane, m = t.m * C::kTileM + r;  // row in the tile, in the matrix
+      const bool live = m < g.M;
+      // the first g, u come in while the MMAs run
+      const int cols = MODE == kDenseGateUp ? bn / 2 : bn;
+      constexpr bool kGrad = MODE == kDenseGateUpGrad;
+      float fg[kGrad ? 16 : 1], fu[kGrad ? 16 : 1];
+      if constexpr (kGrad)
+        if (live && t.slot < 0) load_gateup(p, g, m, t.n * cols + 16 * half, min(g.N - t.n * cols, cols) - 16 * half, fg, fu);
       if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
         break;
@@ -531,8 +555,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       __syncwarp();
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * BN;
-      const int r = (int)rank * 128 + q * 32 + lane, m = t.m * C::kTileM + r;  // row in the tile, in the matrix
-      const bool live = m < g.M;
       if (!kMany && t.slot >= 0 && p.splits > 1) {
         // a K slice's sums as they are: [slot][row of the tile][bn]
         float* part = p.partial + ((size_t)t.slot * C::kTileM + r) * bn;
@@ -547,8 +569,27 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
           }
           __syncwarp();  // the next tensor-memory load is the whole warp's
         }
+      } else if constexpr (kGrad) {
+        // 16 columns at a time, the next ones' g, u on their way meanwhile
+        const int n0 = t.n * cols, end = min(g.N - n0, cols);
+#pragma unroll 2
+        for (int c = 16 * half; c < cols; c += 32) {
+          float v[16], ng[16], nu[16];
+          uint32_t raw[16];
+          if (live) load_gateup(p, g, m, n0 + c + 32, end - c - 32, ng, nu);
+          tmem_ld_32x32b_x16(acc + c, raw);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
+          if (live && c < end) epilogue_grad<X>(p, g, m, n0 + c, end - c, v, fg, fu);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            fg[j] = ng[j];
+            fu[j] = nu[j];
+          }
+          __syncwarp();
+        }
       } else {
-        const int cols = MODE == kDenseGateUp ? bn / 2 : bn;
 #pragma unroll 1
         for (int c = 32 * half; c < cols; c += 64) {
           float v[32], w[32];
