@@ -29,6 +29,7 @@ using namespace ptx;
 
 namespace {
 
+constexpr int kAhead = 2;                       // 16-column steps that the derivative's g, u come in ahead
 constexpr int kEpiWarps = 8;                    // two per tensor-memory lane quarter
 constexpr int kDenseThreads = 96 + 32 * kEpiWarps;
 constexpr uint64_t kDrainLimit = 1000000000ull;  // ns for MMAs already issued (1 s)
@@ -545,9 +546,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       // the first g, u come in while the MMAs run
       const int cols = MODE == kDenseGateUp ? bn / 2 : bn;
       constexpr bool kGrad = MODE == kDenseGateUpGrad;
-      float fg[kGrad ? 16 : 1], fu[kGrad ? 16 : 1];
+      const int n0 = t.n * cols, end = min(g.N - n0, cols);
+      float gs[kGrad ? kAhead + 1 : 1][16], us[kGrad ? kAhead + 1 : 1][16];
       if constexpr (kGrad)
-        if (live && t.slot < 0) load_gateup(p, g, m, t.n * cols + 16 * half, min(g.N - t.n * cols, cols) - 16 * half, fg, fu);
+        if (live && t.slot < 0) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) load_gateup(p, g, m, n0 + 16 * half + 32 * j, end - 16 * half - 32 * j, gs[j], us[j]);
+        }
       if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
         break;
@@ -570,25 +575,25 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
           __syncwarp();  // the next tensor-memory load is the whole warp's
         }
       } else if constexpr (kGrad) {
-        // 16 columns at a time, the next ones' g, u on their way meanwhile
-        const int n0 = t.n * cols, end = min(g.N - n0, cols);
-#pragma unroll 2
-        for (int c = 16 * half; c < cols; c += 32) {
-          float v[16], ng[16], nu[16];
-          uint32_t raw[16];
-          if (live) load_gateup(p, g, m, n0 + c + 32, end - c - 32, ng, nu);
-          tmem_ld_32x32b_x16(acc + c, raw);
-          tmem_wait_ld();
+        // 16 columns at a time, the g, u of the next kAhead times on their way meanwhile
+#pragma unroll 1
+        for (int c0 = 16 * half; c0 < cols; c0 += 32 * (kAhead + 1))
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(raw[j]);
-          if (live && c < end) epilogue_grad<X>(p, g, m, n0 + c, end - c, v, fg, fu);
+          for (int j = 0; j <= kAhead; ++j) {
+            const int c = c0 + 32 * j;
+            if (c >= cols) break;
+            constexpr int kAll = kAhead + 1;
+            const int next = c + 32 * kAhead;
+            if (live) load_gateup(p, g, m, n0 + next, end - next, gs[(j + kAhead) % kAll], us[(j + kAhead) % kAll]);
+            uint32_t raw[16];
+            float v[16];
+            tmem_ld_32x32b_x16(acc + c, raw);
+            tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            fg[j] = ng[j];
-            fu[j] = nu[j];
+            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(raw[k]);
+            if (live && c < end) epilogue_grad<X>(p, g, m, n0 + c, end - c, v, gs[j], us[j]);
+            __syncwarp();
           }
-          __syncwarp();
-        }
       } else {
 #pragma unroll 1
         for (int c = 32 * half; c < cols; c += 64) {
@@ -596,8 +601,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
           tmem_ld_32x32b_x32(acc + c, v);
           if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + bn / 2 + c, w);
           tmem_wait_ld();
-          const int n = t.n * cols + c, left = min(g.N - n, cols - c);  // a multiple of 8
-          if (live) epilogue<X, MODE, 32>(p, g, m, n, left, v, w);
+          if (live) epilogue<X, MODE, 32>(p, g, m, n0 + c, end - c, v, w);  // end - c: a multiple of 8
           __syncwarp();
         }
       }
