@@ -167,6 +167,10 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float (&v)
 // fragments that the others write into its shared memory, added in rank order.  (K split
 // between the warps of a block, with a copy per slice and stage, measured slower: one token
 // x 131072 x 4096 67.8 us against 53.2.)
+// What bounds it: over many rows HBM and the ALU pipe nearly alike (that product: 5.36 TB/s
+// of a copy's 6.7, the ALU pipe 0.59 busy with the codes' conversions, the last of 2.25
+// rounds a quarter full); at 16 tokens the instructions (gated 14336 x 4096: 21.6 us, of
+// them about 3 for packing x); below 10 MB the launch (2880 x 2880: 5.1 us).
 constexpr int kUnitBytes = kMatvecUnitBytes;
 constexpr int kGroupBytes = kMatvecGroup * kUnitBytes;  // one K unit of eight tiles
 constexpr uint64_t kMatvecWaitNs = 1000000000ull;       // a wait may take 1 s
@@ -527,7 +531,8 @@ __global__ void matvec_prepare_kernel(MatvecPrepareParams p) {
 // SM have 128 KB in flight.  Two or four tiles per block, which share the x fragments,
 // measured slower at every size (16 tokens, 4096 x 14336: 71 and 76 us against 70; one
 // token 57 and 70 against 55, 0.96 of the measured copy rate), and so did three and four
-// blocks per SM with fewer units each.
+// blocks per SM with fewer units each.  Bound by HBM; at 2880 x 2880, where the two launches
+// take 13.0 us for 50 MB, by their starts and by 1.2 and 0.6 rounds of blocks.
 template <typename X, int NT, bool GATED, int ACT>
 __global__ void __launch_bounds__(kThinThreads, 2) thin16_kernel(const __grid_constant__ ThinParams p) {
   constexpr int kUnits = 8;
