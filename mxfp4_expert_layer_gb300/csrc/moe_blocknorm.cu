@@ -561,11 +561,16 @@ __global__ void __launch_bounds__(256) block_norm_reduce_kernel(const float* par
   float* out = outs[blockIdx.y];
   if (!out) return;
   const int c = blockIdx.x * 32 + tx;
-  float v = 0.f;
-  if (c < H) {
-#pragma unroll 8
-    for (int r = ty; r < rows; r += 8) v += __ldcg(partial + ((size_t)r * 3 + blockIdx.y) * H + c);
+  // every load at once: a few in turn would each wait for L2
+  constexpr int kEach = (kNormBlocks + 7) / 8;
+  float part[kEach], v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = ty + 8 * i;
+    part[i] = r < rows && c < H ? __ldcg(partial + ((size_t)r * 3 + blockIdx.y) * H + c) : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) v += part[i];
   buf[ty][tx] = v;
   __syncthreads();
   if (ty == 0 && c < H) {
