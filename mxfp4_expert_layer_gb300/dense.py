@@ -76,8 +76,8 @@ def block_norm_backward(d_residual_out: Optional[torch.Tensor], d_out: Optional[
     """Every gradient of block_norm (moe_block_norm_backward).  ``residual_out`` is the s
     that the forward returned; ``d_residual_out`` and ``d_out`` the gradients of its two
     results (None for one that nothing read); ``has_residual`` False: no residual was added."""
-    return BlockNormGrads(*_ext.block_norm_backward(d_residual_out, d_out, block, residual_out, norm_weight, gate,
-                                                    residual_scale, next_weight, eps, has_residual))
+    return BlockNormGrads._make(_ext.block_norm_backward(d_residual_out, d_out, block, residual_out, norm_weight, gate,
+                                                         residual_scale, next_weight, eps, has_residual))
 
 
 # ------------------------------------------------------------------ gated feed-forward block
@@ -103,7 +103,7 @@ def ffn_backward(d_out: torch.Tensor, x: torch.Tensor, gateup: torch.Tensor, w_g
                  need_weights: bool = True) -> FfnGrads:
     """The gradients of ffn_forward (moe_ffn_backward) from its inputs, the ``gateup`` it
     saved and ``act`` as given there; all of x's type."""
-    return FfnGrads(*_ext.ffn_backward(d_out, x, gateup, w_gateup, w_down, act, need_x, need_weights))
+    return FfnGrads._make(_ext.ffn_backward(d_out, x, gateup, w_gateup, w_down, act, need_x, need_weights))
 
 
 def dense_status() -> int:
