@@ -232,7 +232,7 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8]) {
 // arguments alone would be a third of a row's instructions.  Bound by HBM over many rows
 // (8192 x 4096 bf16, f32 stream, with the reduction below: 101 us, 6.0 TB/s of a copy's 6.7),
 // by the latency of two launches and of a block's rows in turn over few (333 x 2880 f16,
-// full gate: 9.9 us).
+// full gate: 8.7 us).
 template <typename A, typename S, int VPT, int GATE>
 __global__ void __launch_bounds__(512)
     block_norm_backward_kernel(const __grid_constant__ BlockNormBackwardParams q, const __grid_constant__ RowCopies rows) {

@@ -32,7 +32,9 @@ namespace {
 // 16-column steps that the derivative epilogue's g, u come in ahead (forward and backward of
 // 2048 tokens x 2880 x 2880: 250 us with one, 242 with two, 276 with three)
 constexpr int kAhead = 2;
-constexpr int kEpiWarps = 8;                    // two per tensor-memory lane quarter
+// kParts epilogue warps per tensor-memory lane quarter (three and four measured no faster:
+// what bounds an epilogue is its rows' separate sectors, not its instructions)
+constexpr int kEpiWarps = 8, kParts = kEpiWarps / 4;
 constexpr int kDenseThreads = 96 + 32 * kEpiWarps;
 constexpr uint64_t kDrainLimit = 1000000000ull;  // ns for MMAs already issued (1 s)
 constexpr uint64_t kLandingNs = 20000000ull;     // ns after a time-out in which every issued copy has landed (20 ms)
@@ -123,18 +125,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, float (&f)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+// The values of a tensor-memory load, once it has been waited for: the registers pass through
+// an empty statement behind the wait, so that no use of them can move ahead of it.
+__device__ __forceinline__ void landed(uint32_t (&r)[16], float (&f)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 #pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
 // A whole 32-byte sector per thread: with 16-byte accesses of a thread per row, every
@@ -537,7 +534,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lane quarter; which 32-column chunks
+    const int q = warp & 3, part0 = 16 * ((warp - 2) >> 2);  // tensor-memory lane quarter; its first columns
     int i = 0;
     for (; it.on(); it.next(), ++i) {
       const Unit t = it.get();
@@ -548,12 +545,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       // the first g, u come in while the MMAs run
       const int cols = MODE == kDenseGateUp ? bn / 2 : bn;
       constexpr bool kGrad = MODE == kDenseGateUpGrad;
+      constexpr int kStep = 16 * kParts;  // a warp takes 16 columns of every kStep
       const int n0 = t.n * cols, end = min(g.N - n0, cols);
       float gs[kGrad ? kAhead + 1 : 1][16], us[kGrad ? kAhead + 1 : 1][16];
       if constexpr (kGrad)
         if (live && t.slot < 0) {
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) load_gateup(p, g, m, n0 + 16 * half + 32 * j, end - 16 * half - 32 * j, gs[j], us[j]);
+          for (int j = 0; j < kAhead; ++j) {
+            const int c = part0 + kStep * j;
+            load_gateup(p, g, m, n0 + c, end - c, gs[j], us[j]);
+          }
         }
       if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
@@ -566,44 +567,48 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
         // a K slice's sums as they are: [slot][row of the tile][bn]
         float* part = p.partial + ((size_t)t.slot * C::kTileM + r) * bn;
 #pragma unroll 1
-        for (int c = 32 * half; c < bn; c += 64) {
-          float v[32];
-          tmem_ld_32x32b_x32(acc + c, v);
+        for (int c = part0; c < bn; c += kStep) {
+          uint32_t raw[16];
+          float v[16];
+          tmem_ld_32x32b_x16(acc + c, raw);
           tmem_wait_ld();
+          landed(raw, v);
           if (live) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) store8(part + c + j, v + j);
+            for (int j = 0; j < 16; j += 8) store8(part + c + j, v + j);
           }
           __syncwarp();  // the next tensor-memory load is the whole warp's
         }
       } else if constexpr (kGrad) {
         // 16 columns at a time, the g, u of the next kAhead times on their way meanwhile
 #pragma unroll 1
-        for (int c0 = 16 * half; c0 < cols; c0 += 32 * (kAhead + 1))
+        for (int c0 = part0; c0 < cols; c0 += kStep * (kAhead + 1))
 #pragma unroll
           for (int j = 0; j <= kAhead; ++j) {
-            const int c = c0 + 32 * j;
+            const int c = c0 + kStep * j;
             if (c >= cols) break;
             constexpr int kAll = kAhead + 1;
-            const int next = c + 32 * kAhead;
+            const int next = c + kStep * kAhead;
             if (live) load_gateup(p, g, m, n0 + next, end - next, gs[(j + kAhead) % kAll], us[(j + kAhead) % kAll]);
             uint32_t raw[16];
             float v[16];
             tmem_ld_32x32b_x16(acc + c, raw);
             tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(raw[k]);
+            landed(raw, v);
             if (live && c < end) epilogue_grad<X>(p, g, m, n0 + c, end - c, v, gs[j], us[j]);
             __syncwarp();
           }
       } else {
 #pragma unroll 1
-        for (int c = 32 * half; c < cols; c += 64) {
-          float v[32], w[32];
-          tmem_ld_32x32b_x32(acc + c, v);
-          if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x32(acc + bn / 2 + c, w);
+        for (int c = part0; c < cols; c += kStep) {
+          uint32_t raw[16], raw_up[16];
+          float v[16], w[16];
+          tmem_ld_32x32b_x16(acc + c, raw);
+          if constexpr (MODE == kDenseGateUp) tmem_ld_32x32b_x16(acc + bn / 2 + c, raw_up);
           tmem_wait_ld();
-          if (live) epilogue<X, MODE, 32>(p, g, m, n0 + c, end - c, v, w);  // end - c: a multiple of 8
+          landed(raw, v);
+          if constexpr (MODE == kDenseGateUp) landed(raw_up, w);
+          if (live) epilogue<X, MODE, 16>(p, g, m, n0 + c, end - c, v, w);  // end - c: a multiple of 8
           __syncwarp();
         }
       }
@@ -636,8 +641,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   if (warp == 1) tmem_dealloc_g<PAIR>(tmem, C::kTmemCols);
 }
 
-// The split tiles: the slices' sums in slice order, then the epilogue (about 4 us, from L2).  16 columns (of gate
-// and of up) per thread.
+// The split tiles: the slices' sums in slice order, then the epilogue (about 4 us, from L2).
+// 16 columns (of gate and of up) per thread.
 template <typename X, int MODE>
 __global__ void __launch_bounds__(256) dense_join_kernel(const __grid_constant__ DenseGemmParams p, int tile_rows, int bn) {
   pdl_wait();
