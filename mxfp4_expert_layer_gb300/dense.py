@@ -55,7 +55,7 @@ def block_norm(block: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
     block [T, H] bf16 or f16; ``residual`` of the same type or f32 (the type of s);
     ``norm_weight`` None: no norm after the block; ``gate``: None, [H] or [T, H] of
     block's type, or f32 [T, 1].  ``residual_out`` may be ``residual``, ``out`` may be
-    ``block``."""
+    ``block``.  Small results of one type share a storage."""
     return _ext.block_norm(block, residual, norm_weight, gate, residual_scale, next_weight, eps, residual_out, out)
 
 
