@@ -556,11 +556,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
             load_gateup(p, g, m, n0 + c, end - c, gs[j], us[j]);
           }
         }
-      if (!mbar_wait_bounded(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
+      // (one answer for the warp: its lanes leave together, or all go on to the warp's
+      // tensor-memory loads)
+      if (!wait_warp(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
         break;
       }
-      __syncwarp();
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * BN;
       if (!kMany && t.slot >= 0 && p.splits > 1) {
