@@ -111,6 +111,16 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                      smem_u32(bar))
                  : "memory");
 }
+// The same on this block's barrier alone.
+template <bool PAIR>
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(MOE_ELECTED "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+  else
+    commit<false>(bar);
+}
 #undef MOE_ELECTED
 // A bounded wait of a whole warp, in step; the answer is the same in every lane.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -475,6 +485,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
         }
       }
     }
+    // the MMAs' arrivals on the second block's barriers are all there before it leaves
+    if (PAIR && !of_b)
+      for (int i = 0; i < C::kStages && ok; ++i) {
+        ok = wait_warp(&empty_bar[s], phase ^ 1, p.wait_ns);
+        if (++s == C::kStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp, in step)
@@ -528,8 +547,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
         }
         if (ok) commit<PAIR>(&accf_bar[b]);
       }
-      // all tensor-core work is done before the tensor memory is freed
-      commit<PAIR>(&drain_bar);
+      // all tensor-core work is done before the tensor memory is freed (known to this block
+      // alone: nothing would keep the second one until an arrival of its own)
+      commit_own<PAIR>(&drain_bar);
       wait_warp(&drain_bar, 0, kDrainLimit);
     }
   } else {

@@ -57,3 +57,22 @@ def test_no_time_out_goes_unreported(T, H, I, limit):
         for a, b in zip(training_step(m), want):
             assert torch.equal(a, b), ns
         assert pkg.dense_status() == 0
+
+
+@pytest.mark.parametrize("T,H,I", [(129, 8, 8), (300, 8, 264), (513, 264, 8)])
+def test_pairs_that_end_at_once(T, H, I):
+    """Pair tiles of one to five K groups, many launches close behind one another: a pair's
+    blocks leave as soon as their barriers have had every arrival."""
+    import mxfp4_expert_layer_gb300 as pkg
+    m = ffn.make(T, H, I, torch.float16, seed=T)
+    want = training_step(m)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(50):
+            got = training_step(m)
+    for _ in range(4):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert pkg.dense_status() == 0
