@@ -417,7 +417,8 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  * returns) for words that the library holds per GPU: synchronises `stream`, reads them
  * into *status and clears them when set.  A bounded wait that gave up sets a bit (the
  * GEMMs' limit is moe_set_wait_limit_ns, the others' 1 s); results of calls since the
- * last reading are then not reliable.  Not for the hot path.                        */
+ * last reading are then not reliable.  The launch that gave up stays until its copies
+ * have landed (20 ms); others are not held up.  Not for the hot path.                */
 int moe_dense_status(int* status, moe_stream_t stream);
 
 /* moe_prepare_matvec: one-time re-layout of raw MXFP4 weights [rows][K/2] codes and

@@ -127,6 +127,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64
   const bool ok = mbar_wait_bounded(bar, parity, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
+// A wait gave up: in the status word, and for this launch in the block's own flag.
+__device__ __forceinline__ void give_up(volatile uint32_t* late, uint32_t bits) {
+  if ((threadIdx.x & 31) == 0) {
+    report_status(&g_dense_status, bits);
+    *late = 1;
+  }
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -395,6 +405,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dense_smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages], accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t late;  // a wait of this launch gave up, in this block or its peer
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
   const int bn = PAIR ? p.bn : BN;  // columns of a tile
@@ -408,6 +419,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       mbar_init(&acce_bar[b], kEpiWarps * C::kCtas);  // one lane of each epilogue warp
     }
     mbar_init(&drain_bar, 1);
+    late = 0;
     fence_mbar_init();
     for (int i = 0; i < (kMany ? p.group : 1); ++i) {
       tma_prefetch_desc(&p.g[i].tm_a);
@@ -447,7 +459,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       const int m0 = w.m * C::kTileM + (int)rank * 128, nt = w.n;
       for (int k0 = w.k0; k0 < w.k1; k0 += C::kGroups) {
         if (!wait_warp(&empty_bar[s], phase ^ 1, p.wait_ns)) {
-          if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutProducer);
+          give_up(&late, kStatusTimeoutProducer);
           ok = false;
           break;
         }
@@ -489,6 +501,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
     if (PAIR && !of_b)
       for (int i = 0; i < C::kStages && ok; ++i) {
         ok = wait_warp(&empty_bar[s], phase ^ 1, p.wait_ns);
+        if (!ok) give_up(&late, kStatusTimeoutProducer);
         if (++s == C::kStages) {
           s = 0;
           phase ^= 1;
@@ -517,14 +530,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
         const bool free = PAIR ? __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns))
                                : wait_warp(&acce_bar[b], ((i >> 1) & 1) ^ 1, p.wait_ns);
         if (!free) {
-          if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutMain);
+          give_up(&late, kStatusTimeoutMain);
           break;
         }
         tc_fence_after();
         const uint32_t acc = tmem + b * BN;
         for (int k0 = w.k0; k0 < w.k1; k0 += C::kGroups) {
           if (!wait_warp(&full_bar[s], phase, p.wait_ns)) {
-            if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutMain);
+            give_up(&late, kStatusTimeoutMain);
             ok = false;
             break;
           }
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
       // (one answer for the warp: its lanes leave together, or all go on to the warp's
       // tensor-memory loads)
       if (!wait_warp(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
-        if (lane == 0) atomicOr(&g_dense_status, kStatusTimeoutEpi);
+        give_up(&late, kStatusTimeoutEpi);
         break;
       }
       tc_fence_after();
@@ -647,14 +660,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) {  // neither block's memory goes while the other may still use it
+    if (threadIdx.x == 0 && late) st_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(&late)), rank ^ 1), 1);
+    __syncwarp();
     cluster_arrive_release();
     cluster_wait_acquire();
   }
   tc_fence_after();
-  // Ordinarily every copy has been consumed by now.  After a time-out of either block
-  // (both see it past the barrier above) some may still be on their way: stay until they
-  // have surely landed.
-  if (threadIdx.x == 0 && __ldcg(&g_dense_status) != 0) {
+  // Ordinarily every copy has been consumed by now.  After a time-out of either block some
+  // may still be on their way: stay until they have surely landed.
+  if (threadIdx.x == 0 && late) {
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < kLandingNs) __nanosleep(1000);
   }

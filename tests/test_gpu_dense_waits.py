@@ -76,3 +76,26 @@ def test_pairs_that_end_at_once(T, H, I):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert pkg.dense_status() == 0
+
+
+@pytest.mark.parametrize("T", [100, 600])  # one-SM and pair tiles
+def test_a_time_out_holds_up_its_own_launch_only(T, limit):
+    """A launch whose wait gave up stays 20 ms for its copies to land.  Later launches do
+    not, also while nobody has read the status word: ten of them take less than those 20 ms
+    (each a few microseconds of work), and are right."""
+    import mxfp4_expert_layer_gb300 as pkg
+    m = ffn.make(T, 512, 1024, torch.bfloat16, seed=T)
+    want = pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
+    limit(1)
+    pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
+    torch.cuda.synchronize()
+    limit(0)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    for _ in range(5):
+        got = pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
+    end.record()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert start.elapsed_time(end) < 20
+    assert pkg.dense_status() != 0
