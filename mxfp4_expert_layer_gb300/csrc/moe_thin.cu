@@ -119,8 +119,9 @@ __device__ __forceinline__ void finish(const ThinParams& p, const float (&total)
   }
 }
 
-// x as f16.  bf16: a power of two that brings the largest finite exponent (of the values
-// scaled together) to 14 takes values to f16, and its inverse is returned; f16 as it is.
+// x as f16.  bf16: a power of two, 2^126 at most, that brings the largest finite exponent (of
+// the values scaled together) to 14 takes values to f16, and its inverse is returned; 2^126
+// leaves subnormals, whose smallest step is 2^-133, exact.  f16 as it is.
 template <typename X>
 __device__ __forceinline__ uint32_t max_exponent(const uint4& v) {
   if constexpr (std::is_same<X, __half>::value) return 0;
@@ -136,7 +137,7 @@ __device__ __forceinline__ uint32_t max_exponent(const uint4& v) {
 template <typename X>
 __device__ __forceinline__ float scale_to_f16(uint4& v, uint32_t emax) {
   if constexpr (std::is_same<X, __half>::value) return 1.f;
-  const int pw = emax == 0 ? 0 : min(126, 14 + 127 - (int)emax);
+  const int pw = min(126, 14 + 127 - (int)emax);
   const float up = pow2_int(pw);
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -1,0 +1,36 @@
+"""MXFP4 products (moe_matvec_mxfp4) of bf16 values at the ends of their range, with row
+scales that bring the result back to the middle.  Bound: as in test_gpu_matvec.py, whose
+terms are all relative to the values; powers of two are taken out and put back exactly as
+long as the value itself is inside f32's range."""
+
+import pytest
+import torch
+
+from tests import test_gpu_matvec as matvec
+
+pytestmark = pytest.mark.gpu
+
+# (tokens, K): x resident, packed by one, two and four column groups
+FORMS = [(3, 256), (3, 4096), (13, 256), (40, 256)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import mxfp4_expert_layer_gb300 as pkg
+    pkg.build()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,K", FORMS)
+def test_tokens_of_subnormals(T, K, gated):
+    """Tokens whose values are all below 2^-126, the smallest normal value, and one of zeros."""
+    import mxfp4_expert_layer_gb300 as pkg
+    m = matvec.make(T, 96, K, torch.bfloat16, seed=T + K, lo=250, hi=255, bias=False)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    tiny = torch.randint(-63, 64, (T, K), generator=g, device="cuda").double() * 2.0 ** -133  # a bf16's smallest step
+    m["x"] = tiny.to(torch.bfloat16)
+    assert torch.equal(m["x"].double(), tiny)
+    m["x"][1] = 0
+    _, y = matvec.check(m, gated)
+    assert y[0].any() and not y[1].any()
+    assert pkg.dense_status() == 0
