@@ -225,7 +225,7 @@ struct ThinParams {
   int log_kw;               // MXFP4: log2 of the blocks of a cluster, which split K
   const uint8_t* row_exp;   // MXFP4: the rows' largest E8M0 bytes, tile order
   uint8_t* packed;          // MXFP4: workspace for x in fragment order
-  float* x_scale;           // MXFP4: and, behind it, its tokens' scales
+  int32_t* x_exp;           // MXFP4: and, behind it, the powers of two taken out of its tokens
   void* out;                // [T, n_out]
   float* gateup;            // f32 [T, 2 n_out] or null: the products before the activation
 };

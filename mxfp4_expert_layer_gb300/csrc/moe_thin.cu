@@ -13,9 +13,9 @@
 // MXFP4: two codes become an f16 pair by one conversion instruction (exact); a group's
 // 32 products are summed by two MMAs and then scaled in f32 by the group's scale, kept
 // relative to the largest of its row (taken out of the sum once, at the end).
-// x as f16: a power of two per (token, 128 values) brings its largest value to [2^14,
-// 2^15), so bf16 values are exact down to 2^-28 of the largest (absolute error 2^-39 of
-// it below), and is taken out again in f32.
+// x as f16: a power of two per token brings its largest value to [2^14, 2^15), so bf16
+// values are exact down to 2^-28 of the largest (absolute error 2^-39 of it below), and is
+// taken out again in f32, together with the row's scale.
 #include "moe_dense.cuh"
 #include "sm100_ptx.cuh"
 
@@ -120,8 +120,8 @@ __device__ __forceinline__ void finish(const ThinParams& p, const float (&total)
 }
 
 // x as f16.  bf16: a power of two, 2^126 at most, that brings the largest finite exponent (of
-// the values scaled together) to 14 takes values to f16, and its inverse is returned; 2^126
-// leaves subnormals, whose smallest step is 2^-133, exact.  f16 as it is.
+// the values scaled together) to 14 takes values to f16, and its inverse's exponent is
+// returned; 2^126 leaves subnormals, whose smallest step is 2^-133, exact.  f16 as it is.
 template <typename X>
 __device__ __forceinline__ uint32_t max_exponent(const uint4& v) {
   if constexpr (std::is_same<X, __half>::value) return 0;
@@ -135,8 +135,8 @@ __device__ __forceinline__ uint32_t max_exponent(const uint4& v) {
   return e;
 }
 template <typename X>
-__device__ __forceinline__ float scale_to_f16(uint4& v, uint32_t emax) {
-  if constexpr (std::is_same<X, __half>::value) return 1.f;
+__device__ __forceinline__ int scale_to_f16(uint4& v, uint32_t emax) {
+  if constexpr (std::is_same<X, __half>::value) return 0;
   const int pw = min(126, 14 + 127 - (int)emax);
   const float up = pow2_int(pw);
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -146,7 +146,7 @@ __device__ __forceinline__ float scale_to_f16(uint4& v, uint32_t emax) {
     w[j] = pack2<__half>(f.x * up, f.y * up);
   }
   v = make_uint4(w[0], w[1], w[2], w[3]);
-  return pow2_int(-pw);
+  return -pw;
 }
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float (&v)[4]) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
@@ -223,14 +223,18 @@ __device__ __forceinline__ void unit_product(const uint8_t* unit, float (&sum)[N
   }
 }
 
-// A product's row scale: 2^(byte - 127) of the row's largest group scale; byte 0 is the
-// subnormal 2^-127.
-__device__ __forceinline__ float row_scale(const ThinParams& p, int tile_row) {
-  return __uint_as_float(max((uint32_t)__ldg(p.row_exp + tile_row) << 23, 0x00400000u));
+// A sum times 2^e, plus the bias.  e, of the token's scale and of the row's largest group
+// scale together, is in [-253, 240], so the power goes in two halves: one scale after the
+// other would leave f32's range on the way to results inside it (values near 2^120 against
+// scales near 2^-120, and the reverse).  Each half is a normal f32: -126 in place of -127
+// for the least e is as good, the result being zero with either.
+__device__ __forceinline__ float scaled(float sum, int e, float bias) {
+  const int half = e >> 1;
+  return fmaf(sum * pow2_int(max(half, -126)), pow2_int(max(e - half, -126)), bias);
 }
 
 // ---- packed x: [token group][K units][4 groups][NT][32 lanes][16 bytes] f16, then the
-// tokens' f32 scales.  One block per token of the padded groups.
+// tokens' exponents.  One block per token of the padded groups.
 template <int NT>
 inline size_t packed_bytes(int T, int ku) { return (size_t)ceil_div(T, NT * 8) * ku * NT * 2048; }
 
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(256) matvec_pack_kernel(const __grid_constant_
 #pragma unroll
   for (int w = 0; w < 8; ++w) emax = max(emax, s_max[w]);
   const int group = tok / (NT * 8), r = tok - group * NT * 8;
-  float down = 1.f;
+  int down = 0;
   auto put = [&](int i, uint4 v) {
     down = scale_to_f16<X>(v, emax);
     // vector i: unit i / 16, its group (i % 16) / 4, fragment lane 4 (token % 8) + i % 4
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(256) matvec_pack_kernel(const __grid_constant_
     if (i < vecs) put(i, first[j]);
   }
   for (int i = threadIdx.x + 1024; i < vecs; i += 256) put(i, load(i));
-  if (threadIdx.x == 0) p.x_scale[tok] = down;
+  if (threadIdx.x == 0) p.x_exp[tok] = down;
 }
 
 template <typename X, int NT, bool PACKED, bool GATED, int ACT>
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
       if (PACKED) issue_x(s, at);
       else issue_w(s, grp, at);
     });
-  float down[2] = {1.f, 1.f};  // scales of x's tokens 2 t, 2 t + 1 (resident x)
+  int down[2] = {0, 0};  // exponents of x's tokens 2 t, 2 t + 1 (resident x)
   const int row_halves = resident_row_halves(p.ku);
   if constexpr (!PACKED) {
     // 16 lanes take one (token, unit), 8 values each; zero past K
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
     const int f8 = GATED ? p.n_out + f : f + 8;  // the weight row of the second half
     const bool low = GATED || f8 < p.n_out;
     const float b0 = p.bias ? p.bias[f] : 0.f, b1 = p.bias && low ? p.bias[f8] : 0.f;
-    const float r0 = row_scale(p, tile * 16 + g), r1 = row_scale(p, tile * 16 + g + 8);
+    const int r0 = __ldg(p.row_exp + tile * 16 + g) - 127, r1 = __ldg(p.row_exp + tile * 16 + g + 8) - 127;
 #pragma unroll
     for (int n8 = 0; n8 < NT; ++n8)
 #pragma unroll
@@ -446,8 +450,8 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
         const int tok = 8 * n8 + 2 * t + c;
         if (tok >= nt || (n8 & (S - 1)) != rank) continue;
         const size_t row = (size_t)(t0 + tok) * p.n_out;
-        const float q = PACKED ? __ldcg(p.x_scale + t0 + tok) : down[c];
-        const float v0 = fmaf(total[n8][c] * q, r0, b0), v1 = fmaf(total[n8][2 + c] * q, r1, b1);
+        const int q = PACKED ? __ldcg(p.x_exp + t0 + tok) : down[c];
+        const float v0 = scaled(total[n8][c], r0 + q, b0), v1 = scaled(total[n8][2 + c], r1 + q, b1);
         if constexpr (GATED) {
           out[row + f] = static_cast<X>(act_f<ACT>(v0) * v1);
         } else {
@@ -596,7 +600,7 @@ cudaError_t launch_matvec_t(ThinParams p, cudaStream_t stream) {
   const int groups_t = ceil_div(p.T, NT * 8);
   cudaError_t e;
   if constexpr (PACKED) {
-    p.x_scale = reinterpret_cast<float*>(p.packed + packed_bytes<NT>(p.T, p.ku));
+    p.x_exp = reinterpret_cast<int32_t*>(p.packed + packed_bytes<NT>(p.T, p.ku));
     e = launch_pdl(matvec_pack_kernel<X, NT>, dim3(groups_t * NT * 8), dim3(256), 0, stream, p);
     if (e != cudaSuccess) return e;
   }
@@ -669,7 +673,7 @@ size_t matvec_workspace_bytes(int T, int K) {
   const int ku = ceil_div(K, 128);
   if (matvec_resident(T, ku)) return 0;
   const size_t x = T <= 8 ? packed_bytes<1>(T, ku) : T <= 16 ? packed_bytes<2>(T, ku) : packed_bytes<4>(T, ku);
-  return x + kMatvecMaxTokens * sizeof(float);
+  return x + kMatvecMaxTokens * sizeof(int32_t);
 }
 
 uint32_t* thin_status_word() {

@@ -34,3 +34,29 @@ def test_tokens_of_subnormals(T, K, gated):
     _, y = matvec.check(m, gated)
     assert y[0].any() and not y[1].any()
     assert pkg.dense_status() == 0
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,K", FORMS)
+def test_large_values_against_small_scales(T, K, gated):
+    """Values around 2^120 against row scales of 2^-127 to 2^-123: the sums with the tokens'
+    scales alone are past f32's largest value, the results are ordinary."""
+    m = matvec.make(T, 96, K, torch.bfloat16, seed=T + K, lo=0, hi=5)
+    m["x"] *= 2.0 ** 120
+    assert torch.isfinite(m["x"]).all()
+    m["x"][-1] *= 2.0 ** -120  # beside them, an ordinary token: its products vanish beside the bias
+    _, y = matvec.check(m, gated)
+    assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("T,K", FORMS)
+def test_small_values_against_a_large_scale_of_zero_codes(T, K):
+    """Values around 2^-120 in rows whose largest scale, 2^127, has only zero codes, and whose
+    other scales are around 2^35: the sums with the tokens' scales alone are below f32's
+    smallest value, the results around 2^-80."""
+    m = matvec.make(T, 96, K, torch.bfloat16, seed=T + K, lo=160, hi=165, bias=False)
+    m["x"] *= 2.0 ** -120
+    m["codes"][:, 16:32] = 0
+    m["scales"][:, 1] = 254
+    _, y = matvec.check(m, False)
+    assert y.float().abs().max() > 2.0 ** -85
