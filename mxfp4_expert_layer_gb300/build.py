@@ -1,5 +1,6 @@
 """Builds the CUDA library ``libmoe_mxfp4.so`` in-tree with nvcc for sm_103a, and, where
-torch is installed, the torch binding of the dense operators ``_dense_ext.so`` over it.
+torch with CUDA is installed, the torch binding of the dense operators ``_dense_ext.so``
+over it.  The library is in place before the binding is, and without it.
 
 Each translation unit is compiled in parallel into ``_build/`` next to this file
 and linked into ``libmoe_mxfp4.so`` beside it; nothing is installed elsewhere.
@@ -46,7 +47,7 @@ def _inputs():
 
 
 def _targets():
-    return [LIB_PATH] + ([EXT_PATH] if _torch_dir() else [])
+    return [LIB_PATH] + ([EXT_PATH] if _torch_has_cuda() else [])
 
 
 def is_stale() -> bool:
@@ -60,6 +61,11 @@ def _torch_dir() -> str | None:
     """torch's install folder (found without importing it), or None."""
     spec = importlib.util.find_spec("torch")
     return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _torch_has_cuda() -> bool:
+    torch_dir = _torch_dir()
+    return torch_dir is not None and os.path.exists(os.path.join(torch_dir, "lib", "libtorch_cuda.so"))
 
 
 def _run(what: str, cmd) -> str:
@@ -109,17 +115,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(_compile_ext) if _torch_dir() else None
+        ext = ex.submit(_compile_ext) if _torch_has_cuda() else None
         objs = list(ex.map(lambda s: _compile(nvcc, s, verbose), SOURCES))
-        ext_obj = ext.result() if ext else None
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-Xlinker", f"-soname={LIB_NAME}", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
-    if ext_obj:
-        _link_ext(ext_obj)
+    if ext:
+        _link_ext(ext.result())
     return LIB_PATH
 
 
