@@ -54,7 +54,27 @@ def is_stale() -> bool:
     if not all(os.path.exists(p) for p in _targets()):
         return True
     t = min(os.path.getmtime(p) for p in _targets())
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    if any(os.path.getmtime(p) > t for p in _inputs()):
+        return True
+    return _torch_has_cuda() and _read(_stamp_path()) != _binding_stamp()
+
+
+def _read(path: str) -> str | None:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD_DIR, "binding.txt")
+
+
+def _binding_stamp() -> str:
+    """The Python and the torch that a binding is good for: both have an ABI of their own."""
+    torch_dir = _torch_dir()
+    return "\n".join((str(sysconfig.get_config_var("SOABI")), torch_dir, _read(os.path.join(torch_dir, "version.py")) or ""))
 
 
 def _torch_dir() -> str | None:
@@ -125,6 +145,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.replace(tmp, LIB_PATH)
     if ext:
         _link_ext(ext.result())
+        with open(_stamp_path(), "w") as f:
+            f.write(_binding_stamp())
     return LIB_PATH
 
 

@@ -41,3 +41,27 @@ def test_a_binding_that_fails_leaves_the_library(build, tmp_path, monkeypatch):
         build.build()
     assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.EXT_PATH)
     assert build.is_stale()
+
+
+def test_a_binding_of_another_torch_or_python_is_built_anew(build, tmp_path, monkeypatch):
+    folder = torch_folder(tmp_path, True)
+    version = tmp_path / "torch" / "version.py"
+    version.write_text("__version__ = '1'\n")
+    monkeypatch.setattr(build, "_torch_dir", lambda: folder)
+    built = []
+
+    def link(obj):
+        built.append(obj)
+        (tmp_path / "_dense_ext.so").touch()
+    monkeypatch.setattr(build, "_compile_ext", lambda: "binding.o")
+    monkeypatch.setattr(build, "_link_ext", link)
+    build.build()
+    assert len(built) == 1 and not build.is_stale()
+    build.build()
+    assert len(built) == 1
+    version.write_text("__version__ = '2'\n")
+    assert build.is_stale()
+    build.build()
+    assert len(built) == 2 and not build.is_stale()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399-other")
+    assert build.is_stale()
