@@ -11,9 +11,11 @@
 #include <initializer_list>
 #include <sstream>
 #include <string>
+#include <utility>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -43,6 +45,16 @@ const at::Tensor& tensor(const char* name, PyObject* o) {
   const at::Tensor* t = optional(name, o);
   if (!t) value_error(std::string(name) + ": a tensor is needed, got None");
   return *t;
+}
+
+// The results carry no history: where autograd records, a tensor that requires grad would
+// lose its gradient without a word.
+void no_history(std::initializer_list<std::pair<const char*, const at::Tensor*>> ts) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (const auto& [name, t] : ts)
+    if (t && t->requires_grad())
+      value_error(std::string(name) + " requires grad, but gradients of this operator are explicit calls: call it under "
+                                      "torch.no_grad(), or with detached tensors");
 }
 
 using Shape = std::initializer_list<int64_t>;
@@ -175,6 +187,8 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      *gate = optional("gate", a[3]), *next_w = optional("next_weight", a[5]),
                      *given_res = optional("residual_out", a[7]), *given_out = optional("out", a[8]);
     const float scale = (float)number(a[4]), eps = (float)number(a[6]);
+    no_history({{"block", &block}, {"residual", residual}, {"norm_weight", norm_w}, {"gate", gate}, {"next_weight", next_w},
+                {"residual_out", given_res}, {"out", given_out}});
     matrix("block", block);
     const int64_t T = block.size(0), H = block.size(1);
     const at::ScalarType type = block.scalar_type();
@@ -217,6 +231,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      *gate = optional("gate", a[5]), *next_w = optional("next_weight", a[7]);
     const float scale = (float)number(a[6]), eps = (float)number(a[8]);
     const bool has_residual = PyObject_IsTrue(a[9]) == 1;
+    no_history({{"d_residual_out", ds}, {"d_out", dy}});
     matrix("block", block);
     const int64_t T = block.size(0), H = block.size(1);
     const at::ScalarType type = block.scalar_type();
@@ -275,6 +290,7 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int act = integer(a[3]);
     const bool save = PyObject_IsTrue(a[4]) == 1;
     const at::Tensor* given = optional("out", a[5]);
+    no_history({{"x", &x}, {"w_gateup", &wgu}, {"w_down", &wd}, {"out", given}});
     const auto [T, H, I] = ffn_shape(x, wgu);
     const at::ScalarType type = x.scalar_type();
     const at::Device device = x.device();
@@ -306,6 +322,7 @@ PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      &wgu = tensor("w_gateup", a[3]), &wd = tensor("w_down", a[4]);
     const int act = integer(a[5]);
     const bool need_x = PyObject_IsTrue(a[6]) == 1, need_w = PyObject_IsTrue(a[7]) == 1;
+    no_history({{"d_out", &dout}});
     const auto [T, H, I] = ffn_shape(x, wgu);
     const at::ScalarType type = x.scalar_type();
     const at::Device device = x.device();
@@ -341,6 +358,7 @@ PyObject* matvec(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &x = tensor("x", a[0]), &w = tensor("weight", a[1]);
     const at::Tensor *bias = optional("bias", a[2]), *given = optional("out", a[7]);
     const int rows = integer(a[3]), K = integer(a[4]), kind = integer(a[5]), act = integer(a[6]);
+    no_history({{"x", &x}, {"bias", bias}, {"out", given}});
     matrix("x", x);
     const int64_t T = x.size(0), n_out = kind == MOE_WEIGHTS_GATEUP ? rows / 2 : rows;
     const at::ScalarType type = x.scalar_type();

@@ -9,10 +9,12 @@ with MXFP4 weights.
     gateup = MatvecMXFP4(codes, scales, kind=MOE_WEIGHTS_GATEUP)
     h = gateup(x)                       # x [T <= 64, K] -> silu(gate) * up, [T, rows / 2]
 
-Gradients are explicit calls; nothing here registers with autograd.  Every call runs on
-the current stream of its tensors' device, takes its workspace from torch's allocator
-(so calls on other streams and captured graphs never share one) and keeps no state; the
-checks and allocations are native (csrc/dense_binding.cpp).
+Gradients are explicit calls; nothing here registers with autograd.  Where autograd
+records, a tensor that requires grad is therefore refused (of a backward call: an incoming
+gradient that does); under ``torch.no_grad()`` it is as any other.  Every call runs on the
+current stream of its tensors' device, takes its workspace from torch's allocator (so calls
+on other streams and captured graphs never share one) and keeps no state; the checks and
+allocations are native (csrc/dense_binding.cpp).
 """
 
 from __future__ import annotations

@@ -1,0 +1,74 @@
+"""CPU checks of the dense operators' Python entry points: what they refuse before any
+tensor has to be on a GPU."""
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import mxfp4_expert_layer_gb300 as pkg
+    pkg.build()
+    return pkg
+
+
+def bf16(*shape, grad=False):
+    import torch
+    return torch.zeros(*shape, dtype=torch.bfloat16, requires_grad=grad)
+
+
+def calls(pkg):
+    """(name of the argument that requires grad, call with it)."""
+    z, w = bf16(4, 64), bf16(64)
+    norm = dict(block=z, residual=z, norm_weight=w, gate=w, next_weight=w)
+    for name in norm:
+        yield name, lambda t, n=name: pkg.block_norm(**dict(norm, **{n: t(*norm[n].shape)}))
+    ffn = dict(x=z, w_gateup=bf16(32, 64), w_down=bf16(64, 16))
+    for name in ffn:
+        yield name, lambda t, n=name: pkg.ffn_forward(**dict(ffn, **{n: t(*ffn[n].shape)}))
+    back = dict(d_out=z, x=z, gateup=bf16(4, 32).float(), w_gateup=bf16(32, 64), w_down=bf16(64, 16))
+    yield "d_out", lambda t: pkg.ffn_backward(**dict(back, d_out=t(4, 64)))
+    for name in ("d_residual_out", "d_out"):
+        given = dict(d_residual_out=z, d_out=z, block=z, residual_out=z, next_weight=w)
+        yield name, lambda t, n=name, g=given: pkg.block_norm_backward(**dict(g, **{n: t(4, 64)}))
+
+
+def test_no_gradient_is_cut_in_silence(pkg):
+    """Results carry no history, so a tensor that requires grad is refused while autograd
+    records; outside of that (where these CPU tensors are refused for not being on a GPU)
+    it is as any other."""
+    import torch
+    seen = 0
+    for name, call in calls(pkg):
+        with pytest.raises(ValueError, match=f"{name}.*explicit calls"):
+            call(lambda *s: bf16(*s, grad=True))
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call(lambda *s: bf16(*s, grad=True))
+        with pytest.raises(ValueError, match="CUDA"):
+            call(bf16)
+        seen += 1
+    assert seen == 11
+
+
+@pytest.mark.gpu
+def test_with_parameters_under_no_grad(pkg):
+    import torch
+    from tests import test_gpu_ffn as ffn
+    from tests import test_gpu_matvec as matvec
+    m = ffn.make(20, 64, 72, torch.bfloat16)
+    want = pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
+    p = {k: torch.nn.Parameter(v) for k, v in m.items()}
+    with pytest.raises(ValueError, match="explicit calls"):
+        pkg.ffn_forward(p["x"], p["wgu"], p["wd"])
+    with torch.no_grad():
+        out, gu = pkg.ffn_forward(p["x"], p["wgu"], p["wd"], save=True)
+    assert torch.equal(out, want)
+    grads = pkg.ffn_backward(m["dy"], p["x"], gu, p["wgu"], p["wd"])  # (explicit already)
+    for a, b in zip(grads, pkg.ffn_backward(m["dy"], m["x"], gu, m["wgu"], m["wd"])):
+        assert torch.equal(a, b)
+    v = matvec.make(3, 64, 128, torch.bfloat16)
+    w = pkg.MatvecMXFP4(v["codes"], v["scales"], bias=v["bias"])
+    x = v["x"].clone().requires_grad_()
+    with pytest.raises(ValueError, match="x requires grad.*explicit calls"):
+        w(x)
+    with torch.no_grad():
+        assert torch.equal(w(x), w(v["x"]))
