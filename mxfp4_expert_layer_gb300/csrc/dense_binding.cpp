@@ -155,6 +155,11 @@ int integer(PyObject* o) {
   if (v < INT32_MIN || v > INT32_MAX) value_error("an integer beyond 32 bits");
   return static_cast<int>(v);
 }
+bool flag(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v == 1;
+}
 bool arguments(Py_ssize_t got, Py_ssize_t want) {
   if (got == want) return true;
   PyErr_Format(PyExc_TypeError, "%zd arguments are needed, got %zd", want, got);
@@ -230,7 +235,7 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *res = optional("residual_out", a[3]), *norm_w = optional("norm_weight", a[4]),
                      *gate = optional("gate", a[5]), *next_w = optional("next_weight", a[7]);
     const float scale = (float)number(a[6]), eps = (float)number(a[8]);
-    const bool has_residual = PyObject_IsTrue(a[9]) == 1;
+    const bool has_residual = flag(a[9]);
     no_history({{"d_residual_out", ds}, {"d_out", dy}});
     matrix("block", block);
     const int64_t T = block.size(0), H = block.size(1);
@@ -288,7 +293,7 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const at::Tensor &x = tensor("x", a[0]), &wgu = tensor("w_gateup", a[1]), &wd = tensor("w_down", a[2]);
     const int act = integer(a[3]);
-    const bool save = PyObject_IsTrue(a[4]) == 1;
+    const bool save = flag(a[4]);
     const at::Tensor* given = optional("out", a[5]);
     no_history({{"x", &x}, {"w_gateup", &wgu}, {"w_down", &wd}, {"out", given}});
     const auto [T, H, I] = ffn_shape(x, wgu);
@@ -321,7 +326,7 @@ PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &dout = tensor("d_out", a[0]), &x = tensor("x", a[1]), &gateup = tensor("gateup", a[2]),
                      &wgu = tensor("w_gateup", a[3]), &wd = tensor("w_down", a[4]);
     const int act = integer(a[5]);
-    const bool need_x = PyObject_IsTrue(a[6]) == 1, need_w = PyObject_IsTrue(a[7]) == 1;
+    const bool need_x = flag(a[6]), need_w = flag(a[7]);
     no_history({{"d_out", &dout}});
     const auto [T, H, I] = ffn_shape(x, wgu);
     const at::ScalarType type = x.scalar_type();

@@ -72,3 +72,19 @@ def test_with_parameters_under_no_grad(pkg):
         w(x)
     with torch.no_grad():
         assert torch.equal(w(x), w(v["x"]))
+
+
+def test_flags_without_a_truth_value(pkg):
+    """A flag whose truth value raises passes that error on (these calls would else go on
+    to refuse their CPU tensors, or on a GPU to return with an error set)."""
+    class Flag:
+        def __bool__(self):
+            raise KeyError("no truth value")
+    z, w = bf16(4, 64), bf16(64)
+    wgu, wd, gu = bf16(32, 64), bf16(64, 16), bf16(4, 32).float()
+    for call in (lambda: pkg.ffn_forward(z, wgu, wd, save=Flag()),
+                 lambda: pkg.ffn_backward(z, z, gu, wgu, wd, need_x=Flag()),
+                 lambda: pkg.ffn_backward(z, z, gu, wgu, wd, need_weights=Flag()),
+                 lambda: pkg.block_norm_backward(z, z, z, z, next_weight=w, has_residual=Flag())):
+        with pytest.raises(KeyError, match="no truth value"):
+            call()
