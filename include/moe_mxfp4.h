@@ -443,6 +443,7 @@ int moe_prepare_matvec(const uint8_t* codes, const uint8_t* scales, int rows, in
  * carried as f16 times a power of two per token: values below 2^-28 of their token's
  * largest lose relative precision (absolute error 2^-39 of it).
  *   x [T, K] of dtype; bias f32 [rows] or NULL; act is read for MOE_WEIGHTS_GATEUP.
+ *   out may not overlap x (MOE_ERR_INVALID_ARG).
  *   workspace: moe_matvec_workspace_bytes(T, K) bytes (0 where x fits the
  *   kernel's shared memory: then it may be NULL), 256-byte aligned, contents irrelevant
  *   before and after.

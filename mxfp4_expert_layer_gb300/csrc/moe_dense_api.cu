@@ -8,6 +8,10 @@ using namespace moe;
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 static_assert(MOE_DTYPE_BF16 == kDtypeBf16 && MOE_DTYPE_F16 == kDtypeF16 && MOE_DTYPE_F32 == kDtypeF32, "dtype codes");
@@ -307,6 +311,9 @@ int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int
   if (need && (!workspace || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
   if (need > workspace_bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const bool gated = kind == MOE_WEIGHTS_GATEUP;
+  const int n_out = gated ? rows / 2 : rows;
+  // (the first blocks write their outputs while others still read x)
+  if (overlap(x, (size_t)T * K * 2, out, (size_t)T * n_out * 2)) return MOE_ERR_INVALID_ARG;
   const MatvecLayout L = make_matvec_layout(rows, K, gated);
   ThinParams p{};
   p.x = x;
@@ -316,7 +323,7 @@ int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int
   p.bias = bias;
   p.T = T;
   p.K = K;
-  p.n_out = gated ? rows / 2 : rows;
+  p.n_out = n_out;
   p.tiles = L.tiles;
   p.ku = L.ku;
   p.act = act;

@@ -124,7 +124,7 @@ class MatvecMXFP4:
     (moe_prepare_matvec, moe_matvec_mxfp4): codes uint8 [rows, K/2], scales uint8
     [rows, K/32].  kind MOE_WEIGHTS_DOWN: y = x W^T + bias, [T, rows].  kind
     MOE_WEIGHTS_GATEUP: act(gate) * up of the gate rows [0, rows/2) and the up rows,
-    [T, rows/2].  ``bias``: f32 [rows] or None."""
+    [T, rows/2].  ``bias``: f32 [rows] or None.  ``out`` may not overlap ``x``."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, kind: int = L.MOE_WEIGHTS_DOWN,
                  bias: Optional[torch.Tensor] = None, act: int = L.MOE_ACT_SILU):

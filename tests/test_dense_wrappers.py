@@ -88,3 +88,21 @@ def test_flags_without_a_truth_value(pkg):
                  lambda: pkg.block_norm_backward(z, z, z, z, next_weight=w, has_residual=Flag())):
         with pytest.raises(KeyError, match="no truth value"):
             call()
+
+
+def test_a_products_output_over_its_input(pkg):
+    """Blocks of the MXFP4 product write their outputs while others still read x: outputs
+    over any part of x are refused, outputs beside it are not."""
+    from mxfp4_expert_layer_gb300 import _lib as L
+    base = 1 << 20  # never dereferenced: what passes the checks finds no GPU, or is not run
+
+    def call(x, out, T=2, rows=64, K=96, kind=L.MOE_WEIGHTS_DOWN):
+        return L.moe_matvec_mxfp4(x, base << 4, None, T, rows, K, kind, 0, 0, out, None, 0, None)
+    n_x, n_out = 2 * 96 * 2, 2 * 64 * 2
+    for out in (base, base + 16, base + n_x - 16, base - n_out + 16):
+        assert call(base, out) == L.MOE_ERR_INVALID_ARG
+    assert call(base, base - n_out // 2, kind=L.MOE_WEIGHTS_GATEUP, rows=128) == L.MOE_ERR_INVALID_ARG
+    import torch
+    if not torch.cuda.is_available():
+        for out in (base + n_x, base - n_out):
+            assert call(base, out) == L.MOE_ERR_CUDA
