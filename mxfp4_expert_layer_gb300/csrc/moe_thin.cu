@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(kThinThreads, MatvecCfg<NT, PACKED>::kPerSm)
     if (S > 1) {
       // (one group per cluster) Each block finishes the column groups n8 = rank (mod S): the
       // others send theirs to its ring, [n8 / S][sender][warp][lane], whose copies have all
-      // been consumed once its warps have arrived.
+      // been consumed once its warps have arrived.  (The first lane may still be in the last
+      // refill's branch, and the barrier's instruction is the whole warp's.)
+      __syncwarp();
       ptx::cluster_arrive_release();
       ptx::cluster_wait_acquire();
       const uint32_t slot = (warp * 32 + lane) * 16;

@@ -60,3 +60,21 @@ def test_small_values_against_a_large_scale_of_zero_codes(T, K):
     m["scales"][:, 1] = 254
     _, y = matvec.check(m, False)
     assert y.float().abs().max() > 2.0 ** -85
+
+
+@pytest.mark.parametrize("T", [1, 9, 30])
+def test_clusters_along_k_repeat(T):
+    """Few rows and a long K: the blocks of a cluster take a share of K each and meet at its
+    barrier straight after their last stages, many times over."""
+    import mxfp4_expert_layer_gb300 as pkg
+    m = matvec.make(T, 260, 16384, torch.bfloat16, seed=T)
+    w, want = matvec.check(m, False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(200):
+            got = w(m["x"])
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert pkg.dense_status() == 0
