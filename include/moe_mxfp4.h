@@ -388,9 +388,10 @@ int moe_block_norm_backward(const void* d_residual_out, const void* d_out, const
  * or a dense layer beside the experts).
  *   g = x W_gate^T, u = x W_up^T, h = act(g) * u        one kernel
  *   out = h W_down^T
- * Sums are f32; h is rounded to dtype between the products.
+ * Sums are f32; h is rounded to dtype between the products: in f16 an h beyond 65504 becomes
+ * infinite and one below 2^-14 loses bits, where bf16 has f32's range.
  *   x [T, H]; w_gateup [2I, H], gate rows [0, I) then up rows; w_down [H, I]: as stored,
- *   nothing is prepared; out [T, H].
+ *   nothing is prepared; out [T, H], which may be x itself.
  *   gateup_out: f32 [T, 2I] (g, then u), written for moe_ffn_backward; NULL to skip.
  *   1 <= T <= 2^24, H and I multiples of 8 from 8 to 2^17; arrays 16-byte aligned,
  *   workspace moe_ffn_workspace_bytes(T, H, I, 0) bytes, 256-byte aligned, contents
@@ -404,7 +405,8 @@ int moe_ffn_forward(const void* x, const void* w_gateup, const void* w_down, int
 /* moe_ffn_backward: the gradients of moe_ffn_forward, from its inputs and saved g, u.
  *   dh = d_out W_down;  dg = dh * u * act'(g);  du = dh * act(g);  h = act(g) * u
  *   d_x = [dg du] w_gateup;  d_w_gateup = [dg du]^T x;  d_w_down = d_out^T h
- * dg, du and h are formed in f32 and rounded to dtype as the next products' operands.
+ * dg, du and h are formed in f32 and rounded to dtype as the next products' operands, with
+ * f16's range as above: scale d_out where its gradients are small.
  *   d_x [T, H], d_w_gateup [2I, H], d_w_down [H, I] of dtype: overwritten; each may be
  *   NULL (not all).  workspace: moe_ffn_workspace_bytes(T, H, I, 1) bytes.
  *   No output may overlap an input.  Everything else is as for moe_ffn_forward.      */

@@ -600,8 +600,11 @@ cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
   const bool every = p.norm_w && p.next_w && p.residual && p.residual_out;
   const int gate = !every ? kAnyGate : p.gate_kind == kGateToken ? kGateNone : p.gate_kind;
   const int row_threads = (p.H / 8 + 31) / 32 * 32, groups = min(512 / row_threads, kNormMaxGroups);
-  // many rows: persistent blocks, as many per SM as 56 registers a thread allow (fewer rows
-  // are done sooner by a block each)
+  // many rows: persistent blocks, as many per SM as 56 registers a thread allow, which f16
+  // takes at most and bf16 without a feature or full gate does (fewer rows are done sooner by a
+  // block each).  With such a gate bf16 takes 58 to 64: at some widths (2880 is one) one block
+  // per SM fewer is resident than this asks for, and the last ones run in a second round.
+  // Rows of calls without every argument, and of more than 4096 values, have a block each.
   const int per_sm = groups > 0 ? 1152 / (groups * row_threads) : 0, blocks = per_sm * device_sms();
   if (every && groups > 0 && p.T >= 4 * groups * blocks) {
     const void* src[3] = {p.block, p.residual, gate == kGateFull ? p.gate : nullptr};

@@ -62,7 +62,8 @@ def block_norm(block: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
 
 
 class BlockNormGrads(NamedTuple):
-    """Gradients of block_norm; None for an argument that the call did not have."""
+    """Gradients of block_norm; None for an argument that the call did not have.  The f32 [H]
+    ones share a storage (3 H values at most)."""
     block: torch.Tensor
     residual: Optional[torch.Tensor]
     norm_weight: Optional[torch.Tensor]   # f32 [H]
@@ -87,8 +88,8 @@ def ffn_forward(x: torch.Tensor, w_gateup: torch.Tensor, w_down: torch.Tensor, *
                 save: bool = False, out: Optional[torch.Tensor] = None):
     """out = (act(x W_gate^T) * (x W_up^T)) W_down^T (moe_ffn_forward): x [T, H],
     w_gateup [2I, H] (gate rows, then up rows) and w_down [H, I], all bf16 or all f16.
-    With ``save``, (out, gateup): the products before the activation, f32 [T, 2I], for
-    ffn_backward."""
+    ``out`` may be ``x``.  With ``save``, (out, gateup): the products before the activation,
+    f32 [T, 2I], for ffn_backward, which needs x as it was."""
     r = _ext.ffn_forward(x, w_gateup, w_down, act, save, out)
     return r if save else r[0]
 

@@ -100,3 +100,14 @@ def test_many_weight_rows_for_several_groups_of_tokens(T, dtype, gated):
     groups of up to 32 tokens; K with a tail inside its last unit."""
     matvec.check(matvec.make(T, 2 * 30010, 1632, dtype, seed=T), gated)
     matvec.check(matvec.make(T, 2 * 1001, 4000, dtype, seed=T), gated, "gelu")
+
+
+@pytest.mark.parametrize("T", [3, 16, 100, 600])
+def test_feed_forward_in_place(T):
+    import mxfp4_expert_layer_gb300 as pkg
+    m = ffn.make(T, 520, 1024, BF16, seed=T)
+    want = pkg.ffn_forward(m["x"], m["wgu"], m["wd"])
+    x = m["x"].clone()
+    out, gu = pkg.ffn_forward(x, m["wgu"], m["wd"], out=x, save=True)
+    assert out is x and torch.equal(x, want)
+    assert torch.equal(gu, pkg.ffn_forward(m["x"], m["wgu"], m["wd"], save=True)[1])
