@@ -356,7 +356,7 @@ int moe_tensor_peak(int kind, int mmas_per_sm, double* tflops, moe_stream_t stre
  *   stream_dtype: dtype or MOE_DTYPE_F32.
  *   residual_out: s, [T, H] of stream_dtype, or NULL when only `out` is wanted; it may
  *   be `residual` itself.  out: [T, H] of dtype; NULL exactly when next_weight is; it
- *   may be `block` itself.
+ *   may be `block` itself; outputs overlap inputs in no other way.
  *   1 <= T <= 2^24, H % 8 == 0 with 8 <= H <= 8192; arrays 16-byte aligned (a token
  *   gate 4); eps finite and >= 0; residual_scale finite.
  * Source: "triton-kernels" README, "Kernels" (rmsnorm_residual_fused), with the norm
