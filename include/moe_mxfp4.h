@@ -414,6 +414,51 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
                      int T, int H, int I, int act, int dtype, void* d_x, void* d_w_gateup, void* d_w_down,
                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* moe_sort_tokens: token rows into expert order, for experts of the caller's own (the
+ * layer's permute step by itself), in the order of moe_build_tile_table: by expert, then by
+ * assignment a = t*k + j.  An index outside [0, E) drops its assignment (a padding token, an
+ * expert that lives elsewhere): dropped assignments follow behind all others, as rows of
+ * zeros, and their entries of perm and inv_perm are kept as -1 - entry.
+ *   offsets i32 [E + 1]: rows of expert e are [offsets[e], offsets[e + 1]); the rows from
+ *   offsets[E] on are those of the dropped.
+ *   perm i32 [T*k]: assignment at each row.  inv_perm i32 [T, k]: row of each assignment.
+ *   rows [T*k] rows of row_bytes: x[perm / k].  row_scales, or NULL: the same of `scales`.
+ *   x: [T] rows of row_bytes bytes (of any type), a multiple of 16 up to 65536; scales: [T]
+ *   rows of scale_bytes (0 .. 4096; 0 with scales and row_scales NULL).  T, k and E as in the
+ *   conventions above.  Arrays 16-byte aligned; no output may overlap an input.
+ * Source: "Quick Start", "Fused MoE Dispatch" (permute).                             */
+int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, int T, int k, int E, int row_bytes,
+                    int scale_bytes, int32_t* offsets, int32_t* perm, int32_t* inv_perm, void* rows, void* row_scales,
+                    moe_stream_t stream);
+
+/* moe_unsort_tokens: rows in expert order back to tokens, weighted:
+ *   out[t] = sum_j topk_w[t, j] * y[inv_perm[t, j]]      f32, ascending j, rounded once
+ * over the j whose inv_perm is in [0, T*k); a token without any gets zeros, and no other row
+ * of y is read.  With topk_w NULL (all 1) it is the gradient of moe_sort_tokens: d_x of d_rows.
+ *   y [T*k, H], out [T, H] of dtype (MOE_DTYPE_BF16, _F16 or _F32); H a multiple of 8, a row
+ *   at most 65536 bytes; arrays 16-byte aligned; out may not overlap an input.
+ * Source: "Quick Start", "Fused MoE Dispatch" (unpermute).                           */
+int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_w, int T, int k, int H, int dtype, void* out,
+                      moe_stream_t stream);
+
+/* moe_unsort_tokens_backward: the gradients of moe_unsort_tokens.
+ *   d_y[inv_perm[t, j]] = topk_w[t, j] * d_out[t]; a dropped assignment's row (-1 - inv_perm):
+ *   zeros, so that after moe_sort_tokens every row of d_y is written
+ *   d_topk_w[t, j] = sum_h d_out[t, h] * y[inv_perm[t, j], h]   (f32; 0 where dropped)
+ * Either may be NULL; y is read for d_topk_w alone, and may be NULL without it.  Types,
+ * sizes and overlaps as for moe_unsort_tokens.                                       */
+int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* inv_perm, const float* topk_w, int T, int k,
+                               int H, int dtype, void* d_y, float* d_topk_w, moe_stream_t stream);
+
+/* moe_route_backward: the gradient of moe_route's weights into its logits.
+ *   d_topk_w f32 [T, k]; logits f32 [T, E], topk_idx and topk_w as moe_route gave them (the
+ *   indices as routed, not with assignments dropped); gating: moe_route's flag, or 0.
+ *   d_logits f32 [T, E]: written whole, 0 where the weights do not depend on the logit.
+ *   The selection itself has no gradient.  An expert listed twice gets the sum, an index
+ *   outside [0, E) nothing.  Arrays 16-byte aligned; d_logits may not overlap an input. */
+int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t* topk_idx, const float* topk_w, int T, int k,
+                       int E, int gating, float* d_logits, moe_stream_t stream);
+
 /* moe_dense_status: the device status of the dense operators' pipelines (feed-forward
  * GEMMs, MXFP4 products, norms' row copies) on the current device, as moe_get_device_status (bits and
  * returns) for words that the library holds per GPU: synchronises `stream`, reads them

@@ -73,6 +73,10 @@ SIGNATURES = {
     "moe_ffn_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "moe_ffn_forward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _S, _P]),
     "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P]),
+    "moe_sort_tokens": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_unsort_tokens": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_unsort_tokens_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_route_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_dense_status": (_I, [ctypes.POINTER(_I), _P]),
     "moe_prepared_matvec_bytes": (_S, [_I, _I, _I]),
     "moe_prepare_matvec": (_I, [_P, _P, _I, _I, _I, _P, _S, _P]),
@@ -149,6 +153,10 @@ moe_block_norm_backward = _call("moe_block_norm_backward")
 moe_ffn_workspace_bytes = _call("moe_ffn_workspace_bytes")
 moe_ffn_forward = _call("moe_ffn_forward")
 moe_ffn_backward = _call("moe_ffn_backward")
+moe_sort_tokens = _call("moe_sort_tokens")
+moe_unsort_tokens = _call("moe_unsort_tokens")
+moe_unsort_tokens_backward = _call("moe_unsort_tokens_backward")
+moe_route_backward = _call("moe_route_backward")
 moe_dense_status = _call("moe_dense_status")
 moe_prepared_matvec_bytes = _call("moe_prepared_matvec_bytes")
 moe_prepare_matvec = _call("moe_prepare_matvec")

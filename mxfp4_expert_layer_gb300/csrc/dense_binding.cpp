@@ -96,6 +96,13 @@ at::Tensor row_of(const at::Tensor& m, int64_t i) {
   t.unsafeGetTensorImpl()->set_sizes_contiguous(m.sizes().slice(1));
   return t;
 }
+// The tensor of this shape at element `at` of a tensor's storage, sharing it.
+at::Tensor part_of(const at::Tensor& m, int64_t at, Shape shape) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(m.storage()), m.key_set(), m.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(shape));
+  return t;
+}
 // Results of up to this many bytes together share one allocation: each costs host time that a
 // decoded token's norm waits for (4.6 us a call among others, 4.1 shared), while larger
 // results had better be freed one by one.
@@ -388,6 +395,138 @@ PyObject* matvec(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ tokens sorted by expert
+int dtype_any(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? MOE_DTYPE_F32 : dtype16(t); }
+// Bytes of a row of a matrix.
+int row_bytes(const at::Tensor& t) { return narrow(t.size(1) * (int64_t)t.element_size()); }
+
+// x, topk_idx, n_experts, scales
+PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 4)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &x = tensor("x", a[0]), &idx = tensor("topk_idx", a[1]);
+    const int E = integer(a[2]);
+    const at::Tensor* scales = optional("scales", a[3]);
+    no_history({{"x", &x}, {"scales", scales}});
+    matrix("x", x);
+    matrix("topk_idx", idx);
+    if (scales) matrix("scales", *scales);
+    const int64_t T = x.size(0), k = idx.size(1);
+    const at::Device device = x.device();
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *px = need("x", &x, {T, x.size(1)}, x.scalar_type(), device), *pi = need("topk_idx", &idx, {T, k}, at::kInt, device),
+         *ps = scales ? need("scales", scales, {T, scales->size(1)}, scales->scalar_type(), device) : nullptr;
+    const int t = narrow(T), kk = narrow(k), rb = row_bytes(x), sb = scales ? row_bytes(*scales) : 0;
+    if (T < 1 || k < 1 || E < 1 || T > INT32_MAX / k) refuse("moe_sort_tokens", MOE_ERR_UNSUPPORTED_SHAPE);
+    // offsets, perm and inv_perm in one allocation, each 16-byte aligned
+    const int64_t rows = T * k, at_perm = ((int64_t)E + 4) / 4 * 4, at_inv = at_perm + (rows + 3) / 4 * 4;
+    const at::Tensor order = empty({at_inv + rows}, at::kInt, device);
+    const at::Tensor offsets = part_of(order, 0, {(int64_t)E + 1}), perm = part_of(order, at_perm, {rows}),
+                     inv = part_of(order, at_inv, {T, k});
+    const at::Tensor sorted = empty({rows, x.size(1)}, x.scalar_type(), device);
+    at::Tensor sorted_scales;
+    if (scales) sorted_scales = empty({rows, scales->size(1)}, scales->scalar_type(), device);
+    call("moe_sort_tokens", device, [&](moe_stream_t s) {
+      return moe_sort_tokens(px, ps, static_cast<const int32_t*>(pi), t, kk, E, rb, sb, static_cast<int32_t*>(offsets.data_ptr()),
+                             static_cast<int32_t*>(perm.data_ptr()), static_cast<int32_t*>(inv.data_ptr()), sorted.data_ptr(),
+                             address(sorted_scales), s);
+    });
+    return tuple({sorted, sorted_scales, offsets, perm, inv});
+  });
+}
+
+// y (or d_rows), inv_perm, topk_w, out; the name of the first for messages
+PyObject* unsort(const char* name, PyObject* oy, PyObject* oinv, PyObject* ow, PyObject* oout) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &y = tensor(name, oy), &inv = tensor("inv_perm", oinv);
+    const at::Tensor *w = optional("topk_w", ow), *given = optional("out", oout);
+    no_history({{name, &y}, {"topk_w", w}, {"out", given}});
+    matrix(name, y);
+    matrix("inv_perm", inv);
+    const int64_t T = inv.size(0), k = inv.size(1), H = y.size(1);
+    const at::Device device = y.device();
+    const int code = dtype_any(y);
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *py = need(name, &y, {T * k, H}, y.scalar_type(), device), *pi = need("inv_perm", &inv, {T, k}, at::kInt, device),
+         *pw = need("topk_w", w, {T, k}, at::kFloat, device);
+    need("out", given, {T, H}, y.scalar_type(), device);
+    const int t = narrow(T), kk = narrow(k), h = narrow(H);
+    const at::Tensor out = given ? *given : empty({T, H}, y.scalar_type(), device);
+    call("moe_unsort_tokens", device, [&](moe_stream_t s) {
+      return moe_unsort_tokens(py, static_cast<const int32_t*>(pi), static_cast<const float*>(pw), t, kk, h, code, out.data_ptr(), s);
+    });
+    return wrap(out);
+  });
+}
+// d_rows, inv_perm, out
+PyObject* sort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return arguments(n, 3) ? unsort("d_rows", a[0], a[1], Py_None, a[2]) : nullptr;
+}
+// y, inv_perm, topk_w, out
+PyObject* unsort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return arguments(n, 4) ? unsort("y", a[0], a[1], a[2], a[3]) : nullptr;
+}
+
+// d_out, y, inv_perm, topk_w, need_y, need_w
+PyObject* unsort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& dout = tensor("d_out", a[0]);
+    const at::Tensor* y = optional("y", a[1]);
+    const at::Tensor& inv = tensor("inv_perm", a[2]);
+    const at::Tensor* w = optional("topk_w", a[3]);
+    const bool need_y = flag(a[4]), need_w = flag(a[5]);
+    no_history({{"d_out", &dout}});
+    matrix("d_out", dout);
+    matrix("inv_perm", inv);
+    const int64_t T = inv.size(0), k = inv.size(1), H = dout.size(1);
+    const at::ScalarType type = dout.scalar_type();
+    const at::Device device = dout.device();
+    const int code = dtype_any(dout);
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *pd = need("d_out", &dout, {T, H}, type, device), *py = need("y", y, {T * k, H}, type, device),
+         *pi = need("inv_perm", &inv, {T, k}, at::kInt, device), *pw = need("topk_w", w, {T, k}, at::kFloat, device);
+    const int t = narrow(T), kk = narrow(k), h = narrow(H);
+    at::Tensor d_y, d_w;
+    if (need_y) d_y = empty({T * k, H}, type, device);
+    if (need_w) d_w = empty({T, k}, at::kFloat, device);
+    call("moe_unsort_tokens_backward", device, [&](moe_stream_t s) {
+      return moe_unsort_tokens_backward(pd, py, static_cast<const int32_t*>(pi), static_cast<const float*>(pw), t, kk, h, code,
+                                        address(d_y), static_cast<float*>(address(d_w)), s);
+    });
+    return tuple({d_y, d_w});
+  });
+}
+
+// d_topk_w, logits, topk_idx, topk_w, gating
+PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &dw = tensor("d_topk_w", a[0]), &logits = tensor("logits", a[1]), &idx = tensor("topk_idx", a[2]),
+                     &w = tensor("topk_w", a[3]);
+    const int gating = integer(a[4]);
+    no_history({{"d_topk_w", &dw}});
+    matrix("logits", logits);
+    matrix("topk_idx", idx);
+    const int64_t T = logits.size(0), E = logits.size(1), k = idx.size(1);
+    const at::Device device = logits.device();
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *pd = need("d_topk_w", &dw, {T, k}, at::kFloat, device), *pl = need("logits", &logits, {T, E}, at::kFloat, device),
+         *pi = need("topk_idx", &idx, {T, k}, at::kInt, device), *pw = need("topk_w", &w, {T, k}, at::kFloat, device);
+    const int t = narrow(T), kk = narrow(k), e = narrow(E);
+    const at::Tensor d_logits = empty({T, E}, at::kFloat, device);
+    call("moe_route_backward", device, [&](moe_stream_t s) {
+      return moe_route_backward(static_cast<const float*>(pd), static_cast<const float*>(pl), static_cast<const int32_t*>(pi),
+                                static_cast<const float*>(pw), t, kk, e, gating, static_cast<float*>(d_logits.data_ptr()), s);
+    });
+    return wrap(d_logits);
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_INCREF(cls);
   Py_XSETREF(g_error_class, cls);
@@ -397,7 +536,10 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(block_norm),   FAST(block_norm_backward),
                          FAST(ffn_forward),  FAST(ffn_backward),
-                         FAST(matvec),       {"set_error", set_error, METH_O, nullptr},
+                         FAST(matvec),       FAST(sort_tokens),
+                         FAST(sort_tokens_backward), FAST(unsort_tokens),
+                         FAST(unsort_tokens_backward), FAST(route_backward),
+                         {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dense_ext", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -172,6 +172,38 @@ uint32_t* norm_status_word();
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int dtype, int stream_dtype,
                                        cudaStream_t stream);
 
+// ------------------------------------------------------------------ tokens sorted by expert
+struct SortParams {
+  const int32_t* idx;       // [T, k]; outside [0, E): dropped
+  const void *x, *scales;   // [T] rows of row_bytes, and of scale_bytes (or null)
+  int T, k, E, row_bytes, scale_bytes;
+  int32_t *offsets, *perm, *inv_perm;  // [E + 1], [T k], [T k]
+  void *rows, *row_scales;  // [T k] rows
+};
+struct UnsortParams {
+  const void* y;            // [T k, H]
+  const int32_t* inv_perm;  // [T, k]; negative: dropped
+  const float* w;           // [T, k] or null: 1
+  int T, k, H;
+  void* out;                // [T, H]
+};
+struct UnsortBackwardParams {
+  UnsortParams f;           // out unused
+  const void* d_out;        // [T, H]
+  void* d_y;                // [T k, H] or null
+  float* d_w;               // [T, k] or null
+};
+struct RouteBackwardParams {
+  const float *d_w, *logits, *w;  // [T, k], [T, E], [T, k]
+  const int32_t* idx;       // [T, k]
+  int T, k, E, gating;
+  float* d_logits;          // [T, E]
+};
+cudaError_t launch_sort(const SortParams& p, cudaStream_t stream);
+cudaError_t launch_unsort(const UnsortParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_unsort_backward(const UnsortBackwardParams& q, int dtype, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t stream);
+
 // ------------------------------------------------------------------ products of a few tokens
 constexpr int kThinTokens = 16;   // tokens of the 16-bit few-token kernel
 constexpr int kThinRows = 16;     // weight rows of one of their tiles (MMA M)

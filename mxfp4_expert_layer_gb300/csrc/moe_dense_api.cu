@@ -22,6 +22,8 @@ static_assert(MOE_ACT_SILU == kActSilu && MOE_ACT_GELU == kActGelu, "activations
 constexpr int kMaxRows = 1 << 24;      // tokens of a call
 constexpr int kMaxNormDim = 8192;      // a row sits in one block's registers
 constexpr int kMaxFfnDim = 1 << 17;    // H and I of the feed-forward block
+constexpr int kMaxMovedBytes = 1 << 16;  // a row moved between token and expert order
+constexpr int kMaxScaleBytes = 1 << 12;  // and its scales
 constexpr int kMaxMatvecRows = 1 << 22, kMaxMatvecDim = 1 << 16;
 
 bool dtype16(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
@@ -94,6 +96,16 @@ int check_ffn(int T, int H, int I, int dtype, int act) {
   if (!dtype16(dtype) || (act != MOE_ACT_SILU && act != MOE_ACT_GELU)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
+
+// Tokens and experts of a routing, as the layer's.
+bool routing_shape(int T, int k, int E) {
+  return T >= 1 && k >= 1 && k <= kMaxTopK && k <= E && E <= kMaxExperts && (long long)T * k <= kMaxRows;
+}
+// Rows of `H` values that the moves between token and expert order take.
+bool moved_shape(int T, int k, int H, int dtype) {
+  return routing_shape(T, k, kMaxExperts) && H >= 8 && H % 8 == 0 && H <= (dtype == MOE_DTYPE_F32 ? kMaxMovedBytes / 4 : kMaxMovedBytes / 2);
+}
+bool dtype_any(int d) { return dtype16(d) || d == MOE_DTYPE_F32; }
 
 }  // namespace
 
@@ -266,6 +278,113 @@ int moe_block_norm_backward(const void* d_residual_out, const void* d_out, const
   q.partial = static_cast<float*>(workspace);
   q.blocks = block_norm_backward_blocks(T, H);
   return cuda_status(launch_block_norm_backward(q, dtype, stream_dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, int T, int k, int E, int row_bytes,
+                    int scale_bytes, int32_t* offsets, int32_t* perm, int32_t* inv_perm, void* rows, void* row_scales,
+                    moe_stream_t stream) {
+  if (!routing_shape(T, k, E) || row_bytes < 16 || row_bytes % 16 || row_bytes > kMaxMovedBytes) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (scale_bytes < 0 || scale_bytes > kMaxScaleBytes) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!x || !topk_idx || !offsets || !perm || !inv_perm || !rows) return MOE_ERR_INVALID_ARG;
+  if ((scales != nullptr) != (scale_bytes > 0) || (row_scales != nullptr) != (scale_bytes > 0)) return MOE_ERR_INVALID_ARG;
+  const void* all[] = {x, scales, topk_idx, offsets, perm, inv_perm, rows, row_scales};
+  for (const void* q : all)
+    if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  // (rows are written while others are still read)
+  const size_t n = (size_t)T * k;
+  const struct { const void* p; size_t bytes; } in[] = {{x, (size_t)T * row_bytes}, {scales, (size_t)T * scale_bytes},
+                                                        {topk_idx, n * 4}},
+      out[] = {{offsets, (size_t)(E + 1) * 4}, {perm, n * 4}, {inv_perm, n * 4}, {rows, n * row_bytes}, {row_scales, n * scale_bytes}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (o.p && i.p && overlap(o.p, o.bytes, i.p, i.bytes)) return MOE_ERR_INVALID_ARG;
+  SortParams p{};
+  p.idx = topk_idx;
+  p.x = x;
+  p.scales = scales;
+  p.T = T;
+  p.k = k;
+  p.E = E;
+  p.row_bytes = row_bytes;
+  p.scale_bytes = scale_bytes;
+  p.offsets = offsets;
+  p.perm = perm;
+  p.inv_perm = inv_perm;
+  p.rows = rows;
+  p.row_scales = row_scales;
+  return cuda_status(launch_sort(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_w, int T, int k, int H, int dtype, void* out,
+                      moe_stream_t stream) {
+  if (!dtype_any(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!moved_shape(T, k, H, dtype)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!y || !inv_perm || !out || !aligned(y, 16) || !aligned(inv_perm, 16) || !aligned(topk_w, 16) || !aligned(out, 16))
+    return MOE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
+  if (overlap(y, bytes * k, out, bytes) || overlap(inv_perm, n, out, bytes) || (topk_w && overlap(topk_w, n, out, bytes)))
+    return MOE_ERR_INVALID_ARG;
+  UnsortParams p{};
+  p.y = y;
+  p.inv_perm = inv_perm;
+  p.w = topk_w;
+  p.T = T;
+  p.k = k;
+  p.H = H;
+  p.out = out;
+  return cuda_status(launch_unsort(p, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* inv_perm, const float* topk_w, int T, int k,
+                               int H, int dtype, void* d_y, float* d_topk_w, moe_stream_t stream) {
+  if (!dtype_any(dtype)) return MOE_ERR_INVALID_ARG;
+  if (!moved_shape(T, k, H, dtype)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!d_out || !inv_perm || (!d_y && !d_topk_w) || (d_topk_w && !y)) return MOE_ERR_INVALID_ARG;
+  const void* all[] = {d_out, y, inv_perm, topk_w, d_y, d_topk_w};
+  for (const void* q : all)
+    if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
+  const struct { const void* p; size_t bytes; } in[] = {{d_out, bytes}, {y, bytes * k}, {inv_perm, n}, {topk_w, n}},
+                                                out[] = {{d_y, bytes * k}, {d_topk_w, n}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (o.p && i.p && overlap(o.p, o.bytes, i.p, i.bytes)) return MOE_ERR_INVALID_ARG;
+  UnsortBackwardParams q{};
+  q.f.y = y;
+  q.f.inv_perm = inv_perm;
+  q.f.w = topk_w;
+  q.f.T = T;
+  q.f.k = k;
+  q.f.H = H;
+  q.d_out = d_out;
+  q.d_y = d_y;
+  q.d_w = d_topk_w;
+  return cuda_status(launch_unsort_backward(q, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t* topk_idx, const float* topk_w, int T, int k,
+                       int E, int gating, float* d_logits, moe_stream_t stream) {
+  if (!routing_shape(T, k, E)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const int kind = gating & MOE_ROUTE_FROM_LOGITS ? -1 : gating_from_flags(gating);
+  if (kind < 0) return MOE_ERR_INVALID_ARG;
+  const void* need[] = {d_topk_w, logits, topk_idx, topk_w, d_logits};
+  for (const void* q : need)
+    if (!q || !aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t all = (size_t)T * E * 4, n = (size_t)T * k * 4;
+  if (overlap(d_logits, all, d_topk_w, n) || overlap(d_logits, all, logits, all) || overlap(d_logits, all, topk_idx, n) ||
+      overlap(d_logits, all, topk_w, n))
+    return MOE_ERR_INVALID_ARG;
+  RouteBackwardParams p{};
+  p.d_w = d_topk_w;
+  p.logits = logits;
+  p.w = topk_w;
+  p.idx = topk_idx;
+  p.T = T;
+  p.k = k;
+  p.E = E;
+  p.gating = kind;
+  p.d_logits = d_logits;
+  return cuda_status(launch_route_backward(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_prepared_matvec_bytes(int rows, int K, int kind) {

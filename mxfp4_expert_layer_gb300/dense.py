@@ -1,11 +1,16 @@
 """Torch-facing wrappers of the dense operators around the expert layer: the norms
-before and after a block, the gated feed-forward block, and products of a few tokens
-with MXFP4 weights.
+before and after a block, the gated feed-forward block, tokens sorted by expert and back,
+and products of a few tokens with MXFP4 weights.
 
     s, y = block_norm(z, r, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn)
     grads = block_norm_backward(ds, dy, z, s, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn)
     out, gu = ffn_forward(x, w_gateup, w_down, save=True)
     d_x, d_w_gateup, d_w_down = ffn_backward(d_out, x, gu, w_gateup, w_down)
+    s = sort_tokens(x, topk_idx, E)     # s.rows: x by expert; experts of one's own give y [T*k, H]
+    out = unsort_tokens(y, s.inv_perm, topk_w)
+    d_y, d_topk_w = unsort_tokens_backward(d_out, y, s.inv_perm, topk_w)
+    d_logits = route_backward(d_topk_w, logits, topk_idx, topk_w)
+    d_x = sort_tokens_backward(d_rows, s.inv_perm)
     gateup = MatvecMXFP4(codes, scales, kind=MOE_WEIGHTS_GATEUP)
     h = gateup(x)                       # x [T <= 64, K] -> silu(gate) * up, [T, rows / 2]
 
@@ -107,6 +112,60 @@ def ffn_backward(d_out: torch.Tensor, x: torch.Tensor, gateup: torch.Tensor, w_g
     """The gradients of ffn_forward (moe_ffn_backward) from its inputs, the ``gateup`` it
     saved and ``act`` as given there; all of x's type."""
     return FfnGrads._make(_ext.ffn_backward(d_out, x, gateup, w_gateup, w_down, act, need_x, need_weights))
+
+
+# ------------------------------------------------------------------ tokens sorted by expert
+class SortedTokens(NamedTuple):
+    """Token rows in expert order.  The three integer arrays share a storage."""
+    rows: torch.Tensor                # [T*k, H]: by expert, then by token; what was dropped comes last, as zeros
+    scales: Optional[torch.Tensor]    # [T*k, S]: the rows' scales
+    offsets: torch.Tensor             # i32 [E + 1]: rows of expert e are [offsets[e], offsets[e + 1])
+    perm: torch.Tensor                # i32 [T*k]: assignment t*k + j of each row; -1 - it where dropped
+    inv_perm: torch.Tensor            # i32 [T, k]: row of each assignment; -1 - it where dropped
+
+
+def sort_tokens(x: torch.Tensor, topk_idx: torch.Tensor, n_experts: int, *,
+                scales: Optional[torch.Tensor] = None) -> SortedTokens:
+    """The rows of x [T, H] (any type, rows of a multiple of 16 bytes) in the order of the
+    experts that topk_idx (i32 [T, k]) names (moe_sort_tokens).  An index outside
+    [0, n_experts) drops its assignment.  ``scales`` [T, S] go with their rows."""
+    return SortedTokens._make(_ext.sort_tokens(x, topk_idx, n_experts, scales))
+
+
+def sort_tokens_backward(d_rows: torch.Tensor, inv_perm: torch.Tensor,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """d_x [T, H], the gradient of sort_tokens: each token's rows of d_rows [T*k, H] (bf16, f16
+    or f32) summed (moe_unsort_tokens)."""
+    return _ext.sort_tokens_backward(d_rows, inv_perm, out)
+
+
+def unsort_tokens(y: torch.Tensor, inv_perm: torch.Tensor, topk_w: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = sum_j topk_w[t, j] * y[inv_perm[t, j]] over the j that were not dropped
+    (moe_unsort_tokens): y [T*k, H] bf16, f16 or f32 in the order of sort_tokens, topk_w
+    f32 [T, k] (None: 1).  ``out`` may not overlap an input."""
+    return _ext.unsort_tokens(y, inv_perm, topk_w, out)
+
+
+class UnsortGrads(NamedTuple):
+    """Gradients of unsort_tokens; None for one that was not asked for."""
+    y: Optional[torch.Tensor]         # [T*k, H]; 0 in the rows of what was dropped
+    topk_w: Optional[torch.Tensor]    # f32 [T, k]; 0 where dropped
+
+
+def unsort_tokens_backward(d_out: torch.Tensor, y: Optional[torch.Tensor], inv_perm: torch.Tensor,
+                           topk_w: Optional[torch.Tensor] = None, *, need_y: bool = True,
+                           need_w: bool = True) -> UnsortGrads:
+    """The gradients of unsort_tokens from its arguments (moe_unsort_tokens_backward); without
+    ``need_w``, y may be None."""
+    return UnsortGrads._make(_ext.unsort_tokens_backward(d_out, y, inv_perm, topk_w, need_y, need_w))
+
+
+def route_backward(d_topk_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, *,
+                   gating: int = 0) -> torch.Tensor:
+    """d_logits f32 [T, E] from the gradient of route's weights and what route returned
+    (moe_route_backward): the indices as routed, before any were dropped."""
+    return _ext.route_backward(d_topk_w, logits, topk_idx, topk_w, gating)
 
 
 def dense_status() -> int:
