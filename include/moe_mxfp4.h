@@ -345,6 +345,7 @@ int moe_tensor_peak(int kind, int mmas_per_sm, double* tflops, moe_stream_t stre
 
 #define MOE_ACT_SILU 0
 #define MOE_ACT_GELU 1 /* tanh form                                                   */
+#define MOE_ACT_NONE 2 /* projections only                                            */
 
 /* moe_block_norm: the end of one block and the start of the next in one launch.
  *   n = block / sqrt(mean_H(block^2) + eps) * norm_weight   (n = block without norm_weight)
@@ -413,6 +414,36 @@ int moe_ffn_forward(const void* x, const void* w_gateup, const void* w_down, int
 int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, const void* w_gateup, const void* w_down,
                      int T, int H, int I, int act, int dtype, void* d_x, void* d_w_gateup, void* d_w_down,
                      void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_linear_forward: a projection with 16-bit weights and what follows it.
+ *   pre = x W^T + bias;  out = act(pre) + residual      f32, rounded once to out_dtype
+ *   x [T, K], weight [N, K] of dtype; bias f32 [N] or NULL; residual [T, N] of out_dtype or
+ *   NULL; out [T, N] of out_dtype (dtype, or MOE_DTYPE_F32: router logits, a residual stream
+ *   kept in f32), which may be `residual` itself and overlap nothing else.
+ *   act: MOE_ACT_NONE, _SILU or _GELU.  pre_out: f32 [T, N] for moe_linear_backward, or NULL;
+ *   NULL with MOE_ACT_NONE, whose backward does not need it.
+ *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
+ *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
+ *   256-byte aligned, contents irrelevant before and after.  Up to 16 tokens take a kernel
+ *   that streams the weights through mma.sync, more the tcgen05 GEMMs.
+ * The pages have no counterpart ("triton-kernels" README, "Kernels", lists the fused GEMMs
+ * of the feed-forward block).                                                        */
+size_t moe_linear_workspace_bytes(int T, int K, int N, int backward);
+int moe_linear_forward(const void* x, const void* weight, const float* bias, const void* residual, int T, int K, int N, int act,
+                       int dtype, int out_dtype, float* pre_out, void* out, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream);
+
+/* moe_linear_backward: the gradients of moe_linear_forward (the residual's is d_out itself).
+ *   dp = d_out act'(pre);  d_x = dp W;  d_weight = dp^T x;  d_bias = sum_t dp
+ *   d_out [T, N] of out_dtype; pre: what pre_out received, NULL exactly with MOE_ACT_NONE.
+ *   dp is formed in f32, summed into d_bias (f32 [N]) in a fixed order, and rounded to dtype
+ *   as the products' operand (in f16 with f16's range: scale d_out where it is small).
+ *   d_x [T, K], d_weight [N, K] of dtype, d_bias: overwritten; each may be NULL (not all).
+ *   weight may be NULL without d_x, x without d_weight.  No output may overlap an input.
+ *   workspace: moe_linear_workspace_bytes(T, K, N, 1) bytes, 256-byte aligned.       */
+int moe_linear_backward(const void* d_out, const void* x, const void* weight, const float* pre, int T, int K, int N, int act,
+                        int dtype, int out_dtype, void* d_x, void* d_weight, float* d_bias, void* workspace,
+                        size_t workspace_bytes, moe_stream_t stream);
 
 /* moe_sort_tokens: token rows into expert order, for experts of the caller's own (the
  * layer's permute step by itself), in the order of moe_build_tile_table: by expert, then by

@@ -5,8 +5,8 @@ The compute path is the CUDA library ``libmoe_mxfp4.so`` (C ABI in
 """
 
 from . import _lib  # noqa: F401
-from ._lib import (MOE_ACT_GELU, MOE_ACT_SILU, MOE_ROUTE_GATING_SIGMOID, MOE_ROUTE_GATING_SOFTMAX_ALL,  # noqa: F401
-                   MOE_WEIGHTS_DOWN, MOE_WEIGHTS_GATEUP)  # noqa: F401
+from ._lib import (MOE_ACT_GELU, MOE_ACT_NONE, MOE_ACT_SILU, MOE_ROUTE_GATING_SIGMOID,  # noqa: F401
+                   MOE_ROUTE_GATING_SOFTMAX_ALL, MOE_WEIGHTS_DOWN, MOE_WEIGHTS_GATEUP)  # noqa: F401
 from .build import build, LIB_PATH  # noqa: F401
 
 
@@ -18,7 +18,7 @@ def __getattr__(name):
         return getattr(api, name)
     if name in ("block_norm", "block_norm_backward", "BlockNormGrads", "ffn_forward", "ffn_backward", "FfnGrads",
                 "dense_status", "MatvecMXFP4", "sort_tokens", "sort_tokens_backward", "SortedTokens", "unsort_tokens",
-                "unsort_tokens_backward", "UnsortGrads", "route_backward"):
+                "linear_forward", "linear_backward", "LinearGrads", "unsort_tokens_backward", "UnsortGrads", "route_backward"):
         from . import dense
         value = globals()[name] = getattr(dense, name)  # found directly from now on
         return value

@@ -35,6 +35,7 @@ MOE_GATE_TOKEN = 2
 MOE_GATE_FULL = 3
 MOE_ACT_SILU = 0
 MOE_ACT_GELU = 1
+MOE_ACT_NONE = 2
 
 # every symbol the header declares, with its C signature
 _P = ctypes.c_void_p
@@ -73,6 +74,9 @@ SIGNATURES = {
     "moe_ffn_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "moe_ffn_forward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _S, _P]),
     "moe_ffn_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P]),
+    "moe_linear_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "moe_linear_forward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _S, _P]),
+    "moe_linear_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P]),
     "moe_sort_tokens": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "moe_unsort_tokens": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_unsort_tokens_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
@@ -153,6 +157,9 @@ moe_block_norm_backward = _call("moe_block_norm_backward")
 moe_ffn_workspace_bytes = _call("moe_ffn_workspace_bytes")
 moe_ffn_forward = _call("moe_ffn_forward")
 moe_ffn_backward = _call("moe_ffn_backward")
+moe_linear_workspace_bytes = _call("moe_linear_workspace_bytes")
+moe_linear_forward = _call("moe_linear_forward")
+moe_linear_backward = _call("moe_linear_backward")
 moe_sort_tokens = _call("moe_sort_tokens")
 moe_unsort_tokens = _call("moe_unsort_tokens")
 moe_unsort_tokens_backward = _call("moe_unsort_tokens_backward")

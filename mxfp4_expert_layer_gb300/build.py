@@ -29,7 +29,7 @@ EXT_SOURCE = "dense_binding.cpp"
 
 SOURCES = ["moe_route.cu", "moe_gemm.cu", "moe_aux.cu", "moe_api.cu", "moe_noalloc.cu", "moe_peak.cu",
            "moe_blocknorm.cu", "moe_thin.cu", "moe_dense_gemm.cu", "moe_dense_api.cu",
-           "moe_sort.cu"]
+           "moe_sort.cu", "moe_linear.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr"]

@@ -395,6 +395,87 @@ PyObject* matvec(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ projections
+// The type of out: x's, or f32.
+int out_code(at::ScalarType out, at::ScalarType type, int code) {
+  if (out == type) return code;
+  if (out == at::kFloat) return MOE_DTYPE_F32;
+  value_error(std::string("the result has x's type or float32, got ") + c10::toString(out));
+}
+
+// x, weight, bias, residual, act, out_f32 (None: residual's or out's type, else x's), save, out
+PyObject* linear_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &x = tensor("x", a[0]), &w = tensor("weight", a[1]);
+    const at::Tensor *bias = optional("bias", a[2]), *residual = optional("residual", a[3]), *given = optional("out", a[7]);
+    const int act = integer(a[4]);
+    const bool save = flag(a[6]) && act != MOE_ACT_NONE;
+    no_history({{"x", &x}, {"weight", &w}, {"bias", bias}, {"residual", residual}, {"out", given}});
+    matrix("x", x);
+    matrix("weight", w);
+    const int64_t T = x.size(0), K = x.size(1), N = w.size(0);
+    const at::ScalarType type = x.scalar_type();
+    const at::Device device = x.device();
+    const int code = dtype16(x);
+    const at::ScalarType otype = a[5] != Py_None ? (flag(a[5]) ? at::kFloat : type)
+                                 : residual      ? residual->scalar_type()
+                                 : given         ? given->scalar_type()
+                                                 : type;
+    const int ocode = out_code(otype, type, code);
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *px = need("x", &x, {T, K}, type, device), *pw = need("weight", &w, {N, K}, type, device),
+         *pb = need("bias", bias, {N}, at::kFloat, device), *pr = need("residual", residual, {T, N}, otype, device);
+    need("out", given, {T, N}, otype, device);
+    const int t = narrow(T), k = narrow(K), nn = narrow(N);
+    const size_t bytes = moe_linear_workspace_bytes(t, k, nn, 0);
+    at::Tensor out = given ? *given : empty({T, N}, otype, device), pre, ws;
+    if (save) pre = empty({T, N}, at::kFloat, device);
+    if (bytes) ws = empty({(int64_t)bytes}, at::kByte, device);
+    call("moe_linear_forward", device, [&](moe_stream_t s) {
+      return moe_linear_forward(px, pw, static_cast<const float*>(pb), pr, t, k, nn, act, code, ocode,
+                                static_cast<float*>(address(pre)), out.data_ptr(), address(ws), bytes, s);
+    });
+    return tuple({out, pre});
+  });
+}
+
+// d_out, x, weight, pre, act, need_x, need_weight, need_bias
+PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor &dout = tensor("d_out", a[0]), &x = tensor("x", a[1]), &w = tensor("weight", a[2]);
+    const at::Tensor* pre = optional("pre", a[3]);
+    const int act = integer(a[4]);
+    const bool need_x = flag(a[5]), need_w = flag(a[6]), need_b = flag(a[7]);
+    no_history({{"d_out", &dout}});
+    matrix("x", x);
+    matrix("weight", w);
+    const int64_t T = x.size(0), K = x.size(1), N = w.size(0);
+    const at::ScalarType type = x.scalar_type(), otype = dout.scalar_type();
+    const at::Device device = x.device();
+    const int code = dtype16(x), ocode = out_code(otype, type, code);
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *pd = need("d_out", &dout, {T, N}, otype, device), *px = need("x", &x, {T, K}, type, device),
+         *pw = need("weight", &w, {N, K}, type, device), *pp = need("pre", pre, {T, N}, at::kFloat, device);
+    const int t = narrow(T), k = narrow(K), nn = narrow(N);
+    const size_t bytes = moe_linear_workspace_bytes(t, k, nn, 1);
+    if (!bytes) refuse("moe_linear_backward", MOE_ERR_UNSUPPORTED_SHAPE);
+    at::Tensor d_x, d_w, d_b;
+    if (need_x) d_x = empty({T, K}, type, device);
+    if (need_w) d_w = empty({N, K}, type, device);
+    if (need_b) d_b = empty({N}, at::kFloat, device);
+    const at::Tensor ws = empty({(int64_t)bytes}, at::kByte, device);
+    call("moe_linear_backward", device, [&](moe_stream_t s) {
+      return moe_linear_backward(pd, px, pw, static_cast<const float*>(pp), t, k, nn, act, code, ocode, address(d_x),
+                                 address(d_w), static_cast<float*>(address(d_b)), ws.data_ptr(), bytes, s);
+    });
+    return tuple({d_x, d_w, d_b});
+  });
+}
+
 // ------------------------------------------------------------------ tokens sorted by expert
 int dtype_any(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? MOE_DTYPE_F32 : dtype16(t); }
 // Bytes of a row of a matrix.
@@ -537,6 +618,7 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 PyMethodDef methods[] = {FAST(block_norm),   FAST(block_norm_backward),
                          FAST(ffn_forward),  FAST(ffn_backward),
                          FAST(matvec),       FAST(sort_tokens),
+                         FAST(linear_forward), FAST(linear_backward),
                          FAST(sort_tokens_backward), FAST(unsort_tokens),
                          FAST(unsort_tokens_backward), FAST(route_backward),
                          {"set_error", set_error, METH_O, nullptr},

@@ -111,7 +111,7 @@ struct Vec8<float> {
 };
 
 // ------------------------------------------------------------------ activations
-constexpr int kActSilu = 0, kActGelu = 1;
+constexpr int kActSilu = 0, kActGelu = 1, kActNone = 2;
 
 // act(g) and, in the second form, its derivative too.  SiLU: g * s with s = 1 / (1 +
 // e^-g), derivative s (1 + g (1 - s)).  GELU (tanh form): with t = tanh(c (g + b g^3)),
@@ -260,20 +260,38 @@ struct ThinParams {
   int32_t* x_exp;           // MXFP4: and, behind it, the powers of two taken out of its tokens
   void* out;                // [T, n_out]
   float* gateup;            // f32 [T, 2 n_out] or null: the products before the activation
+  const void* residual;     // projections: [T, n_out] of out's type, or null
+  int out_f32;              // projections: out's type
 };
+cudaError_t launch_thin_linear(const ThinParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_matvec(const ThinParams& p, int dtype, bool gated, cudaStream_t stream);
 cudaError_t launch_thin16(const ThinParams& p, int dtype, bool gated, cudaStream_t stream);
 size_t matvec_workspace_bytes(int T, int K);
 uint32_t* thin_status_word();  // device addresses on the current device, or null
 uint32_t* dense_status_word();
 
+// ------------------------------------------------------------------ gradient of a projection's epilogue
+// dp = d_out act'(pre), rounded to 16 bits, and its column sums before that rounding.
+struct LinearGradParams {
+  const void* d_out;        // [T, N] of `dtype` or f32
+  const float* pre;         // f32 [T, N]; null: no activation
+  void* dp;                 // 16-bit [T, N] or null
+  float* d_bias;            // f32 [N] or null
+  float* partial;           // f32 [splits][N]
+  int T, N, act, splits;    // splits: blocks along T
+};
+int linear_grad_splits(int T, int N);
+cudaError_t launch_linear_grad(const LinearGradParams& p, int dtype, int out_dtype, cudaStream_t stream);
+
 // ------------------------------------------------------------------ dense GEMMs
 // C[m, n] = sum_k A[m, k] B[n, k] of 16-bit operands, each stored with K or with M / N
-// contiguous, and one of three epilogues.
+// contiguous, and one of several epilogues.
 constexpr int kDenseStore = 0;       // C in the operands' type
 constexpr int kDenseGateUp = 1;      // B rows: gate, then up; h = act(g) u, and g, u in f32 when asked for
 constexpr int kDenseGateUpGrad = 2;  // C = dh: dg, du from the saved g, u; and h again
 constexpr int kDenseProducts = 3;    // several products, each as kDenseStore
+constexpr int kDenseLinear = 4;      // out = act(C + bias) + residual; and C + bias in f32 when asked for
+constexpr int kDenseLinear32 = 5;    // the same with out and residual in f32
 constexpr int kDenseMaxSplits = 16;
 
 // One product: C [M, N] = A B^T.
@@ -292,7 +310,9 @@ struct DenseGemmParams {
   int group, long_n, lead;  // several products: how many, those of the long class, and the lead (see below)
   int act;
   void* out_h;              // gate/up grad: h [M, N]
-  float* gateup;            // f32 [M, 2 N]: written by gate/up (or null), read by its gradient
+  float* gateup;            // f32 [M, 2 N]: written by gate/up (or null), read by its gradient; linear: [M, N] or null
+  const float* bias;        // linear: f32 [N] or null
+  const void* residual;     // linear: [M, N] of out's type, or null
   float* partial;           // f32 [slices][tile rows][tile columns]
   uint64_t wait_ns;
 };

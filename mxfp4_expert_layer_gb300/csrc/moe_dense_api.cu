@@ -17,11 +17,12 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA
 static_assert(MOE_DTYPE_BF16 == kDtypeBf16 && MOE_DTYPE_F16 == kDtypeF16 && MOE_DTYPE_F32 == kDtypeF32, "dtype codes");
 static_assert(MOE_GATE_NONE == kGateNone && MOE_GATE_FEATURE == kGateFeature && MOE_GATE_TOKEN == kGateToken &&
                   MOE_GATE_FULL == kGateFull, "gate kinds");
-static_assert(MOE_ACT_SILU == kActSilu && MOE_ACT_GELU == kActGelu, "activations");
+static_assert(MOE_ACT_SILU == kActSilu && MOE_ACT_GELU == kActGelu && MOE_ACT_NONE == kActNone, "activations");
 
 constexpr int kMaxRows = 1 << 24;      // tokens of a call
 constexpr int kMaxNormDim = 8192;      // a row sits in one block's registers
 constexpr int kMaxFfnDim = 1 << 17;    // H and I of the feed-forward block
+constexpr int kMaxLinearOut = 1 << 20;   // N of a projection (K as kMaxFfnDim)
 constexpr int kMaxMovedBytes = 1 << 16;  // a row moved between token and expert order
 constexpr int kMaxScaleBytes = 1 << 12;  // and its scales
 constexpr int kMaxMatvecRows = 1 << 22, kMaxMatvecDim = 1 << 16;
@@ -95,6 +96,49 @@ int check_ffn(int T, int H, int I, int dtype, int act) {
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!dtype16(dtype) || (act != MOE_ACT_SILU && act != MOE_ACT_GELU)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
+}
+
+// A projection's workspace: dp [T, N] and the bias gradient's partial sums (backward), then
+// the partial sums of whichever product splits K.
+struct LinearLayout {
+  size_t sums, partial, total;
+};
+LinearLayout linear_layout(int T, int K, int N, bool backward) {
+  LinearLayout L{};
+  size_t part = 0;
+  auto need = [&](int m, int n, int k) {
+    const size_t b = dense_partial_bytes(m, n, k, kDenseStore, backward);
+    if (b > part) part = b;
+  };
+  if (backward) {
+    L.sums = align_up((size_t)T * N * 2, 256);
+    L.partial = align_up(L.sums + (size_t)linear_grad_splits(T, N) * N * sizeof(float), 256);
+    need(T, K, N);
+    need(N, K, T);
+  } else if (T > kThinTokens) {
+    need(T, N, K);
+  }
+  L.total = L.partial + align_up(part, 256);
+  return L;
+}
+int check_linear(int T, int K, int N, int dtype, int out_dtype, int act) {
+  if (T < 1 || T > kMaxRows || K < 8 || N < 8 || K % 8 || N % 8 || K > kMaxFfnDim || N > kMaxLinearOut)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!dtype16(dtype) || (out_dtype != dtype && out_dtype != MOE_DTYPE_F32)) return MOE_ERR_INVALID_ARG;
+  if (act != MOE_ACT_SILU && act != MOE_ACT_GELU && act != MOE_ACT_NONE) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+// An array, and whether it overlaps another.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+template <int N, int M>
+bool any_overlap(const Span (&a)[N], const Span (&b)[M]) {
+  for (const Span& x : a)
+    for (const Span& y : b)
+      if (x.p && y.p && overlap(x.p, x.bytes, y.p, y.bytes)) return true;
+  return false;
 }
 
 // Tokens and experts of a routing, as the layer's.
@@ -211,6 +255,113 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
   return launch_dense_products(q, n, a, b, dtype, s);
 }
 
+size_t moe_linear_workspace_bytes(int T, int K, int N, int backward) {
+  if (check_linear(T, K, N, MOE_DTYPE_BF16, MOE_DTYPE_BF16, MOE_ACT_NONE) != MOE_OK) return 0;
+  return linear_layout(T, K, N, backward != 0).total;
+}
+
+int moe_linear_forward(const void* x, const void* weight, const float* bias, const void* residual, int T, int K, int N, int act,
+                       int dtype, int out_dtype, float* pre_out, void* out, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream) {
+  const int st = check_linear(T, K, N, dtype, out_dtype, act);
+  if (st != MOE_OK) return st;
+  if (!x || !weight || !out) return MOE_ERR_INVALID_ARG;
+  const void* all[] = {x, weight, bias, residual, pre_out, out};
+  for (const void* q : all)
+    if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  if (pre_out && act == MOE_ACT_NONE) return MOE_ERR_INVALID_ARG;
+  const size_t size = out_dtype == MOE_DTYPE_F32 ? 4 : 2, cells = (size_t)T * N;
+  // (tiles are written while others still read; the residual is read by the thread that writes its element)
+  const Span in[] = {{x, (size_t)T * K * 2}, {weight, (size_t)N * K * 2}, {bias, (size_t)N * 4},
+                     {residual == out ? nullptr : residual, cells * size}, {pre_out, cells * 4}};
+  const Span written[] = {{out, cells * size}};
+  if (any_overlap(written, in)) return MOE_ERR_INVALID_ARG;
+  const Span read[] = {in[0], in[1], in[2], {residual, cells * size}}, kept[] = {{pre_out, cells * 4}};
+  if (any_overlap(kept, read)) return MOE_ERR_INVALID_ARG;
+  const LinearLayout L = linear_layout(T, K, N, false);
+  if (L.total && (!workspace || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T <= kThinTokens) {
+    ThinParams g{};
+    g.x = x;
+    g.w = weight;
+    g.bias = bias;
+    g.T = T;
+    g.K = K;
+    g.n_out = N;
+    g.tiles = ceil_div(N, kThinRows);
+    g.ku = ceil_div(K, 32);
+    g.act = act;
+    g.out = out;
+    g.gateup = pre_out;
+    g.residual = residual;
+    g.out_f32 = out_dtype == MOE_DTYPE_F32;
+    return cuda_status(launch_thin_linear(g, dtype, s));
+  }
+  DenseGemmParams g{};
+  g.g[0].M = T; g.g[0].N = N; g.g[0].K = K;
+  g.g[0].out = out;
+  g.act = act;
+  g.gateup = pre_out;
+  g.bias = bias;
+  g.residual = residual;
+  g.partial = ws_ptr<float>(workspace, L.partial);
+  return launch_dense_gemm(g, {x, T, K, 0}, {weight, N, K, 0}, out_dtype == MOE_DTYPE_F32 ? kDenseLinear32 : kDenseLinear,
+                           dtype, s);
+}
+
+int moe_linear_backward(const void* d_out, const void* x, const void* weight, const float* pre, int T, int K, int N, int act,
+                        int dtype, int out_dtype, void* d_x, void* d_weight, float* d_bias, void* workspace,
+                        size_t workspace_bytes, moe_stream_t stream) {
+  const int st = check_linear(T, K, N, dtype, out_dtype, act);
+  if (st != MOE_OK) return st;
+  if (!d_out || (!d_x && !d_weight && !d_bias) || (d_x && !weight) || (d_weight && !x)) return MOE_ERR_INVALID_ARG;
+  if ((act != MOE_ACT_NONE) != (pre != nullptr)) return MOE_ERR_INVALID_ARG;
+  const void* all[] = {d_out, x, weight, pre, d_x, d_weight, d_bias};
+  for (const void* q : all)
+    if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t cells = (size_t)T * N;
+  const Span in[] = {{d_out, cells * (out_dtype == MOE_DTYPE_F32 ? 4 : 2)}, {x, (size_t)T * K * 2}, {weight, (size_t)N * K * 2},
+                     {pre, cells * 4}};
+  const Span out[] = {{d_x, (size_t)T * K * 2}, {d_weight, (size_t)N * K * 2}, {d_bias, (size_t)N * 4}};
+  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  const LinearLayout L = linear_layout(T, K, N, true);
+  if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool products = d_x || d_weight;
+  const void* dp = d_out;  // without an activation, a 16-bit d_out is dp
+  LinearGradParams g{};
+  if (products && (pre || out_dtype == MOE_DTYPE_F32)) dp = g.dp = workspace;
+  if (g.dp || d_bias) {
+    g.d_out = d_out;
+    g.pre = pre;
+    g.d_bias = d_bias;
+    g.partial = ws_ptr<float>(workspace, L.sums);
+    g.T = T;
+    g.N = N;
+    g.act = act;
+    g.splits = linear_grad_splits(T, N);
+    if (launch_linear_grad(g, dtype, out_dtype, s) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (!products) return MOE_OK;
+  DenseGemmParams q{};
+  q.partial = ws_ptr<float>(workspace, L.partial);
+  DenseOperand a[kDenseGroup], b[kDenseGroup];
+  int n = 0;
+  auto product = [&](int m, int cols, int k, const DenseOperand& am, const DenseOperand& bm, void* to) {
+    if (!to) return;
+    q.g[n].M = m; q.g[n].N = cols; q.g[n].K = k;
+    q.g[n].out = to;
+    a[n] = am;
+    b[n++] = bm;
+  };
+  product(T, K, N, {dp, T, N, 0}, {weight, N, K, 1}, d_x);
+  product(N, K, T, {dp, T, N, 1}, {x, T, K, 1}, d_weight);
+  return launch_dense_products(q, n, a, b, dtype, s);
+}
+
 int moe_dense_status(int* status, moe_stream_t stream) {
   if (!status) return MOE_ERR_INVALID_ARG;
   uint32_t* words[] = {dense_status_word(), thin_status_word(), norm_status_word()};
@@ -292,12 +443,10 @@ int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, 
     if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
   // (rows are written while others are still read)
   const size_t n = (size_t)T * k;
-  const struct { const void* p; size_t bytes; } in[] = {{x, (size_t)T * row_bytes}, {scales, (size_t)T * scale_bytes},
-                                                        {topk_idx, n * 4}},
-      out[] = {{offsets, (size_t)(E + 1) * 4}, {perm, n * 4}, {inv_perm, n * 4}, {rows, n * row_bytes}, {row_scales, n * scale_bytes}};
-  for (const auto& o : out)
-    for (const auto& i : in)
-      if (o.p && i.p && overlap(o.p, o.bytes, i.p, i.bytes)) return MOE_ERR_INVALID_ARG;
+  const Span in[] = {{x, (size_t)T * row_bytes}, {scales, (size_t)T * scale_bytes}, {topk_idx, n * 4}};
+  const Span out[] = {{offsets, (size_t)(E + 1) * 4}, {perm, n * 4}, {inv_perm, n * 4}, {rows, n * row_bytes},
+                      {row_scales, n * scale_bytes}};
+  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   SortParams p{};
   p.idx = topk_idx;
   p.x = x;
@@ -322,8 +471,8 @@ int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_
   if (!y || !inv_perm || !out || !aligned(y, 16) || !aligned(inv_perm, 16) || !aligned(topk_w, 16) || !aligned(out, 16))
     return MOE_ERR_INVALID_ARG;
   const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
-  if (overlap(y, bytes * k, out, bytes) || overlap(inv_perm, n, out, bytes) || (topk_w && overlap(topk_w, n, out, bytes)))
-    return MOE_ERR_INVALID_ARG;
+  const Span in[] = {{y, bytes * k}, {inv_perm, n}, {topk_w, n}}, written[] = {{out, bytes}};
+  if (any_overlap(written, in)) return MOE_ERR_INVALID_ARG;
   UnsortParams p{};
   p.y = y;
   p.inv_perm = inv_perm;
@@ -344,11 +493,8 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
   for (const void* q : all)
     if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
   const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
-  const struct { const void* p; size_t bytes; } in[] = {{d_out, bytes}, {y, bytes * k}, {inv_perm, n}, {topk_w, n}},
-                                                out[] = {{d_y, bytes * k}, {d_topk_w, n}};
-  for (const auto& o : out)
-    for (const auto& i : in)
-      if (o.p && i.p && overlap(o.p, o.bytes, i.p, i.bytes)) return MOE_ERR_INVALID_ARG;
+  const Span in[] = {{d_out, bytes}, {y, bytes * k}, {inv_perm, n}, {topk_w, n}}, out[] = {{d_y, bytes * k}, {d_topk_w, n}};
+  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   UnsortBackwardParams q{};
   q.f.y = y;
   q.f.inv_perm = inv_perm;
@@ -371,9 +517,8 @@ int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t
   for (const void* q : need)
     if (!q || !aligned(q, 16)) return MOE_ERR_INVALID_ARG;
   const size_t all = (size_t)T * E * 4, n = (size_t)T * k * 4;
-  if (overlap(d_logits, all, d_topk_w, n) || overlap(d_logits, all, logits, all) || overlap(d_logits, all, topk_idx, n) ||
-      overlap(d_logits, all, topk_w, n))
-    return MOE_ERR_INVALID_ARG;
+  const Span in[] = {{d_topk_w, n}, {logits, all}, {topk_idx, n}, {topk_w, n}}, out[] = {{d_logits, all}};
+  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
   RouteBackwardParams p{};
   p.d_w = d_topk_w;
   p.logits = logits;

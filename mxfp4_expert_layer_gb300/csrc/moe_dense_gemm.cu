@@ -1,7 +1,8 @@
-// Dense GEMMs of the gated feed-forward block on the 5th-generation tensor cores:
+// Dense GEMMs of the gated feed-forward block and of projections on the 5th-generation tensor cores:
 //   forward   gu = x Wgu^T, h = act(g) u (one kernel);  out = h Wd^T
 //   backward  dh = dout Wd, with dg = dh u act'(g), du = dh act(g) and h again in its
 //             epilogue;  dx = dgu Wgu;  dWgu = dgu^T x;  dWd = dout^T h
+// and of projections:  out = act(x W^T + b) + r;  dx = dp W;  dW = dp^T x.
 // All are C[m, n] = sum_k A[m, k] B[n, k].  The operands are used as they are stored: a
 // matrix whose rows run along K is a K-major operand, one whose rows run along M or N
 // an MN-major one (both are forms of the same swizzled shared-memory tile), so nothing
@@ -360,6 +361,59 @@ __device__ __forceinline__ void epilogue_grad(const DenseGemmParams& p, const De
     }
 }
 
+// Sums of 16 columns of a projection -> act(v + bias) + residual, in out's type O (16 bits or
+// f32), and v + bias in f32 where it is kept.  The residual's element and out's may be one.
+template <typename O, int W>
+__device__ __forceinline__ void load_out(const O* p, int left, float (&f)[W]) {
+#pragma unroll
+  for (int j = 0; j < W; j += 8)
+    if (j < left) {
+      Vec8<O> t;
+      float v[8];
+      t.load(p + j, 0);
+      t.get(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j + i] = v[i];
+    }
+}
+template <typename O>
+__device__ __forceinline__ void store_out(O* p, const float* v, int n) {
+  if constexpr (std::is_same<O, float>::value) {
+    store8(p, v);
+    if (n >= 16) store8(p + 8, v + 8);
+  } else {
+    store16(p, v, n);
+  }
+}
+template <typename O, int W>
+__device__ __forceinline__ void epilogue_linear(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left,
+                                                float (&v)[W]) {
+  static_assert(W == 16, "a step of columns");
+  if (left <= 0) return;
+  O* out = reinterpret_cast<O*>(c.out) + (size_t)m * c.N + n;
+  float r[W] = {};
+  if (p.residual) load_out(reinterpret_cast<const O*>(p.residual) + (size_t)m * c.N + n, left, r);
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < W; j += 4)
+      if (j < left) {  // (left: a multiple of 8)
+        const float4 b = __ldcg(reinterpret_cast<const float4*>(p.bias + n + j));
+        v[j] += b.x; v[j + 1] += b.y; v[j + 2] += b.z; v[j + 3] += b.w;
+      }
+  }
+  if (p.gateup) store_out(p.gateup + (size_t)m * c.N + n, v, left);
+  if (p.act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = act_f<kActSilu>(v[j]);
+  } else if (p.act == kActGelu) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[j] = act_f<kActGelu>(v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) v[j] += r[j];
+  store_out(out, v, left);
+}
+
 // What happens to the sums of W columns of a row (`left` of them inside the matrix, in
 // eights): v, and for gate/up w the up sums.
 template <typename X, int MODE, int W>
@@ -370,6 +424,10 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, const DensePr
 #pragma unroll
     for (int j = 0; j < W; j += 16)
       if (j < left) store16(out + (size_t)m * c.N + n + j, v + j, left - j);
+  } else if constexpr (MODE == kDenseLinear) {
+    epilogue_linear<X>(p, c, m, n, left, v);
+  } else if constexpr (MODE == kDenseLinear32) {
+    epilogue_linear<float>(p, c, m, n, left, v);
   } else if constexpr (MODE == kDenseGateUp) {
     if (p.gateup) {
       float* gu = p.gateup + (size_t)m * 2 * c.N + n;
@@ -768,6 +826,7 @@ Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
 // The estimate is a function of the sizes alone; the last ones are kept per thread, since a
 // small product's launch would wait for its 3 us otherwise.
 Shape pick_shape(int M, int N, int K, int mode, bool b_mn) {
+  if (mode != kDenseGateUp) mode = kDenseStore;  // (what tiles cost apart from their epilogues)
   struct Entry {
     int M, N, K, key;
     Shape s;
@@ -883,6 +942,8 @@ template <typename X>
 cudaError_t launch_type(const DenseGemmParams& p, const Shape& s, int mode, cudaStream_t stream) {
   if (mode == kDenseGateUp) return launch_mode<X, kDenseGateUp>(p, s, stream);
   if (mode == kDenseGateUpGrad) return launch_mode<X, kDenseGateUpGrad>(p, s, stream);
+  if (mode == kDenseLinear) return launch_mode<X, kDenseLinear>(p, s, stream);
+  if (mode == kDenseLinear32) return launch_mode<X, kDenseLinear32>(p, s, stream);
   return launch_mode<X, kDenseStore>(p, s, stream);
 }
 

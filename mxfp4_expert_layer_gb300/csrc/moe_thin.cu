@@ -1,5 +1,5 @@
 // Products of a few tokens with many weight rows (decode): MXFP4 weights, and the
-// 16-bit weights of the dense feed-forward block.
+// 16-bit weights of the dense feed-forward block and of projections.
 //   plain  y[t, n] = sum_k x[t, k] W[n, k] (+ bias[n])
 //   gated  h[t, i] = act(g) u,  g and u the products with gate row i and up row i
 //
@@ -116,6 +116,40 @@ __device__ __forceinline__ void finish(const ThinParams& p, const float (&total)
     } else {
       out[row * p.n_out + f] = static_cast<X>(sum(o));
     }
+  }
+}
+
+// The same of a projection: act(sum + bias) + residual, in out's type, and sum + bias in f32
+// where it is kept.
+template <typename X, int NT>
+__device__ __forceinline__ void finish_linear(const ThinParams& p, const float (&total)[NT][4], float* red, int tile) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      red[(warp * NT * 8 + n * 8 + 2 * t + (c & 1)) * kFinishStride + g + 8 * (c >> 1)] = total[n][c];
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.T * kThinRows; i += kThinThreads) {
+    const int tok = i / kThinRows, o = i % kThinRows, f = tile * kThinRows + o;
+    if (f >= p.n_out) continue;
+    const size_t at = (size_t)tok * p.n_out + f;
+    float r = 0.f;
+    if (p.residual)
+      r = p.out_f32 ? __ldcg(reinterpret_cast<const float*>(p.residual) + at)
+                    : to_f32<X>(__ldcg(reinterpret_cast<const X*>(p.residual) + at));
+    float v = red[tok * kFinishStride + o];
+#pragma unroll
+    for (int w = 1; w < kThinWarps; ++w) v += red[(w * NT * 8 + tok) * kFinishStride + o];
+    if (p.bias) v += __ldcg(p.bias + f);
+    if (p.gateup) p.gateup[at] = v;
+    if (p.act == kActSilu) v = act_f<kActSilu>(v);
+    if (p.act == kActGelu) v = act_f<kActGelu>(v);
+    v += r;
+    if (p.out_f32)
+      reinterpret_cast<float*>(p.out)[at] = v;
+    else
+      reinterpret_cast<X*>(p.out)[at] = static_cast<X>(v);
   }
 }
 
@@ -540,7 +574,7 @@ __global__ void matvec_prepare_kernel(MatvecPrepareParams p) {
 // token 57 and 70 against 55, 0.96 of the measured copy rate), and so did three and four
 // blocks per SM with fewer units each.  Bound by HBM; at 2880 x 2880, where the two launches
 // take 13.0 us for 50 MB, by their starts and by 1.2 and 0.6 rounds of blocks.
-template <typename X, int NT, bool GATED, int ACT>
+template <typename X, int NT, bool GATED, int ACT, bool LINEAR = false>
 __global__ void __launch_bounds__(kThinThreads, 2) thin16_kernel(const __grid_constant__ ThinParams p) {
   constexpr int kUnits = 8;
   extern __shared__ __align__(128) uint8_t thin_smem[];
@@ -592,7 +626,10 @@ __global__ void __launch_bounds__(kThinThreads, 2) thin16_kernel(const __grid_co
     if (u >= u_end) break;
     load(u);
   }
-  finish<X, NT, GATED, ACT>(p, total, reinterpret_cast<float*>(thin_smem), tile);
+  if constexpr (LINEAR)
+    finish_linear<X, NT>(p, total, reinterpret_cast<float*>(thin_smem), tile);
+  else
+    finish<X, NT, GATED, ACT>(p, total, reinterpret_cast<float*>(thin_smem), tile);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -669,6 +706,16 @@ cudaError_t launch_matvec(const ThinParams& p, int dtype, bool gated, cudaStream
 cudaError_t launch_thin16(const ThinParams& p, int dtype, bool gated, cudaStream_t stream) {
   return dtype == kDtypeBf16 ? launch_act<false, __nv_bfloat16>(p, gated, stream)
                              : launch_act<false, __half>(p, gated, stream);
+}
+
+template <typename X, int NT>
+cudaError_t launch_thin_linear_t(const ThinParams& p, cudaStream_t stream) {
+  return launch_pdl(thin16_kernel<X, NT, false, kActNone, true>, dim3(p.tiles), dim3(kThinThreads), finish_bytes<NT>(), stream, p);
+}
+cudaError_t launch_thin_linear(const ThinParams& p, int dtype, cudaStream_t stream) {
+  if (dtype == kDtypeBf16)
+    return p.T <= 8 ? launch_thin_linear_t<__nv_bfloat16, 1>(p, stream) : launch_thin_linear_t<__nv_bfloat16, 2>(p, stream);
+  return p.T <= 8 ? launch_thin_linear_t<__half, 1>(p, stream) : launch_thin_linear_t<__half, 2>(p, stream);
 }
 
 size_t matvec_workspace_bytes(int T, int K) {

@@ -1,11 +1,13 @@
 """Torch-facing wrappers of the dense operators around the expert layer: the norms
-before and after a block, the gated feed-forward block, tokens sorted by expert and back,
-and products of a few tokens with MXFP4 weights.
+before and after a block, the gated feed-forward block, projections with bias, activation
+and residual, tokens sorted by expert and back, and products of a few tokens with MXFP4 weights.
 
     s, y = block_norm(z, r, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn)
     grads = block_norm_backward(ds, dy, z, s, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn)
     out, gu = ffn_forward(x, w_gateup, w_down, save=True)
     d_x, d_w_gateup, d_w_down = ffn_backward(d_out, x, gu, w_gateup, w_down)
+    out, pre = linear_forward(x, weight, bias, residual, act=MOE_ACT_GELU, save=True)
+    d_x, d_weight, d_bias = linear_backward(d_out, x, weight, pre, act=MOE_ACT_GELU)
     s = sort_tokens(x, topk_idx, E)     # s.rows: x by expert; experts of one's own give y [T*k, H]
     out = unsort_tokens(y, s.inv_perm, topk_w)
     d_y, d_topk_w = unsort_tokens_backward(d_out, y, s.inv_perm, topk_w)
@@ -112,6 +114,36 @@ def ffn_backward(d_out: torch.Tensor, x: torch.Tensor, gateup: torch.Tensor, w_g
     """The gradients of ffn_forward (moe_ffn_backward) from its inputs, the ``gateup`` it
     saved and ``act`` as given there; all of x's type."""
     return FfnGrads._make(_ext.ffn_backward(d_out, x, gateup, w_gateup, w_down, act, need_x, need_weights))
+
+
+# ------------------------------------------------------------------ projections
+def linear_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, *, act: int = L.MOE_ACT_NONE,
+                   out_dtype: Optional[torch.dtype] = None, save: bool = False, out: Optional[torch.Tensor] = None):
+    """out = act(x W^T + bias) + residual (moe_linear_forward): x [T, K] and weight [N, K] bf16
+    or f16, ``bias`` f32 [N]; ``residual`` and out [T, N] of x's type or f32 (``out_dtype``, or
+    as the residual is).  ``out`` may be ``residual``.  With ``save``, (out, pre): what the
+    activation was taken of, f32 [T, N], for linear_backward (None without an activation)."""
+    if out_dtype is not None and out_dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"out_dtype: x's type or float32, got {out_dtype}")
+    wide = None if out_dtype is None else out_dtype == torch.float32
+    r = _ext.linear_forward(x, weight, bias, residual, act, wide, save, out)
+    return r if save else r[0]
+
+
+class LinearGrads(NamedTuple):
+    """Gradients of linear_forward; None for one that was not asked for.  The residual's is d_out."""
+    x: Optional[torch.Tensor]        # [T, K]
+    weight: Optional[torch.Tensor]   # [N, K]
+    bias: Optional[torch.Tensor]     # f32 [N]
+
+
+def linear_backward(d_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, pre: Optional[torch.Tensor] = None, *,
+                    act: int = L.MOE_ACT_NONE, need_x: bool = True, need_weight: bool = True,
+                    need_bias: bool = True) -> LinearGrads:
+    """The gradients of linear_forward (moe_linear_backward) from its inputs, the ``pre`` it
+    saved and ``act`` as given there; d_out [T, N] of the type that out had."""
+    return LinearGrads._make(_ext.linear_backward(d_out, x, weight, pre, act, need_x, need_weight, need_bias))
 
 
 # ------------------------------------------------------------------ tokens sorted by expert
