@@ -366,6 +366,23 @@ int moe_block_norm(const void* block, const void* norm_weight, const void* gate,
                    float residual_scale, const void* next_weight, float eps, int T, int H, int dtype, int stream_dtype,
                    void* residual_out, void* out, moe_stream_t stream);
 
+/* moe_block_norm_8bit: moe_block_norm with `out` in 8 bits, for products with 8-bit
+ * activations and for moe_sort_tokens to move: E4M3 codes and scales of the f32 y,
+ *   code = E4M3(y / scale), nearest, ties to even
+ *   MOE_SCALE_MX: E8M0 bytes [T, H / 32], scale 2^(byte - 127), one for 32 values: the least
+ *     with |y| <= 448 scale (2^-126 at least), so that no value saturates.  H % 32 == 0.
+ *   MOE_SCALE_ROW: f32 [T], one for a row: max |y| / 448 (2^-126 at least).
+ * A group with an infinite or NaN y has a NaN scale (E8M0 255) and NaN codes.
+ *   codes [T, H] bytes, written, and scales: overlap nothing else.  residual_out, or NULL.
+ *   out: y rounded to dtype as well (for a router, say), or NULL.  next_weight is needed;
+ *   every other argument as for moe_block_norm.  Gradients: moe_block_norm_backward, the
+ *   rounding passing d_out through.                                                  */
+#define MOE_SCALE_MX 0
+#define MOE_SCALE_ROW 1
+int moe_block_norm_8bit(const void* block, const void* norm_weight, const void* gate, int gate_kind, const void* residual,
+                        float residual_scale, const void* next_weight, float eps, int T, int H, int dtype, int stream_dtype,
+                        int scale_kind, void* residual_out, uint8_t* codes, void* scales, void* out, moe_stream_t stream);
+
 /* moe_block_norm_backward: every gradient of moe_block_norm, from the same arguments.
  *   d_residual_out [T, H] of stream_dtype: gradient into s from what reads the stream
  *   later, or NULL for none; d_out [T, H] of dtype: NULL exactly when next_weight is (one

@@ -16,9 +16,10 @@ def __getattr__(name):
                 "build_tile_table", "tile_rows", "max_tiles"):
         from . import api
         return getattr(api, name)
-    if name in ("block_norm", "block_norm_backward", "BlockNormGrads", "ffn_forward", "ffn_backward", "FfnGrads",
-                "dense_status", "MatvecMXFP4", "sort_tokens", "sort_tokens_backward", "SortedTokens", "unsort_tokens",
-                "linear_forward", "linear_backward", "LinearGrads", "unsort_tokens_backward", "UnsortGrads", "route_backward"):
+    if name in ("block_norm", "block_norm_backward", "BlockNormGrads", "block_norm_8bit", "BlockNorm8", "ffn_forward",
+                "ffn_backward", "FfnGrads", "linear_forward", "linear_backward", "LinearGrads", "sort_tokens",
+                "sort_tokens_backward", "SortedTokens", "unsort_tokens", "unsort_tokens_backward", "UnsortGrads",
+                "route_backward", "dense_status", "MatvecMXFP4"):
         from . import dense
         value = globals()[name] = getattr(dense, name)  # found directly from now on
         return value

@@ -33,6 +33,8 @@ MOE_GATE_NONE = 0
 MOE_GATE_FEATURE = 1
 MOE_GATE_TOKEN = 2
 MOE_GATE_FULL = 3
+MOE_SCALE_MX = 0
+MOE_SCALE_ROW = 1
 MOE_ACT_SILU = 0
 MOE_ACT_GELU = 1
 MOE_ACT_NONE = 2
@@ -68,6 +70,7 @@ SIGNATURES = {
     "moe_get_device_status": (_I, [_P, _S, ctypes.POINTER(_I), _P]),
     "moe_tensor_peak": (_I, [_I, _I, ctypes.POINTER(ctypes.c_double), _P]),
     "moe_block_norm": (_I, [_P, _P, _P, _I, _P, _F, _P, _F, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_block_norm_8bit": (_I, [_P, _P, _P, _I, _P, _F, _P, _F, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
     "moe_block_norm_workspace_bytes": (_S, [_I, _I]),
     "moe_block_norm_backward": (_I, [_P, _P, _P, _P, _P, _I, _P, _F, _P, _F, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                                      _S, _P]),
@@ -152,6 +155,7 @@ moe_forward_launches = _call("moe_forward_launches")
 moe_get_device_status = _call("moe_get_device_status")
 moe_tensor_peak = _call("moe_tensor_peak")
 moe_block_norm = _call("moe_block_norm")
+moe_block_norm_8bit = _call("moe_block_norm_8bit")
 moe_block_norm_workspace_bytes = _call("moe_block_norm_workspace_bytes")
 moe_block_norm_backward = _call("moe_block_norm_backward")
 moe_ffn_workspace_bytes = _call("moe_ffn_workspace_bytes")

@@ -233,6 +233,43 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// block, residual, norm_weight, gate, residual_scale, next_weight, eps, scale kind, with_out
+PyObject* block_norm_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arguments(n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& block = tensor("block", a[0]);
+    const at::Tensor *residual = optional("residual", a[1]), *norm_w = optional("norm_weight", a[2]), *gate = optional("gate", a[3]);
+    const at::Tensor& next_w = tensor("next_weight", a[5]);
+    const float scale = (float)number(a[4]), eps = (float)number(a[6]);
+    const int kind = integer(a[7]);
+    const bool with_out = flag(a[8]);
+    no_history({{"block", &block}, {"residual", residual}, {"norm_weight", norm_w}, {"gate", gate}, {"next_weight", &next_w}});
+    matrix("block", block);
+    const int64_t T = block.size(0), H = block.size(1);
+    const at::ScalarType type = block.scalar_type();
+    const at::Device device = block.device();
+    const int code = dtype16(block);
+    const at::ScalarType stype = residual ? residual->scalar_type() : type;
+    const int scode = stream_dtype(stype, type, code);
+    const Gate g = gate_of(gate, T, H, type, device);
+    on_cuda(device);
+    const c10::cuda::CUDAGuard guard(device);
+    void *z = need("block", &block, {T, H}, type, device), *r = need("residual", residual, {T, H}, stype, device),
+         *wz = need("norm_weight", norm_w, {H}, type, device), *wn = need("next_weight", &next_w, {H}, type, device);
+    const int t = narrow(T), h = narrow(H);
+    const bool mx = kind == MOE_SCALE_MX;
+    const at::Tensor res = empty({T, H}, stype, device), codes = empty({T, H}, at::kFloat8_e4m3fn, device);
+    const at::Tensor scales = mx ? empty({T, H / 32}, at::kFloat8_e8m0fnu, device) : empty({T, 1}, at::kFloat, device);
+    at::Tensor out;
+    if (with_out) out = empty({T, H}, type, device);
+    call("moe_block_norm_8bit", device, [&](moe_stream_t s) {
+      return moe_block_norm_8bit(z, wz, g.ptr, g.kind, r, scale, wn, eps, t, h, code, scode, kind, res.data_ptr(),
+                                 static_cast<uint8_t*>(codes.data_ptr()), scales.data_ptr(), address(out), s);
+    });
+    return tuple({res, codes, scales, out});
+  });
+}
+
 // d_residual_out, d_out, block, residual_out, norm_weight, gate, residual_scale, next_weight, eps, has_residual
 PyObject* block_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arguments(n, 10)) return nullptr;
@@ -615,7 +652,7 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(block_norm),   FAST(block_norm_backward),
+PyMethodDef methods[] = {FAST(block_norm),   FAST(block_norm_backward), FAST(block_norm_8bit),
                          FAST(ffn_forward),  FAST(ffn_backward),
                          FAST(matvec),       FAST(sort_tokens),
                          FAST(linear_forward), FAST(linear_backward),

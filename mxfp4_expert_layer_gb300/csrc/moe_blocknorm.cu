@@ -5,7 +5,8 @@
 // next pre-norm's weight and g the gate (per feature, per token, or full):
 //   n = z / rms(z) * w              (n = z without a post-norm)
 //   s = round(a r + g n)            the stream, rounded to its stored type
-//   y = s / rms(s) * v              of the stored s, as the layer's own norm step does
+//   y = s / rms(s) * v              of the stored s, as the layer's own norm step does; as it
+//                                   is, or in 8 bits with a scale for 32 values or for a row
 // Backward, given ds' (into s from downstream) and dy:
 //   ds = ds' + rs (v dy - s rs mean(v dy s rs))    rs = 1 / rms(s)
 //   dr = a ds,  p = g ds,  dg = ds n,  dw = sum_t p z rz,  dv = sum_t dy s rs
@@ -85,15 +86,70 @@ __device__ __forceinline__ void set2(V& v, const f32x2 (&f)[4]) {
   v.set(t);
 }
 
+// ---- 8-bit outputs.  The largest magnitude of a group is taken over the bits (as integers, an
+// infinity is above every finite value and a NaN above that), and becomes the group's scale:
+//   MX: 2^e, e the least in [-126, 120] with largest <= 448 2^e, so that nothing saturates (the
+//       rule of the layer's own encoding; the floor of log2 would cut mantissas above 1.75);
+//   row: largest / 448, 2^-126 at least.
+// A group with an infinity or a NaN gets a NaN as its scale, and NaN codes.
+__device__ __forceinline__ uint32_t largest8(const f32x2 (&y)[4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = split2(y[i]);
+    m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+  }
+  return m;
+}
+// The factor that takes a group's values to codes; `scale` in the form that is stored.
+__device__ __forceinline__ float mx_scale(uint32_t largest, uint8_t& scale) {
+  const int e = max((int)(largest >> 23) - 127 - 8 + ((largest & 0x7FFFFFu) > 0x600000u), -126);
+  const bool finite = largest < 0x7F800000u;
+  scale = finite ? (uint8_t)(e + 127) : 255;
+  return finite ? pow2_int(-e) : __uint_as_float(0x7FFFFFFFu);
+}
+__device__ __forceinline__ float row_scale(uint32_t largest, float& scale) {
+  const float nan = __uint_as_float(0x7FFFFFFFu);
+  scale = largest < 0x7F800000u ? fmaxf(__uint_as_float(largest) * (1.f / 448.f), __uint_as_float(0x00800000u)) : nan;
+  return 1.f / scale;
+}
+// Two values as E4M3 (nearest, ties to even; 448 at most), the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ void store_codes(uint8_t* codes, size_t vec, const f32x2 (&y)[4], float to_code) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = split2(mul2(y[i], both(to_code)));
+    w[i] = e4m3x2(f.x, f.y);
+  }
+  reinterpret_cast<uint2*>(codes)[vec] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+// Eight values a lane, groups of four lanes (H is a multiple of 32: they are whole).
+__device__ __forceinline__ void store_mx(const BlockNormParams& p, bool on, size_t row, int v, size_t at, const f32x2 (&y)[4]) {
+  uint32_t m = largest8(y);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  uint8_t scale;
+  const float to_code = mx_scale(m, scale);
+  if (!on) return;
+  store_codes(p.codes, at, y, to_code);
+  if ((v & 3) == 0) reinterpret_cast<uint8_t*>(p.scales)[row * (p.H / 32) + (v >> 2)] = scale;
+}
+
 // GATE of a kernel: the gate kind (none and token are one) of a call that has every other
 // argument, or kAnyGate, which tests for what is absent.
 constexpr int kAnyGate = -1;
 
 // One block per row, eight values a thread: for few rows, where latency is all (one row of
 // 2880 bf16 values: 1.9 us a call in a graph).
-template <typename A, typename S, int GATE>
+template <typename A, typename S, int GATE, int OUT>
 __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ BlockNormParams p) {
   __shared__ float buf[2][32];
+  __shared__ uint32_t top[32];
   constexpr bool ANY = GATE == kAnyGate;
   const bool has_norm = !ANY || p.norm_w, has_next = !ANY || p.next_w, has_residual = !ANY || p.residual;
   const bool has_out = !ANY || p.residual_out;
@@ -163,14 +219,30 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
   const float2 f = split2(sq);
   float ss[1] = {f.x + f.y};
   block_sums(ss, buf[1]);
-  if (!on) return;
+  if (OUT == kOut16 && !on) return;
   const f32x2 rs = both(rsqrtf(ss[0] / (float)p.H + p.eps));
+  if (OUT != kOut16 && !on) wn.zero();
   get2(wn, w);
 #pragma unroll
   for (int k = 0; k < 4; ++k) z[k] = mul2(mul2(z[k], rs), w[k]);
-  zr.raw = make_uint4(0, 0, 0, 0);
-  set2(zr, z);
-  zr.store(p.out, at);
+  if (OUT == kOut16 || (p.out && on)) {
+    zr.raw = make_uint4(0, 0, 0, 0);
+    set2(zr, z);
+    zr.store(p.out, at);
+  }
+  if constexpr (OUT == kOutMx) store_mx(p, on, row, v, at, z);
+  if constexpr (OUT == kOutRow) {
+    uint32_t m = __reduce_max_sync(0xffffffffu, on ? largest8(z) : 0u);
+    if (blockDim.x > 32) {
+      if ((v & 31) == 0) top[v >> 5] = m;
+      __syncthreads();
+      m = __reduce_max_sync(0xffffffffu, (v & 31) < (int)(blockDim.x >> 5) ? top[v & 31] : 0u);
+    }
+    float scale;
+    const float to_code = row_scale(m, scale);
+    if (on) store_codes(p.codes, at, z, to_code);
+    if (v == 0) reinterpret_cast<float*>(p.scales)[row] = scale;
+  }
 }
 
 // The rows that a block reads in turn, brought to shared memory by bulk copies a few rows
@@ -452,11 +524,12 @@ __global__ void __launch_bounds__(512)
 // the backward; the weights stay in registers as they were loaded.  Two reductions a row
 // (the second is of the rounded stream), each a barrier of the group's own.  Bound by HBM,
 // past the first rows' latency: 4096 x 2880 bf16 17.4 us, 5.4 TB/s (a copy: 6.7).
-template <typename A, typename S, int GATE>
+template <typename A, typename S, int GATE, int OUT>
 __global__ void __launch_bounds__(512, 2)
     block_norm_rows_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float sums[2][16];
+  __shared__ uint32_t top[16];  // (with the barriers of sums, whoever writes it again is past all its readers)
   __shared__ uint64_t full_bar[kNormMaxGroups][3];
   const bool token = GATE == kGateNone && p.gate_kind == kGateToken;
   const int nvec = p.H / 8, per = rows.threads, group = threadIdx.x / per, v = threadIdx.x - group * per;
@@ -539,8 +612,23 @@ __global__ void __launch_bounds__(512, 2)
     get2(wn, w);
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] = mul2(mul2(z[k], rs), w[k]);
-    set2(t, z);
-    if (on) t.store(p.out, at);
+    if (OUT == kOut16 || p.out) {
+      set2(t, z);
+      if (on) t.store(p.out, at);
+    }
+    if constexpr (OUT == kOutMx) store_mx(p, on, row, v, at, z);
+    if constexpr (OUT == kOutRow) {
+      uint32_t m = __reduce_max_sync(0xffffffffu, on ? largest8(z) : 0u);
+      if (warps > 1) {
+        if (lane == 0) top[group * warps + warp] = m;
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(per) : "memory");
+        m = __reduce_max_sync(0xffffffffu, lane < warps ? top[group * warps + lane] : 0u);
+      }
+      float scale;
+      const float to_code = row_scale(m, scale);
+      if (on) store_codes(p.codes, at, z, to_code);
+      if (leader) reinterpret_cast<float*>(p.scales)[row] = scale;
+    }
     if (++stage == rows.stages) {
       stage = 0;
       phase ^= 1;
@@ -595,7 +683,7 @@ RowCopies make_rows(int H, int n, const void* const* src, const int* size) {
   return r;
 }
 
-template <typename A, typename S>
+template <typename A, typename S, int OUT>
 cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
   const bool every = p.norm_w && p.next_w && p.residual && p.residual_out;
   const int gate = !every ? kAnyGate : p.gate_kind == kGateToken ? kGateNone : p.gate_kind;
@@ -618,15 +706,15 @@ cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
       return e != cudaSuccess ? e
                               : launch_pdl(kern, dim3(blocks), dim3(groups * r.threads), groups * r.stages * r.total, stream, p, r);
     };
-    if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature>, o[0]);
-    if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull>, o[1]);
-    return launch(block_norm_rows_kernel<A, S, kGateNone>, o[2]);
+    if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature, OUT>, o[0]);
+    if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull, OUT>, o[1]);
+    return launch(block_norm_rows_kernel<A, S, kGateNone, OUT>, o[2]);
   }
   auto launch = [&](auto kern) { return launch_pdl(kern, dim3(p.T), dim3(row_threads), 0, stream, p); };
-  if (gate == kAnyGate) return launch(block_norm_kernel<A, S, kAnyGate>);
-  if (gate == kGateFeature) return launch(block_norm_kernel<A, S, kGateFeature>);
-  if (gate == kGateFull) return launch(block_norm_kernel<A, S, kGateFull>);
-  return launch(block_norm_kernel<A, S, kGateNone>);
+  if (gate == kAnyGate) return launch(block_norm_kernel<A, S, kAnyGate, OUT>);
+  if (gate == kGateFeature) return launch(block_norm_kernel<A, S, kGateFeature, OUT>);
+  if (gate == kGateFull) return launch(block_norm_kernel<A, S, kGateFull, OUT>);
+  return launch(block_norm_kernel<A, S, kGateNone, OUT>);
 }
 
 template <typename A, typename S>
@@ -682,11 +770,17 @@ int block_norm_backward_blocks(int T, int H) {
   return need < kNormBlocks ? need : kNormBlocks;
 }
 
-cudaError_t launch_block_norm(const BlockNormParams& p, int dtype, int stream_dtype, cudaStream_t stream) {
+template <int OUT>
+cudaError_t forward_out(const BlockNormParams& p, int dtype, int stream_dtype, cudaStream_t stream) {
   if (dtype == kDtypeBf16)
-    return stream_dtype == kDtypeF32 ? forward_t<__nv_bfloat16, float>(p, stream)
-                                     : forward_t<__nv_bfloat16, __nv_bfloat16>(p, stream);
-  return stream_dtype == kDtypeF32 ? forward_t<__half, float>(p, stream) : forward_t<__half, __half>(p, stream);
+    return stream_dtype == kDtypeF32 ? forward_t<__nv_bfloat16, float, OUT>(p, stream)
+                                     : forward_t<__nv_bfloat16, __nv_bfloat16, OUT>(p, stream);
+  return stream_dtype == kDtypeF32 ? forward_t<__half, float, OUT>(p, stream) : forward_t<__half, __half, OUT>(p, stream);
+}
+cudaError_t launch_block_norm(const BlockNormParams& p, int dtype, int stream_dtype, int out_kind, cudaStream_t stream) {
+  if (out_kind == kOutMx) return forward_out<kOutMx>(p, dtype, stream_dtype, stream);
+  if (out_kind == kOutRow) return forward_out<kOutRow>(p, dtype, stream_dtype, stream);
+  return forward_out<kOut16>(p, dtype, stream_dtype, stream);
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& q, int dtype, int stream_dtype,

@@ -151,8 +151,13 @@ struct BlockNormParams {
   int gate_kind, T, H;
   float scale, eps;
   void* residual_out;       // s [T, H] (stream type) or null
-  void* out;                // y [T, H]
+  void* out;                // y [T, H]; beside an 8-bit output, or null
+  uint8_t* codes;           // 8-bit output: [T, H] E4M3
+  void* scales;             // its scales: E8M0 [T, H / 32] or f32 [T]
 };
+// The form of the norm's output: y as it is, or E4M3 codes with an E8M0 scale for 32 values, or
+// with an f32 scale for a row.
+constexpr int kOut16 = 0, kOutMx = 1, kOutRow = 2;
 struct BlockNormBackwardParams {
   BlockNormParams f;          // residual unused; residual_out is the forward's s, read
   const void* d_residual_out; // [T, H] (stream type) or null
@@ -165,7 +170,7 @@ struct BlockNormBackwardParams {
   float* partial;             // f32 [rows of partials][3][H]: next, norm, feature gate
   int blocks;                 // persistent blocks = rows of partials
 };
-cudaError_t launch_block_norm(const BlockNormParams& p, int dtype, int stream_dtype, cudaStream_t stream);
+cudaError_t launch_block_norm(const BlockNormParams& p, int dtype, int stream_dtype, int out_kind, cudaStream_t stream);
 int block_norm_backward_groups(int H);
 int block_norm_backward_blocks(int T, int H);
 uint32_t* norm_status_word();

@@ -390,7 +390,41 @@ int moe_block_norm(const void* block, const void* norm_weight, const void* gate,
   p.residual = residual;
   p.residual_out = residual_out;
   p.out = out;
-  return cuda_status(launch_block_norm(p, dtype, stream_dtype, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_block_norm(p, dtype, stream_dtype, kOut16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_block_norm_8bit(const void* block, const void* norm_weight, const void* gate, int gate_kind, const void* residual,
+                        float residual_scale, const void* next_weight, float eps, int T, int H, int dtype, int stream_dtype,
+                        int scale_kind, void* residual_out, uint8_t* codes, void* scales, void* out, moe_stream_t stream) {
+  const int st = check_norm(block, norm_weight, gate, gate_kind, next_weight, residual_scale, eps, T, H, dtype,
+                            stream_dtype);
+  if (st != MOE_OK) return st;
+  if (scale_kind != MOE_SCALE_MX && scale_kind != MOE_SCALE_ROW) return MOE_ERR_INVALID_ARG;
+  if (scale_kind == MOE_SCALE_MX && H % kMxBlock) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!next_weight || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  const void* all[] = {residual, residual_out, codes, scales, out};
+  for (const void* q : all)
+    if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  // (rows are written while others are still read; s and y go where their own element was read)
+  const size_t cells = (size_t)T * H, size = stream_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const size_t scale_bytes = scale_kind == MOE_SCALE_MX ? cells / kMxBlock : (size_t)T * 4;
+  const size_t gate_bytes = gate_kind == MOE_GATE_FEATURE ? (size_t)H * 2 : gate_kind == MOE_GATE_TOKEN ? (size_t)T * 4 : cells * 2;
+  const Span in[] = {{block, cells * 2}, {norm_weight, (size_t)H * 2}, {gate, gate_bytes}, {residual, cells * size},
+                     {next_weight, (size_t)H * 2}};
+  const Span eight[] = {{codes, cells}, {scales, scale_bytes}}, s_out[] = {{residual_out, cells * size}}, y_out[] = {{out, cells * 2}};
+  const Span not_s[] = {in[0], in[1], in[2], {residual == residual_out ? nullptr : residual, cells * size}, in[4]};
+  const Span not_y[] = {{block == out ? nullptr : block, cells * 2}, in[1], in[2], in[3], in[4]};
+  if (any_overlap(eight, in) || any_overlap(s_out, not_s) || any_overlap(y_out, not_y) || any_overlap(eight, s_out) ||
+      any_overlap(eight, y_out) || any_overlap(s_out, y_out) || overlap(codes, cells, scales, scale_bytes))
+    return MOE_ERR_INVALID_ARG;
+  BlockNormParams p = norm_params(block, norm_weight, gate, gate_kind, next_weight, residual_scale, eps, T, H);
+  p.residual = residual;
+  p.residual_out = residual_out;
+  p.out = out;
+  p.codes = codes;
+  p.scales = scales;
+  return cuda_status(launch_block_norm(p, dtype, stream_dtype, scale_kind == MOE_SCALE_MX ? kOutMx : kOutRow,
+                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_block_norm_workspace_bytes(int T, int H) {

@@ -3,6 +3,7 @@ before and after a block, the gated feed-forward block, projections with bias, a
 and residual, tokens sorted by expert and back, and products of a few tokens with MXFP4 weights.
 
     s, y = block_norm(z, r, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn)
+    s, codes, scales, y = block_norm_8bit(z, r, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn, with_out=True)
     grads = block_norm_backward(ds, dy, z, s, norm_weight=wp, gate=g, residual_scale=a, next_weight=wn)
     out, gu = ffn_forward(x, w_gateup, w_down, save=True)
     d_x, d_w_gateup, d_w_down = ffn_backward(d_out, x, gu, w_gateup, w_down)
@@ -66,6 +67,31 @@ def block_norm(block: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
     block's type, or f32 [T, 1].  ``residual_out`` may be ``residual``, ``out`` may be
     ``block``.  Small results of one type share a storage."""
     return _ext.block_norm(block, residual, norm_weight, gate, residual_scale, next_weight, eps, residual_out, out)
+
+
+class BlockNorm8(NamedTuple):
+    """What block_norm_8bit returns."""
+    residual: torch.Tensor            # s [T, H]
+    codes: torch.Tensor               # float8_e4m3fn [T, H]: out / scale
+    scales: torch.Tensor              # "mx": float8_e8m0fnu [T, H / 32]; "row": f32 [T, 1]
+    out: Optional[torch.Tensor]       # [T, H] of block's type, with ``with_out``
+
+
+_SCALES = {"mx": L.MOE_SCALE_MX, "row": L.MOE_SCALE_ROW}
+
+
+def block_norm_8bit(block: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                    norm_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                    residual_scale: float = 1.0, next_weight: torch.Tensor, eps: float = 1e-5, scales: str = "mx",
+                    with_out: bool = False) -> BlockNorm8:
+    """block_norm with out in 8 bits (moe_block_norm_8bit): E4M3 codes, and scales that are powers
+    of two for 32 values each ("mx", H a multiple of 32) or one for a row ("row").  codes and
+    scales are as sort_tokens takes them.  ``with_out``: out in block's type as well.  Its
+    gradients are block_norm_backward's, the rounding passing d_out through."""
+    if scales not in _SCALES:
+        raise ValueError(f'scales: "mx" or "row", got {scales!r}')
+    return BlockNorm8._make(_ext.block_norm_8bit(block, residual, norm_weight, gate, residual_scale, next_weight, eps,
+                                                 _SCALES[scales], with_out))
 
 
 class BlockNormGrads(NamedTuple):
