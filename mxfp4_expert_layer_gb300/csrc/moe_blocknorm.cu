@@ -524,8 +524,12 @@ __global__ void __launch_bounds__(512)
 // the backward; the weights stay in registers as they were loaded.  Two reductions a row
 // (the second is of the rounded stream), each a barrier of the group's own.  Bound by HBM,
 // past the first rows' latency: 4096 x 2880 bf16 17.4 us, 5.4 TB/s (a copy: 6.7).
-template <typename A, typename S, int GATE, int OUT>
-__global__ void __launch_bounds__(512, 2)
+//
+// TIGHT: 56 registers a thread, for widths at which that lets one more block reside on an SM
+// (2880: 4096 rows bf16 with a feature gate 24.4 -> 19.0 us, 8-bit codes with a row scale 29.9 ->
+// 20.5); elsewhere the compiler's 64 are better (8192 x 4096, f32 stream: 63 us against 76).
+template <typename A, typename S, int GATE, int OUT, bool TIGHT>
+__global__ void __maxnreg__(TIGHT ? 56 : 64)
     block_norm_rows_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float sums[2][16];
@@ -688,11 +692,9 @@ cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
   const bool every = p.norm_w && p.next_w && p.residual && p.residual_out;
   const int gate = !every ? kAnyGate : p.gate_kind == kGateToken ? kGateNone : p.gate_kind;
   const int row_threads = (p.H / 8 + 31) / 32 * 32, groups = min(512 / row_threads, kNormMaxGroups);
-  // many rows: persistent blocks, as many per SM as 56 registers a thread allow, which f16
-  // takes at most and bf16 without a feature or full gate does (fewer rows are done sooner by a
-  // block each).  With such a gate bf16 takes 58 to 64: at some widths (2880 is one) one block
-  // per SM fewer is resident than this asks for, and the last ones run in a second round.
-  // Rows of calls without every argument, and of more than 4096 values, have a block each.
+  // many rows: persistent blocks, as many per SM as 56 registers a thread allow (fewer rows are
+  // done sooner by a block each).  Rows of calls without every argument, and of more than 4096
+  // values, have a block each.
   const int per_sm = groups > 0 ? 1152 / (groups * row_threads) : 0, blocks = per_sm * device_sms();
   if (every && groups > 0 && p.T >= 4 * groups * blocks) {
     const void* src[3] = {p.block, p.residual, gate == kGateFull ? p.gate : nullptr};
@@ -700,15 +702,19 @@ cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
     RowCopies r = make_rows(p.H, 3, src, size);
     r.threads = row_threads;
     r.stages = min(3, kNormSmem / per_sm / (groups * r.total));
-    static SmemOptIn o[3];
     auto launch = [&](auto kern, SmemOptIn& opt_in) {
       const cudaError_t e = opt_in.ensure(kern, kNormSmem);
       return e != cudaSuccess ? e
                               : launch_pdl(kern, dim3(blocks), dim3(groups * r.threads), groups * r.stages * r.total, stream, p, r);
     };
-    if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature, OUT>, o[0]);
-    if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull, OUT>, o[1]);
-    return launch(block_norm_rows_kernel<A, S, kGateNone, OUT>, o[2]);
+    auto pick = [&](auto tight) {
+      constexpr bool TIGHT = decltype(tight)::value;
+      static SmemOptIn o[3];
+      if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature, OUT, TIGHT>, o[0]);
+      if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull, OUT, TIGHT>, o[1]);
+      return launch(block_norm_rows_kernel<A, S, kGateNone, OUT, TIGHT>, o[2]);
+    };
+    return per_sm * groups * row_threads > 1024 ? pick(std::true_type{}) : pick(std::false_type{});
   }
   auto launch = [&](auto kern) { return launch_pdl(kern, dim3(p.T), dim3(row_threads), 0, stream, p); };
   if (gate == kAnyGate) return launch(block_norm_kernel<A, S, kAnyGate, OUT>);

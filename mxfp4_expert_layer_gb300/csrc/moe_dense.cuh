@@ -204,6 +204,7 @@ struct RouteBackwardParams {
   int T, k, E, gating;
   float* d_logits;          // [T, E]
 };
+uint32_t* sort_status_word();
 cudaError_t launch_sort(const SortParams& p, cudaStream_t stream);
 cudaError_t launch_unsort(const UnsortParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_unsort_backward(const UnsortBackwardParams& q, int dtype, cudaStream_t stream);

@@ -15,35 +15,71 @@ namespace moe {
 
 namespace {
 
-constexpr int kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32;
 constexpr int kKeys = kMaxExperts + 1;  // the experts, and what is dropped
+constexpr uint64_t kCopyWaitNs = 1000000000ull;  // a wait for a row may take 1 s
+
+__device__ uint32_t g_sort_status;  // bits as in the layer's status word
 
 __device__ __forceinline__ int key_of(int e, int E) { return e >= 0 && e < E ? e : E; }
 
-// The order of a routing by one block: each warp counts the keys of a contiguous run of
-// assignments, the counts become the warps' first places, and each warp places its run.
-__global__ void __launch_bounds__(kOrderThreads) order_kernel(const __grid_constant__ SortParams p) {
+// ------------------------------------------------------------------ many assignments: the order
+// By one cluster.  Each warp counts the keys of a contiguous run of assignments; the blocks
+// tell one another their sums, from which each knows where its keys begin; and each warp places
+// its run.  What bounds it is the latency of these few steps (16384 assignments: 5.6 us for one
+// block, see the launcher for the cluster), which the rows' copies of the next launch hide in
+// part: it starts with this one and has its first rows in before the order is there.
+constexpr int kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32, kOrderBlocks = 8;
+
+__global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThreads)
+    order_kernel(const __grid_constant__ SortParams p) {
   __shared__ int count[kOrderWarps][kKeys + 2];
+  __shared__ int sums[kOrderBlocks][kKeys + 3];  // written by every block of the cluster
   __shared__ int first[kKeys];
   __shared__ int warp_total[kOrderWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, keys = p.E + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, keys = p.E + 1, rank = blockIdx.x;
   for (int i = tid; i < kOrderWarps * (kKeys + 2); i += kOrderThreads) (&count[0][0])[i] = 0;
   __syncthreads();
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int n = p.T * p.k, run = ceil_div(ceil_div(n, kOrderWarps), 32) * 32;
-  const int begin = min(n, warp * run), end = min(n, begin + run);
+  ptx::cluster_arrive_release();  // (every block has started: its memory may be written)
+  const int n = p.T * p.k, warps = kOrderBlocks * kOrderWarps, run = ceil_div(ceil_div(n, warps), 32) * 32;
+  const int begin = min((long long)n, (long long)(rank * kOrderWarps + warp) * run), end = min(n, begin + run);
   for (int a = begin + lane; a < end; a += 32) atomicAdd(&count[warp][key_of(__ldcg(p.idx + a), p.E)], 1);
   __syncthreads();
-  // the places of key e begin behind the lower keys; those of a warp behind the lower warps
+  // a warp's places of a key begin behind those of the lower warps
   int total = 0;
-  if (tid < keys)
+  if (tid < keys) {
+    int c[kOrderWarps];
+#pragma unroll
+    for (int w = 0; w < kOrderWarps; ++w) c[w] = count[w][tid];
+#pragma unroll
     for (int w = 0; w < kOrderWarps; ++w) {
-      const int c = count[w][tid];
       count[w][tid] = total;
-      total += c;
+      total += c[w];
     }
-  int scan = total;
+  }
+  __syncwarp();
+  ptx::cluster_wait_acquire();
+  if (tid < keys) {
+    const uint32_t mine = ptx::smem_u32(&sums[rank][tid]);
+#pragma unroll
+    for (int b = 0; b < kOrderBlocks; ++b)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ptx::mapa_shared(mine, b)), "r"(total) : "memory");
+  }
+  __syncwarp();
+  ptx::cluster_arrive_release();
+  ptx::cluster_wait_acquire();
+  // behind the lower blocks', and all of them behind those of the lower keys
+  int before = 0, all = 0;
+  if (tid < keys) {
+#pragma unroll
+    for (int b = 0; b < kOrderBlocks; ++b) {
+      const int s = sums[b][tid];
+      if (b < rank) before += s;
+      all += s;
+    }
+  }
+  int scan = all;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, scan, d);
@@ -52,10 +88,10 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const __grid_const
   if (lane == 31) warp_total[warp] = scan;
   __syncthreads();
   if (tid < keys) {
-    int before = scan - total;
-    for (int w = 0; w < warp; ++w) before += warp_total[w];
-    first[tid] = before;
-    p.offsets[tid] = before;
+    int at = scan - all;
+    for (int w = 0; w < warp; ++w) at += warp_total[w];
+    first[tid] = at + before;
+    if (rank == 0) p.offsets[tid] = at;
   }
   __syncthreads();
   for (int a0 = begin; a0 < end; a0 += 32) {
@@ -63,15 +99,15 @@ __global__ void __launch_bounds__(kOrderThreads) order_kernel(const __grid_const
     const bool on = a < end;
     const int key = on ? key_of(__ldcg(p.idx + a), p.E) : -1;
     const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int rank = __popc(same & ((1u << lane) - 1));
+    const int ahead = __popc(same & ((1u << lane) - 1));
     if (on) {
-      const int place = first[key] + count[warp][key] + rank;
+      const int place = first[key] + count[warp][key] + ahead;
       const bool kept = key < p.E;
       p.perm[place] = kept ? a : -1 - a;
       p.inv_perm[a] = kept ? place : -1 - place;
     }
     __syncwarp();
-    if (on && rank == 0) count[warp][key] += __popc(same);
+    if (on && ahead == 0) count[warp][key] += __popc(same);
     __syncwarp();
   }
 }
@@ -91,60 +127,195 @@ __device__ __forceinline__ void move_scales(const SortParams& p, size_t to, size
     move_units<unsigned char>(p.row_scales, p.scales, to, from, p.scale_bytes, kept);
 }
 
-// One block per token: its row is read once and written to its k places.
-__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ SortParams p) {
-  __shared__ int place[kMaxTopK];
+// Zeros to a dropped assignment's row, by a warp.
+__device__ __forceinline__ void zero_row(const SortParams& p, size_t at) {
+  uint4* row = reinterpret_cast<uint4*>(p.rows) + at * (p.row_bytes / 16);
+  for (int v = threadIdx.x & 31; v < p.row_bytes / 16; v += 32) row[v] = make_uint4(0, 0, 0, 0);
+}
+
+// The rows: each warp takes tokens in turn, whose rows come to its ring in shared memory by one
+// bulk copy and leave it by one for each of their places, issued by as many lanes.  The rows
+// are asked for before the order of the launch before is there.  (x was complete when that
+// launch passed its own wait, before which this one cannot start.)
+constexpr int kGatherStages = 2;
+__global__ void __launch_bounds__(128) gather_kernel(const __grid_constant__ SortParams p) {
+  extern __shared__ __align__(128) uint8_t gather_smem[];
+  __shared__ uint64_t full_bar[4][kGatherStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  uint8_t* const ring = gather_smem + (size_t)warp * kGatherStages * p.row_bytes;
+  uint64_t* const bar = full_bar[warp];
+  const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x);
+  uint8_t* rows = reinterpret_cast<uint8_t*>(p.rows);
+  const int t0 = blockIdx.x * warps + warp, step = gridDim.x * warps;
+  auto issue = [&](int s, int t) {
+    ptx::mbar_arrive_expect_tx(&bar[s], p.row_bytes);
+    ptx::bulk_load(ring + (size_t)s * p.row_bytes, x + (size_t)t * p.row_bytes, p.row_bytes, &bar[s]);
+  };
+  if (lane == 0) {
+    for (int s = 0; s < kGatherStages; ++s) ptx::mbar_init(&bar[s], 1);
+    ptx::fence_mbar_init();
+    for (int s = 0; s < kGatherStages; ++s)
+      if ((long long)t0 + (long long)s * step < p.T) issue(s, t0 + s * step);
+  }
+  __syncwarp();
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const size_t t = blockIdx.x;
-  if (threadIdx.x < p.k) place[threadIdx.x] = __ldcg(p.inv_perm + t * p.k + threadIdx.x);
-  __syncthreads();
-  const int vecs = p.row_bytes / 16;
-  uint4* rows = reinterpret_cast<uint4*>(p.rows);
-  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-    const uint4 r = __ldcg(reinterpret_cast<const uint4*>(p.x) + t * vecs + v);
-    for (int j = 0; j < p.k; ++j) {
-      const int at = place[j];
-      if (at >= 0)
-        rows[(size_t)at * vecs + v] = r;
-      else
-        rows[(size_t)(-1 - at) * vecs + v] = make_uint4(0, 0, 0, 0);
+  int s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  int next = t0 < p.T && lane < p.k ? __ldcg(p.inv_perm + (size_t)t0 * p.k + lane) : 0;
+  for (long long t = t0; t < p.T; t += step) {
+    const int at = next;
+    if (t + step < p.T && lane < p.k) next = __ldcg(p.inv_perm + (size_t)(t + step) * p.k + lane);
+    if (ok && !ptx::mbar_wait_bounded(&bar[s], phase, kCopyWaitNs)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+    const bool on = lane < p.k;
+    if (on && at >= 0 && ok) {
+      ptx::bulk_store(rows + (size_t)at * p.row_bytes, ring + (size_t)s * p.row_bytes, p.row_bytes);
+      ptx::bulk_commit();
+    }
+    unsigned gone = __ballot_sync(0xffffffffu, on && at < 0);
+    for (; gone; gone &= gone - 1) zero_row(p, -1 - __shfl_sync(0xffffffffu, at, __ffs(gone) - 1));
+    if (p.scale_bytes)
+      for (int j = 0; j < p.k; ++j) {
+        const int to = __shfl_sync(0xffffffffu, at, j);
+        move_scales(p, to >= 0 ? to : -1 - to, t, to >= 0);
+      }
+    if (on) ptx::bulk_wait_read();
+    __syncwarp();
+    if (lane == 0 && ok && t + (long long)kGatherStages * step < p.T) issue(s, (int)(t + kGatherStages * step));
+    if (++s == kGatherStages) {
+      s = 0;
+      phase ^= 1;
     }
   }
+  ptx::bulk_wait_all();
+  // a copy waited for in vain may still land: report, and stay until it surely has
+  if (!ok && lane == 0) {
+    report_status(&g_sort_status, kStatusTimeoutMain);
+    const uint64_t since = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - since < kCopyWaitNs / 50) __nanosleep(1000);
+  }
+}
+
+// ------------------------------------------------------------------ few assignments
+// One launch: a block per token finds its assignments' places by counting those before them,
+// all N of them for each, while its row comes in.  The last block finds the offsets.
+constexpr int kFewAssignments = 2048, kFewThreads = 128, kFewHeld = 4;
+__global__ void __launch_bounds__(kFewThreads) sort_few_kernel(const __grid_constant__ SortParams p) {
+  __shared__ __align__(16) uint32_t order[kFewAssignments];  // (key, place) as one number
+  __shared__ int place[kMaxTopK];
+  __shared__ int count[kKeys + 31];
+  const int n = p.T * p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool last = (int)blockIdx.x == p.T;
+  const size_t t = blockIdx.x;
+  const int vecs = p.row_bytes / 16;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x) + t * vecs;
+  uint4 held[kFewHeld];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (!last) {
+#pragma unroll
+    for (int i = 0; i < kFewHeld; ++i)
+      if (tid + i * kFewThreads < vecs) held[i] = __ldcg(x + tid + i * kFewThreads);
+  } else {
+    for (int i = tid; i < kKeys + 31; i += kFewThreads) count[i] = 0;
+  }
+  const int padded = (n + 127) / 128 * 128;
+  for (int a = tid; a < padded; a += kFewThreads)
+    order[a] = a < n ? (uint32_t)key_of(__ldcg(p.idx + a), p.E) << 16 | (uint32_t)a : 0xFFFFFFFFu;
+  __syncthreads();
+  if (last) {
+    for (int a = tid; a < n; a += kFewThreads) atomicAdd(&count[order[a] >> 16], 1);
+    __syncthreads();
+    if (warp == 0) {
+      int before = 0;
+      for (int e0 = 0; e0 <= p.E; e0 += 32) {
+        int scan = count[e0 + lane];
+        const int own = scan;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, scan, d);
+          if (lane >= d) scan += o;
+        }
+        if (e0 + lane <= p.E) p.offsets[e0 + lane] = before + scan - own;
+        before += __shfl_sync(0xffffffffu, scan, 31);
+      }
+    }
+    return;
+  }
+  for (int j = warp; j < p.k; j += kFewThreads / 32) {
+    const int a = (int)t * p.k + j;
+    const uint32_t mine = order[a];
+    int less = 0;
+    for (int b = 4 * lane; b < padded; b += 128) {
+      const uint4 o = *reinterpret_cast<const uint4*>(order + b);
+      less += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
+    }
+    less = __reduce_add_sync(0xffffffffu, less);
+    const bool kept = (int)(mine >> 16) < p.E;
+    if (lane == 0) {
+      place[j] = kept ? less : -1 - less;
+      p.perm[less] = kept ? a : -1 - a;
+      p.inv_perm[a] = kept ? less : -1 - less;
+    }
+  }
+  __syncthreads();
+  uint4* rows = reinterpret_cast<uint4*>(p.rows);
+  auto put = [&](int v, const uint4& r) {
+    for (int j = 0; j < p.k; ++j) {
+      const int at = place[j];
+      rows[(size_t)(at >= 0 ? at : -1 - at) * vecs + v] = at >= 0 ? r : make_uint4(0, 0, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kFewHeld; ++i)
+    if (tid + i * kFewThreads < vecs) put(tid + i * kFewThreads, held[i]);
+  for (int v = tid + kFewHeld * kFewThreads; v < vecs; v += kFewThreads) put(v, __ldcg(x + v));
   if (p.scale_bytes)
-    for (int j = threadIdx.x >> 5; j < p.k; j += blockDim.x >> 5) {
+    for (int j = warp; j < p.k; j += kFewThreads / 32) {
       const int at = place[j];
       move_scales(p, at >= 0 ? at : -1 - at, t, at >= 0);
     }
 }
 
+// ------------------------------------------------------------------ back to tokens
 // Row of assignment (t, j) that takes part, or -1; where it was dropped `zero` is its row.
 __device__ __forceinline__ int row_of(int at, int n) { return at >= 0 && at < n ? at : -1; }
 
-// out[t] = sum_j w[t, j] y[place(t, j)], eight columns a thread.
+// Few tokens: a block for each, a thread for eight columns of it at a time, loads of this many
+// rows in flight together.
+constexpr int kRowsAhead = 4;
+
+// out[t] = sum_j w[t, j] y[place(t, j)]
 template <typename A>
-__global__ void __launch_bounds__(256) unsort_kernel(const __grid_constant__ UnsortParams p) {
+__global__ void __launch_bounds__(512) unsort_kernel(const __grid_constant__ UnsortParams p) {
   __shared__ int row[kMaxTopK];
   __shared__ float weight[kMaxTopK];
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const size_t t = blockIdx.x;
-  if (threadIdx.x < p.k) {
-    row[threadIdx.x] = row_of(__ldcg(p.inv_perm + t * p.k + threadIdx.x), p.T * p.k);
-    weight[threadIdx.x] = p.w ? __ldcg(p.w + t * p.k + threadIdx.x) : 1.f;
+  const int vecs = p.H / 8, tid = threadIdx.x;
+  if (tid < p.k) {
+    row[tid] = row_of(__ldcg(p.inv_perm + t * p.k + tid), p.T * p.k);
+    weight[tid] = p.w ? __ldcg(p.w + t * p.k + tid) : 1.f;
   }
   __syncthreads();
-  const int vecs = p.H / 8;
-  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+  for (int v = tid; v < vecs; v += blockDim.x) {
     float sum[8] = {};
-    for (int j = 0; j < p.k; ++j) {
-      if (row[j] < 0) continue;
-      Vec8<A> r;
-      float f[8];
-      r.load(p.y, (size_t)row[j] * vecs + v);
-      r.get(f);
+    for (int j0 = 0; j0 < p.k; j0 += kRowsAhead) {
+      Vec8<A> r[kRowsAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = fmaf(weight[j], f[i], sum[i]);
+      for (int j = 0; j < kRowsAhead; ++j)
+        if (j0 + j < p.k && row[j0 + j] >= 0) r[j].load(p.y, (size_t)row[j0 + j] * vecs + v);
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) {
+        if (j0 + j >= p.k || row[j0 + j] < 0) continue;
+        float f[8];
+        r[j].get(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(weight[j0 + j], f[i], sum[i]);
+      }
     }
     Vec8<A> o;
     o.set(sum);
@@ -152,47 +323,263 @@ __global__ void __launch_bounds__(256) unsort_kernel(const __grid_constant__ Uns
   }
 }
 
-// dy[place(t, j)] = w[t, j] dout[t] and dw[t, j] = <dout[t], y[place(t, j)]>: one block per token.
+// dy[place(t, j)] = w[t, j] dout[t] and dw[t, j] = <dout[t], y[place(t, j)]>, up to kRowsAhead j
+// at a time; the block's shares of their dot products are joined in a fixed order.
 template <typename A>
-__global__ void __launch_bounds__(256) unsort_backward_kernel(const __grid_constant__ UnsortBackwardParams q) {
-  __shared__ float part[8];
+__global__ void __launch_bounds__(512) unsort_backward_kernel(const __grid_constant__ UnsortBackwardParams q) {
+  __shared__ int place[kMaxTopK];
+  __shared__ float weight[kMaxTopK];
+  __shared__ float part[2][16][kRowsAhead];
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const UnsortParams& p = q.f;
   const size_t t = blockIdx.x;
-  const int vecs = p.H / 8, n = p.T * p.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j = 0; j < p.k; ++j) {
-    const int at = __ldcg(p.inv_perm + t * p.k + j), row = row_of(at, n), to = row_of(at >= 0 ? at : -1 - at, n);
-    const float w = row < 0 ? 0.f : p.w ? __ldcg(p.w + t * p.k + j) : 1.f;
-    float dot = 0.f;
-    for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-      Vec8<A> r;
-      float d[8], f[8];
-      r.load(q.d_out, t * vecs + v);
-      r.get(d);
-      if (q.d_w && row >= 0) {
-        r.load(p.y, (size_t)row * vecs + v);
-        r.get(f);
+  const int vecs = p.H / 8, n = p.T * p.k, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+  if (tid < p.k) {
+    place[tid] = __ldcg(p.inv_perm + t * p.k + tid);
+    weight[tid] = p.w ? __ldcg(p.w + t * p.k + tid) : 1.f;
+  }
+  __syncthreads();
+  for (int j0 = 0, turn = 0; j0 < p.k; j0 += kRowsAhead, turn ^= 1) {
+    float dot[kRowsAhead] = {};
+    for (int v = tid; v < vecs; v += blockDim.x) {
+      Vec8<A> d, r[kRowsAhead];
+      d.load(q.d_out, t * vecs + v);
+      if (q.d_w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot = fmaf(d[i], f[i], dot);
+        for (int j = 0; j < kRowsAhead; ++j) {
+          const int row = j0 + j < p.k ? row_of(place[j0 + j], n) : -1;
+          if (row >= 0) r[j].load(p.y, (size_t)row * vecs + v);
+        }
       }
-      if (q.d_y && to >= 0) {
+      float g[8];
+      d.get(g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = row < 0 ? 0.f : w * d[i];
-        r.set(d);
-        r.store(q.d_y, (size_t)to * vecs + v);
+      for (int j = 0; j < kRowsAhead; ++j) {
+        if (j0 + j >= p.k) break;
+        const int at = place[j0 + j], row = row_of(at, n), own = row_of(at >= 0 ? at : -1 - at, n);
+        float f[8];
+        if (q.d_w && row >= 0) {
+          r[j].get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], f[i], dot[j]);
+        }
+        if (q.d_y && own >= 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = row < 0 ? 0.f : weight[j0 + j] * g[i];
+          d.set(f);
+          d.store(q.d_y, (size_t)own * vecs + v);
+        }
       }
     }
     if (!q.d_w) continue;
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-    if (lane == 0) part[warp] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < (int)blockDim.x / 32; ++i) dot += part[i];
-      q.d_w[t * p.k + j] = dot;
+    static_assert(kRowsAhead == 4, "the lanes halve four sums twice");
+    // the lanes halve the sums they carry: lane l ends with the sum of j = l / 8
+    const bool up = lane & 16, up2 = lane & 8;
+    const float a0 = (up ? dot[2] : dot[0]) + __shfl_xor_sync(0xffffffffu, up ? dot[0] : dot[2], 16);
+    const float a1 = (up ? dot[3] : dot[1]) + __shfl_xor_sync(0xffffffffu, up ? dot[1] : dot[3], 16);
+    float s = (up2 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, up2 ? a0 : a1, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    if ((lane & 7) == 0) part[turn][warp][lane >> 3] = s;
+    __syncthreads();  // (two buffers in turn: whoever writes one again is past the barrier between)
+    if (tid < kRowsAhead && j0 + tid < p.k) {
+      float v = part[turn][0][tid];
+      for (int i = 1; i < warps; ++i) v += part[turn][i][tid];
+      q.d_w[t * p.k + j0 + tid] = v;
     }
-    __syncthreads();
+  }
+}
+
+// Many tokens: persistent blocks whose first warp brings the rows in by bulk copies, a stage of
+// the ring at a time: the same columns of up to kGroupRows of a token's rows (and, backward, of
+// dout).  The other warps take a stage's columns, eight a thread.  Loads by the threads
+// themselves stopped at 5.6 TB/s whatever the blocks' size and number (8192 x 2 x 4096 f16:
+// 35.8 to 60 us): too few of them are in flight.
+constexpr int kGroupRows = 8, kRowThreads = 512, kMaxRowStages = 8;
+struct RowPlan {
+  int cols, chunks, groups;      // columns of a stage; column chunks of a row; groups of a token's rows
+  int row_bytes, stage_bytes, stages;
+};
+struct RowStage {
+  int place[kGroupRows];         // as in inv_perm
+  float weight[kGroupRows];
+};
+
+// Sums of eight values over the warp: lane l returns that of value l / 4.
+__device__ __forceinline__ float sums8(float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 4, bit = 16; n >= 1; n >>= 1, bit >>= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+    }
+  }
+  float t = v[0];
+  t += __shfl_xor_sync(0xffffffffu, t, 2);
+  t += __shfl_xor_sync(0xffffffffu, t, 1);
+  return t;
+}
+
+template <typename A, bool BACKWARD>
+__global__ void __launch_bounds__(kRowThreads + 32, 2)
+    token_rows_kernel(const __grid_constant__ UnsortBackwardParams q, const __grid_constant__ RowPlan r) {
+  extern __shared__ __align__(128) uint8_t rows_smem[];
+  __shared__ uint64_t full_bar[kMaxRowStages], empty_bar[kMaxRowStages];
+  __shared__ RowStage info[kMaxRowStages];
+  __shared__ float part[2][kRowThreads / 32][kGroupRows];
+  const UnsortParams& p = q.f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.k, takers = (blockDim.x >> 5) - 1;
+  const bool need_y = !BACKWARD || q.d_w;
+  // a sum over a token's groups is a column's, one over the columns a row's: that runs inside
+  const int outer = BACKWARD ? r.groups : r.chunks, inner = BACKWARD ? r.chunks : r.groups;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < r.stages; ++s) {
+      ptx::mbar_init(&full_bar[s], 1);
+      ptx::mbar_init(&empty_bar[s], takers);
+    }
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  int s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  auto advance = [&]() {
+    if (++s == r.stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  };
+  if (warp == 0) {
+    // ------------------------------------------------------------ the rows' copies
+    auto places = [&](long long t, int& at, float& w) {
+      at = -1;
+      w = 0.f;
+      if (t >= p.T || lane >= p.k) return;
+      at = __ldcg(p.inv_perm + t * p.k + lane);
+      w = p.w ? __ldcg(p.w + t * p.k + lane) : 1.f;
+    };
+    int at, at_next;
+    float w, w_next;
+    places(blockIdx.x, at_next, w_next);
+    for (long long t = blockIdx.x; t < p.T && ok; t += gridDim.x) {
+      at = at_next;
+      w = w_next;
+      places(t + gridDim.x, at_next, w_next);
+      for (int o = 0; o < outer && ok; ++o)
+        for (int i = 0; i < inner; ++i) {
+          const int g = BACKWARD ? o : i, c = BACKWARD ? i : o, here = min(kGroupRows, p.k - g * kGroupRows), j = lane;
+          const int my_at = __shfl_sync(0xffffffffu, at, (g * kGroupRows + j) & 31);
+          const float my_w = __shfl_sync(0xffffffffu, w, (g * kGroupRows + j) & 31);
+          const bool live = j < here && row_of(my_at, n) >= 0 && need_y;
+          const int copies = __popc(__ballot_sync(0xffffffffu, live)) + (BACKWARD ? 1 : 0);
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&empty_bar[s], phase ^ 1, kCopyWaitNs));
+          if (!ok) break;
+          const int col = c * r.cols, bytes = min(r.cols, p.H - col) * (int)sizeof(A);
+          uint8_t* stage = rows_smem + (size_t)s * r.stage_bytes;
+          if (j < here) {
+            info[s].place[j] = my_at;
+            info[s].weight[j] = my_w;
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&full_bar[s], copies * bytes);
+          __syncwarp();
+          if (live)
+            ptx::bulk_load(stage + (size_t)j * r.row_bytes, reinterpret_cast<const A*>(p.y) + (size_t)my_at * p.H + col, bytes,
+                           &full_bar[s]);
+          if (BACKWARD && lane == 31)
+            ptx::bulk_load(stage + (size_t)here * r.row_bytes, reinterpret_cast<const A*>(q.d_out) + (size_t)t * p.H + col, bytes,
+                           &full_bar[s]);
+          advance();
+        }
+    }
+  } else {
+    // ------------------------------------------------------------ their use
+    // (after a time-out they go on to the end without waiting, so that their barriers are met;
+    // the places are checked against the rows where they are used)
+    const int v = threadIdx.x - 32;
+    int turn = 0;
+    for (long long t = blockIdx.x; t < p.T; t += gridDim.x)
+      for (int o = 0; o < outer; ++o) {
+        float sum[8] = {};  // forward: of a chunk, over the groups; backward: each row's share, over the chunks
+        for (int i = 0; i < inner; ++i) {
+          const int g = BACKWARD ? o : i, c = BACKWARD ? i : o, here = min(kGroupRows, p.k - g * kGroupRows);
+          if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full_bar[s], phase, kCopyWaitNs));
+          const int col = c * r.cols + 8 * v;
+          const bool on = 8 * v < r.cols && col < p.H;
+          const uint8_t* stage = rows_smem + (size_t)s * r.stage_bytes;
+          const RowStage& at_stage = info[s];
+          if (on && !BACKWARD) {
+            for (int j = 0; j < here; ++j) {
+              if (row_of(at_stage.place[j], n) < 0) continue;
+              Vec8<A> x;
+              float f[8];
+              x.load_shared(stage + (size_t)j * r.row_bytes, v);
+              x.get(f);
+              const float w = at_stage.weight[j];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, f[e], sum[e]);
+            }
+          }
+          if (on && BACKWARD) {
+            Vec8<A> x;
+            float d[8];
+            x.load_shared(stage + (size_t)here * r.row_bytes, v);
+            x.get(d);
+#pragma unroll
+            for (int j = 0; j < kGroupRows; ++j) {
+              if (j >= here) break;
+              const int at = at_stage.place[j], row = row_of(at, n), own = row_of(at >= 0 ? at : -1 - at, n);
+              float f[8];
+              if (need_y && row >= 0) {
+                x.load_shared(stage + (size_t)j * r.row_bytes, v);
+                x.get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[j] = fmaf(d[e], f[e], sum[j]);
+              }
+              if (q.d_y && own >= 0) {
+                const float w = at_stage.weight[j];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = row < 0 ? 0.f : w * d[e];
+                x.set(f);
+                x.store(q.d_y, ((size_t)own * p.H + col) / 8);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&empty_bar[s]);
+          advance();
+          if (on && !BACKWARD && i == inner - 1) {
+            Vec8<A> x;
+            x.set(sum);
+            x.store(p.out, ((size_t)t * p.H + col) / 8);
+          }
+        }
+        if (BACKWARD && q.d_w) {
+          const int here = min(kGroupRows, p.k - o * kGroupRows);
+          const float mine = sums8(sum);
+          if ((lane & 3) == 0) part[turn][warp - 1][lane >> 2] = mine;
+          asm volatile("bar.sync 1, %0;" ::"r"(32 * takers) : "memory");
+          if (v < here) {
+            float total = part[turn][0][v];
+            for (int e = 1; e < takers; ++e) total += part[turn][e][v];
+            q.d_w[t * p.k + o * kGroupRows + v] = total;
+          }
+          turn ^= 1;  // (whoever writes a buffer again is past the barrier between)
+        }
+      }
+  }
+  if (!ok && lane == 0) {
+    // a copy waited for in vain may still land: report, and stay until it surely has
+    report_status(&g_sort_status, kStatusTimeoutMain);
+    const uint64_t since = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - since < kCopyWaitNs / 50) __nanosleep(1000);
   }
 }
 
@@ -254,20 +641,68 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
   }
 }
 
+// Threads of a block that takes one token.
+int token_threads(int H) { return min(512, ceil_div(H / 8, 32) * 32); }
+
+// The ring of the persistent blocks: stages of at most 48 KB, of at least two per block.
+constexpr int kRowSmem = 222 * 1024, kRowOther = 3 * 1024, kMaxStage = 48 * 1024;  // (other: what else a block takes)
+template <typename A, bool BACKWARD>
+cudaError_t launch_rows(const UnsortBackwardParams& q, cudaStream_t stream, bool& taken) {
+  const int H = q.f.H, k = q.f.k, rows = min(k, kGroupRows) + (BACKWARD ? 1 : 0);
+  const int most = min(8 * kRowThreads, kMaxStage / (rows * (int)sizeof(A)) / 8 * 8);
+  RowPlan r{};
+  r.chunks = ceil_div(H, most);
+  r.cols = ceil_div(H / 8, r.chunks) * 8;
+  r.groups = ceil_div(k, kGroupRows);
+  r.row_bytes = r.cols * (int)sizeof(A);
+  r.stage_bytes = rows * r.row_bytes;
+  const int threads = ceil_div(r.cols / 8, 32) * 32 + 32;
+  const int per_sm = max(1, min(min(16, 2 * (kRowThreads + 32) / threads), kRowSmem / (2 * r.stage_bytes + kRowOther)));
+  r.stages = min(kMaxRowStages, (kRowSmem / per_sm - kRowOther) / r.stage_bytes);
+  const int blocks = per_sm * device_sms();
+  taken = q.f.T >= 2 * blocks;
+  if (!taken) return cudaSuccess;
+  auto kern = token_rows_kernel<A, BACKWARD>;
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in.ensure(kern, kRowSmem);
+  return e != cudaSuccess ? e : launch_pdl(kern, dim3(blocks), dim3(threads), r.stages * r.stage_bytes, stream, q, r);
+}
+
 template <typename A>
 cudaError_t unsort_t(const UnsortParams& p, cudaStream_t stream) {
-  return launch_pdl(unsort_kernel<A>, dim3(p.T), dim3(256), 0, stream, p);
+  UnsortBackwardParams q{};
+  q.f = p;
+  bool taken = false;
+  const cudaError_t e = launch_rows<A, false>(q, stream, taken);
+  return taken || e != cudaSuccess ? e : launch_pdl(unsort_kernel<A>, dim3(p.T), dim3(token_threads(p.H)), 0, stream, p);
 }
 template <typename A>
 cudaError_t unsort_backward_t(const UnsortBackwardParams& q, cudaStream_t stream) {
-  return launch_pdl(unsort_backward_kernel<A>, dim3(q.f.T), dim3(256), 0, stream, q);
+  bool taken = false;
+  const cudaError_t e = launch_rows<A, true>(q, stream, taken);
+  return taken || e != cudaSuccess ? e
+                                   : launch_pdl(unsort_backward_kernel<A>, dim3(q.f.T), dim3(token_threads(q.f.H)), 0, stream, q);
 }
 
 }  // namespace
 
+uint32_t* sort_status_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_sort_status) == cudaSuccess ? static_cast<uint32_t*>(p) : nullptr;
+}
+
 cudaError_t launch_sort(const SortParams& p, cudaStream_t stream) {
-  const cudaError_t e = launch_pdl(order_kernel, dim3(1), dim3(kOrderThreads), 0, stream, p);
-  return e != cudaSuccess ? e : launch_pdl(gather_kernel, dim3(p.T), dim3(256), 0, stream, p);
+  if ((long long)p.T * p.k <= kFewAssignments) return launch_pdl(sort_few_kernel, dim3(p.T + 1), dim3(kFewThreads), 0, stream, p);
+  cudaError_t e = launch_pdl(order_kernel, dim3(kOrderBlocks), dim3(kOrderThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  // warps of a block: as many as leave four blocks per SM, and as many blocks as reside
+  constexpr int kSmem = 224 * 1024;
+  const int ring = kGatherStages * p.row_bytes;
+  const int warps = max(1, min(4, kSmem / 4 / ring)), per_sm = max(1, min(16, kSmem / (warps * ring + 1024)));
+  static SmemOptIn opt_in;
+  e = opt_in.ensure(gather_kernel, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(gather_kernel, dim3(min(ceil_div(p.T, warps), per_sm * device_sms())), dim3(32 * warps), warps * ring, stream, p);
 }
 
 cudaError_t launch_unsort(const UnsortParams& p, int dtype, cudaStream_t stream) {

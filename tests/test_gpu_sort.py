@@ -134,6 +134,15 @@ def test_many_assignments(T, k, E, H):
     all_of(T, k, E, H, BF16, 0.05, seed=T)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,k,E,H", [(2500, 9, 32, 2888), (1300, 2, 8, 8192), (700, 17, 32, 16384), (3000, 4, 128, 2880),
+                                     (12000, 3, 7, 40), (5000, 8, 64, 4096), (613, 32, 40, 4104)])
+def test_many_tokens_of_wide_rows(T, k, E, H, dtype):
+    """Rows in several column chunks, more than eight rows a token, and both at once, where
+    persistent blocks take the tokens in turn."""
+    all_of(T, k, E, H, dtype, 0.05, seed=H + k)
+
+
 @pytest.mark.parametrize("H", [8192, 16384, 32768])
 def test_widest_rows(H):
     all_of(37, 3, 16, H, BF16, 0.1, seed=H)
