@@ -107,7 +107,7 @@ LinearLayout linear_layout(int T, int K, int N, bool backward) {
   LinearLayout L{};
   size_t part = 0;
   auto need = [&](int m, int n, int k) {
-    const size_t b = dense_partial_bytes(m, n, k, kDenseStore, backward);
+    const size_t b = dense_partial_bytes(m, n, k, backward ? kDenseStore : kDenseLinear, backward);
     if (b > part) part = b;
   };
   if (backward) {

@@ -385,33 +385,40 @@ __device__ __forceinline__ void store_out(O* p, const float* v, int n) {
     store16(p, v, n);
   }
 }
-template <typename O, int W>
+template <typename O>
 __device__ __forceinline__ void epilogue_linear(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left,
-                                                float (&v)[W]) {
-  static_assert(W == 16, "a step of columns");
+                                                float (&v)[16], const float (&r)[16], const float (&b)[16]) {
   if (left <= 0) return;
-  O* out = reinterpret_cast<O*>(c.out) + (size_t)m * c.N + n;
-  float r[W] = {};
-  if (p.residual) load_out(reinterpret_cast<const O*>(p.residual) + (size_t)m * c.N + n, left, r);
-  if (p.bias) {
 #pragma unroll
-    for (int j = 0; j < W; j += 4)
-      if (j < left) {  // (left: a multiple of 8)
-        const float4 b = __ldcg(reinterpret_cast<const float4*>(p.bias + n + j));
-        v[j] += b.x; v[j + 1] += b.y; v[j + 2] += b.z; v[j + 3] += b.w;
-      }
-  }
+  for (int j = 0; j < 16; ++j) v[j] += b[j];
   if (p.gateup) store_out(p.gateup + (size_t)m * c.N + n, v, left);
   if (p.act == kActSilu) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = act_f<kActSilu>(v[j]);
+    for (int j = 0; j < 16; ++j) v[j] = act_f<kActSilu>(v[j]);
   } else if (p.act == kActGelu) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[j] = act_f<kActGelu>(v[j]);
+    for (int j = 0; j < 16; ++j) v[j] = act_f<kActGelu>(v[j]);
   }
+  if (p.residual) {
 #pragma unroll
-  for (int j = 0; j < W; ++j) v[j] += r[j];
-  store_out(out, v, left);
+    for (int j = 0; j < 16; ++j) v[j] += r[j];
+  }
+  store_out(reinterpret_cast<O*>(c.out) + (size_t)m * c.N + n, v, left);
+}
+// The residual of 16 columns of a row.
+template <typename O>
+__device__ __forceinline__ void load_residual(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left,
+                                              float (&r)[16]) {
+  if (p.residual) load_out(reinterpret_cast<const O*>(p.residual) + (size_t)m * c.N + n, left, r);
+}
+// The same from a split tile's joined sums.
+template <typename O>
+__device__ __forceinline__ void epilogue_joined(const DenseGemmParams& p, const DenseProblem& c, int m, int n, int left,
+                                                float (&v)[16]) {
+  float r[16] = {}, b[16] = {};
+  load_residual<O>(p, c, m, n, left, r);
+  if (p.bias) load_out(p.bias + n, left, b);
+  epilogue_linear<O>(p, c, m, n, left, v, r, b);
 }
 
 // What happens to the sums of W columns of a row (`left` of them inside the matrix, in
@@ -425,9 +432,9 @@ __device__ __forceinline__ void epilogue(const DenseGemmParams& p, const DensePr
     for (int j = 0; j < W; j += 16)
       if (j < left) store16(out + (size_t)m * c.N + n + j, v + j, left - j);
   } else if constexpr (MODE == kDenseLinear) {
-    epilogue_linear<X>(p, c, m, n, left, v);
+    epilogue_joined<X>(p, c, m, n, left, v);
   } else if constexpr (MODE == kDenseLinear32) {
-    epilogue_linear<float>(p, c, m, n, left, v);
+    epilogue_joined<float>(p, c, m, n, left, v);
   } else if constexpr (MODE == kDenseGateUp) {
     if (p.gateup) {
       float* gu = p.gateup + (size_t)m * 2 * c.N + n;
@@ -463,6 +470,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dense_smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages], accf_bar[2], acce_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
+  constexpr bool kLinear = MODE == kDenseLinear || MODE == kDenseLinear32;
+  __shared__ __align__(16) float bias_s[kLinear ? kEpiWarps : 1][kLinear ? BN : 4];  // each epilogue warp's copy of a tile's
   __shared__ volatile uint32_t late;  // a wait of this launch gave up, in this block or its peer
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
@@ -647,6 +656,22 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
             load_gateup(p, g, m, n0 + c, end - c, gs[j], us[j]);
           }
         }
+      // a projection's bias, and the first of its residual
+      using O = std::conditional_t<MODE == kDenseLinear32, float, X>;
+      float rs[kLinear ? kAhead + 1 : 1][16];
+      if constexpr (kLinear)
+        if (t.slot < 0) {
+          float* b = bias_s[warp - 2];
+          for (int j = lane; j < cols; j += 32) b[j] = p.bias && j < end ? __ldcg(p.bias + n0 + j) : 0.f;
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+              const int c = part0 + kStep * j;
+              load_residual<O>(p, g, m, n0 + c, end - c, rs[j]);
+            }
+          }
+          __syncwarp();
+        }
       // (one answer for the warp: its lanes leave together, or all go on to the warp's
       // tensor-memory loads)
       if (!wait_warp(&accf_bar[b], (i >> 1) & 1, p.wait_ns)) {
@@ -688,6 +713,32 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
             tmem_wait_ld();
             landed(raw, v);
             if (live && c < end) epilogue_grad<X>(p, g, m, n0 + c, end - c, v, gs[j], us[j]);
+            __syncwarp();
+          }
+      } else if constexpr (kLinear) {
+        // as above, with the residual; its loads in step with the arithmetic cost a memory round
+        // trip each (2048 x 4096 -> 4096 onto f32: 54 us)
+        const float* bias = bias_s[warp - 2];
+#pragma unroll 1
+        for (int c0 = part0; c0 < cols; c0 += kStep * (kAhead + 1))
+#pragma unroll
+          for (int j = 0; j <= kAhead; ++j) {
+            const int c = c0 + kStep * j;
+            if (c >= cols) break;
+            constexpr int kAll = kAhead + 1;
+            const int next = c + kStep * kAhead;
+            if (live) load_residual<O>(p, g, m, n0 + next, end - next, rs[(j + kAhead) % kAll]);
+            uint32_t raw[16];
+            float v[16], b[16];
+            tmem_ld_32x32b_x16(acc + c, raw);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 q4 = *reinterpret_cast<const float4*>(bias + c + i);
+              b[i] = q4.x; b[i + 1] = q4.y; b[i + 2] = q4.z; b[i + 3] = q4.w;
+            }
+            tmem_wait_ld();
+            landed(raw, v);
+            if (live && c < end) epilogue_linear<O>(p, g, m, n0 + c, end - c, v, rs[j], b);
             __syncwarp();
           }
       } else {
@@ -826,13 +877,12 @@ Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
 // The estimate is a function of the sizes alone; the last ones are kept per thread, since a
 // small product's launch would wait for its 3 us otherwise.
 Shape pick_shape(int M, int N, int K, int mode, bool b_mn) {
-  if (mode != kDenseGateUp) mode = kDenseStore;  // (what tiles cost apart from their epilogues)
   struct Entry {
     int M, N, K, key;
     Shape s;
   };
   static thread_local Entry kept[16] = {};
-  const int sms = device_sms(), key = sms * 8 + mode * 2 + b_mn;
+  const int sms = device_sms(), key = sms * 16 + mode * 2 + b_mn;
   Entry& e = kept[((unsigned)M * 31u + (unsigned)N * 7u + (unsigned)K * 3u + (unsigned)key) * 2654435761u >> 28];
   if (e.M != M || e.N != N || e.K != K || e.key != key) e = {M, N, K, key, estimate_shape(M, N, K, mode, b_mn, sms)};
   return e.s;

@@ -23,12 +23,14 @@ __device__ uint32_t g_sort_status;  // bits as in the layer's status word
 __device__ __forceinline__ int key_of(int e, int E) { return e >= 0 && e < E ? e : E; }
 
 // ------------------------------------------------------------------ many assignments: the order
-// By one cluster.  Each warp counts the keys of a contiguous run of assignments; the blocks
-// tell one another their sums, from which each knows where its keys begin; and each warp places
-// its run.  What bounds it is the latency of these few steps (16384 assignments: 5.6 us for one
-// block, see the launcher for the cluster), which the rows' copies of the next launch hide in
-// part: it starts with this one and has its first rows in before the order is there.
-constexpr int kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32, kOrderBlocks = 8;
+// By one cluster.  Each warp takes a contiguous run of assignments and counts their keys, which
+// gives each its rank among its key's in the run; the blocks tell one another their sums, from
+// which each knows where its keys begin.  What bounds it is the latency of these few steps,
+// which the rows' copies of the next launch hide in part: it starts with this one and has its
+// first rows in before the order is there.  Up to kHeld x 32 assignments of a run stay in
+// registers; a second reading of them, a load and a match at a time, took 2 of 8 us at 16384
+// assignments and 8 of 15 at 65536.
+constexpr int kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32, kOrderBlocks = 8, kHeld = 8;
 
 __global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThreads)
     order_kernel(const __grid_constant__ SortParams p) {
@@ -43,8 +45,43 @@ __global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThr
   ptx::pdl_launch_dependents();
   ptx::cluster_arrive_release();  // (every block has started: its memory may be written)
   const int n = p.T * p.k, warps = kOrderBlocks * kOrderWarps, run = ceil_div(ceil_div(n, warps), 32) * 32;
-  const int begin = min((long long)n, (long long)(rank * kOrderWarps + warp) * run), end = min(n, begin + run);
-  for (int a = begin + lane; a < end; a += 32) atomicAdd(&count[warp][key_of(__ldcg(p.idx + a), p.E)], 1);
+  const int begin = min(n, (rank * kOrderWarps + warp) * run), end = min(n, begin + run);
+  int* const own = count[warp];
+  // the keys of 32 kHeld assignments from `a0` on, -1 past the run's end
+  int key[kHeld], at[kHeld];
+  auto load = [&](int a0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int a = a0 + 32 * i + lane;
+      key[i] = a < end ? key_of(__ldcg(p.idx + a), p.E) : -1;
+    }
+  };
+  // their ranks in the run, and the run's counts so far
+  auto ranks = [&](int a0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      if (a0 + 32 * i >= end) break;
+      const unsigned same = __match_any_sync(0xffffffffu, key[i]);
+      const int ahead = __popc(same & ((1u << lane) - 1));
+      const int before = key[i] >= 0 ? own[key[i]] : 0;
+      at[i] = before + ahead;
+      __syncwarp();
+      if (key[i] >= 0 && ahead == 0) own[key[i]] = before + __popc(same);
+      __syncwarp();
+    }
+  };
+  const bool held = run <= 32 * kHeld;
+  if (held) {
+    load(begin);
+    ranks(begin);
+  } else {
+    for (int a0 = begin; a0 < end; a0 += 32 * kHeld) {
+      load(a0);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (key[i] >= 0) atomicAdd(&own[key[i]], 1);
+    }
+  }
   __syncthreads();
   // a warp's places of a key begin behind those of the lower warps
   int total = 0;
@@ -88,27 +125,31 @@ __global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThr
   if (lane == 31) warp_total[warp] = scan;
   __syncthreads();
   if (tid < keys) {
-    int at = scan - all;
-    for (int w = 0; w < warp; ++w) at += warp_total[w];
-    first[tid] = at + before;
-    if (rank == 0) p.offsets[tid] = at;
+    int to = scan - all;
+    for (int w = 0; w < warp; ++w) to += warp_total[w];
+    first[tid] = to + before;
+    if (rank == 0) p.offsets[tid] = to;
   }
   __syncthreads();
-  for (int a0 = begin; a0 < end; a0 += 32) {
-    const int a = a0 + lane;
-    const bool on = a < end;
-    const int key = on ? key_of(__ldcg(p.idx + a), p.E) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int ahead = __popc(same & ((1u << lane) - 1));
-    if (on) {
-      const int place = first[key] + count[warp][key] + ahead;
-      const bool kept = key < p.E;
-      p.perm[place] = kept ? a : -1 - a;
-      p.inv_perm[a] = kept ? place : -1 - place;
+  auto place = [&](int a0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int a = a0 + 32 * i + lane;
+      if (key[i] < 0) continue;
+      const int to = first[key[i]] + at[i] + (held ? own[key[i]] : 0);
+      const bool kept = key[i] < p.E;
+      p.perm[to] = kept ? a : -1 - a;
+      p.inv_perm[a] = kept ? to : -1 - to;
     }
-    __syncwarp();
-    if (on && ahead == 0) count[warp][key] += __popc(same);
-    __syncwarp();
+  };
+  if (held) {
+    place(begin);
+  } else {  // (the run's first places, counted on from)
+    for (int a0 = begin; a0 < end; a0 += 32 * kHeld) {
+      load(a0);
+      ranks(a0);
+      place(a0);
+    }
   }
 }
 
@@ -594,6 +635,13 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
   const int lane = threadIdx.x & 31;
   const size_t t = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (t >= (size_t)p.T) return;
+  const float* logits = p.logits + t * p.E;
+  const bool all = p.gating == kGatingSoftmaxAll;
+  float top = -INFINITY, sum = 0.f, l[kMaxExperts / 32];
+  if (all) {
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) l[i] = lane + 32 * i < p.E ? __ldcg(logits + lane + 32 * i) : -INFINITY;
+  }
   int e = -1;
   float g = 0.f, w = 0.f;
   if (lane < p.k) {
@@ -605,18 +653,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
   float s = w * g;
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  const float* logits = p.logits + t * p.E;
   float* out = p.d_logits + t * p.E;
-  const bool all = p.gating == kGatingSoftmaxAll;
   float part = all ? g : w * (g - s);
   if (p.gating == kGatingSigmoid && e >= 0) part *= 1.f / (1.f + expf(__ldcg(logits + e)));
-  float top = -INFINITY, sum = 0.f, l[kMaxExperts / 32];
   if (all) {
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-      l[i] = lane + 32 * i < p.E ? __ldcg(logits + lane + 32 * i) : -INFINITY;
-      top = fmaxf(top, l[i]);
-    }
+    for (int i = 0; i < kMaxExperts / 32; ++i) top = fmaxf(top, l[i]);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
 #pragma unroll
