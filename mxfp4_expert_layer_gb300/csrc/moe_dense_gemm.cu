@@ -365,6 +365,28 @@ __device__ __forceinline__ void epilogue_grad(const DenseGemmParams& p, const De
 // f32), and v + bias in f32 where it is kept.  The residual's element and out's may be one.
 template <typename O, int W>
 __device__ __forceinline__ void load_out(const O* p, int left, float (&f)[W]) {
+  // (a whole sector a thread, as load_sector; through L2 only, as the array may be out itself)
+  if (left >= 16 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    uint32_t w[sizeof(O) * W / 4];
+#pragma unroll
+    for (int j = 0; j < (int)(sizeof(O) * W / 32); ++j)
+      asm volatile("ld.global.cg.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[8 * j]), "=r"(w[8 * j + 1]), "=r"(w[8 * j + 2]), "=r"(w[8 * j + 3]), "=r"(w[8 * j + 4]),
+                     "=r"(w[8 * j + 5]), "=r"(w[8 * j + 6]), "=r"(w[8 * j + 7])
+                   : "l"(reinterpret_cast<const uint32_t*>(p) + 8 * j));
+    if constexpr (std::is_same<O, float>::value) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const float2 v = unpack2<O>(w[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < W; j += 8)
     if (j < left) {
@@ -864,6 +886,8 @@ Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
         const float moved = (float)rem * splits * (float)(s.pair ? 256 : rows) * s.bn * 8.f;
         time += (float)ceil_div(rem * splits, workers) * slice + moved / 2500.f + 5000.f;
       }
+      // (of as many columns the narrower tile: the last one's epilogue has no MMAs to hide behind)
+      if (mode == kDenseLinear) time += 20.f * s.bn;
       if (time < hbm) time = hbm + 0.1f * time;  // (ties on the HBM bound go to the smaller work)
       if (best_time == 0.f || time < best_time) {
         best_time = time;
@@ -877,6 +901,7 @@ Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
 // The estimate is a function of the sizes alone; the last ones are kept per thread, since a
 // small product's launch would wait for its 3 us otherwise.
 Shape pick_shape(int M, int N, int K, int mode, bool b_mn) {
+  if (mode == kDenseLinear32) mode = kDenseLinear;
   struct Entry {
     int M, N, K, key;
     Shape s;
