@@ -526,14 +526,13 @@ __global__ void __launch_bounds__(512)
 // past the first rows' latency: 4096 x 2880 bf16 17.4 us, 5.4 TB/s (a copy: 6.7).
 //
 // TIGHT: 56 registers a thread, for widths at which that lets one more block reside on an SM
-// (2880: 4096 rows bf16 with a feature gate 24.4 -> 19.0 us, 8-bit codes with a row scale 29.9 ->
-// 20.5); elsewhere the compiler's 64 are better (8192 x 4096, f32 stream: 63 us against 76).
-template <typename A, typename S, int GATE, int OUT, bool TIGHT>
+// (2880: 4096 rows bf16 with a feature gate 24.4 -> 19.0 us); elsewhere the compiler's 64 are better
+// (8192 x 4096, f32 stream: 63 us against 76).
+template <typename A, typename S, int GATE, bool TIGHT>
 __global__ void __maxnreg__(TIGHT ? 56 : 64)
     block_norm_rows_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float sums[2][16];
-  __shared__ uint32_t top[16];  // (with the barriers of sums, whoever writes it again is past all its readers)
   __shared__ uint64_t full_bar[kNormMaxGroups][3];
   const bool token = GATE == kGateNone && p.gate_kind == kGateToken;
   const int nvec = p.H / 8, per = rows.threads, group = threadIdx.x / per, v = threadIdx.x - group * per;
@@ -616,21 +615,159 @@ __global__ void __maxnreg__(TIGHT ? 56 : 64)
     get2(wn, w);
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] = mul2(mul2(z[k], rs), w[k]);
-    if (OUT == kOut16 || p.out) {
-      set2(t, z);
-      if (on) t.store(p.out, at);
+    set2(t, z);
+    if (on) t.store(p.out, at);
+    if (++stage == rows.stages) {
+      stage = 0;
+      phase ^= 1;
     }
-    if constexpr (OUT == kOutMx) store_mx(p, on, row, v, at, z);
+  }
+  if (!ok) leave_late();
+}
+
+// The same with 8-bit codes.  Sixteen values a thread: with eight, a row's 300 instructions a
+// warp and three reductions kept the SMs at 2.4 instructions a cycle and HBM at 0.6 of its rate
+// (4096 x 2880 bf16 with a row scale: 20.5 us).  A warp's two vectors are reduced side by side as
+// two of the rows kernel's warps would be, so that s and y are the same bits as there.  The
+// weights stay in shared memory, as 16-bit values.  Bound by HBM at 4096 values (8192 rows bf16,
+// row scale: 37.7 us, 0.92 of the copy rate; 50.3 with eight values a thread), at 2880 by the
+// latency of seven rounds of four rows per SM (4096 rows: 19.1 us, 0.64).
+template <typename A, typename S, int GATE, int OUT>
+__global__ void __launch_bounds__(512, 2)
+    block_norm_codes_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  __shared__ float sums[2][32];
+  __shared__ uint32_t top[16];  // (with the barriers of sums, whoever writes it again is past all its readers)
+  __shared__ uint64_t full_bar[kNormMaxGroups][3];
+  const bool token = GATE == kGateNone && p.gate_kind == kGateToken;
+  const int nvec = p.H / 8, per = rows.threads, group = threadIdx.x / per, v = threadIdx.x - group * per;
+  const int groups = blockDim.x / per, warps = per >> 5, warp = v >> 5, lane = threadIdx.x & 31;
+  const int at0 = 64 * warp + lane, at1 = at0 + 32;  // this thread's vectors
+  const bool on0 = at0 < nvec, on1 = at1 < nvec, leader = v == 0;
+  const float inv_h = 1.f / (float)p.H;
+  uint8_t* const ring = norm_smem + group * rows.stages * rows.total;
+  uint8_t* const weights = norm_smem + groups * rows.stages * rows.total;  // [3][H]: norm_w, next_w, gate
+  auto barrier = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(per) : "memory"); };
+  auto group_sum = [&](f32x2 a, f32x2 b, float* buf) {
+    const float2 f = split2(a), g = split2(b);
+    const float t = warp_sum_butterfly(f.x + f.y), u = warp_sum_butterfly(g.x + g.y);
+    if (warps == 1) return t + u;
+    if (lane == 0) *reinterpret_cast<float2*>(buf + 2 * (group * warps + warp)) = make_float2(t, u);
+    barrier();
+    return warp_sum_butterfly(lane < 2 * warps ? buf[2 * group * warps + lane] : 0.f);
+  };
+  if (leader) {
+    for (int i = 0; i < rows.stages; ++i) ptx::mbar_init(&full_bar[group][i], 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int row0 = blockIdx.x * groups + group, row_step = gridDim.x * groups;
+  if (leader)
+    for (int i = 0; i < rows.stages; ++i)
+      if (row0 + i * row_step < p.T) issue_row(rows, ring + i * rows.total, &full_bar[group][i], row0 + i * row_step);
+  for (int i = threadIdx.x; i < nvec; i += blockDim.x) {
+    Vec8<A> w;
+    w.load_weight(p.norm_w, i);
+    w.store(weights, i);
+    w.load_weight(p.next_w, i);
+    w.store(weights, nvec + i);
+    if (GATE == kGateFeature) {
+      w.load_weight(p.gate, i);
+      w.store(weights, 2 * nvec + i);
+    }
+  }
+  __syncthreads();
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int row = row0; row < p.T; row += row_step) {
+    const uint8_t* st = ring + stage * rows.total;
+    if (ok && !ptx::mbar_wait_bounded(&full_bar[group][stage], phase, kRowWaitNs)) ok = false;
+    const float gt = token ? __ldcg(reinterpret_cast<const float*>(p.gate) + row) : 1.f;
+    f32x2 z[2][4], sq[2] = {0, 0};
+    Vec8<S> r[2];
+    Vec8<A> full[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int at = q ? at1 : at0;
+      Vec8<A> t;
+      t.zero();
+      r[q].zero();
+      full[q].zero();
+      if (q ? on1 : on0) {
+        t.load_shared(st + rows.offset[0], at);
+        r[q].load_shared(st + rows.offset[1], at);
+        if (GATE == kGateFull) full[q].load_shared(st + rows.offset[2], at);
+      }
+      get2(t, z[q]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sq[q] = fma2(z[q][k], z[q][k], sq[q]);
+    }
+    __syncwarp();
+    const f32x2 g2 = both(rsqrtf(group_sum(sq[0], sq[1], sums[0]) * inv_h + p.eps) * gt), a2 = both(p.scale);
+    // (for one warp, the sum's exchanges come after every lane's reads)
+    if (leader && ok && row + rows.stages * row_step < p.T)
+      issue_row(rows, ring + stage * rows.total, &full_bar[group][stage], row + rows.stages * row_step);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int at = q ? at1 : at0;
+      const bool on = q ? on1 : on0;
+      Vec8<A> t;
+      f32x2 w[4];
+      t.zero();
+      if (on) t.load_shared(weights, at);
+      get2(t, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[q][k] = mul2(mul2(z[q][k], g2), w[k]);
+      if (GATE == kGateFeature || GATE == kGateFull) {
+        if (GATE == kGateFeature && on) full[q].load_shared(weights, 2 * nvec + at);
+        get2(full[q], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[q][k] = mul2(z[q][k], w[k]);
+      }
+      get2(r[q], w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[q][k] = fma2(a2, w[k], z[q][k]);
+      set2(r[q], z[q]);
+      if (on) r[q].store(p.residual_out, (size_t)row * nvec + at);
+      get2(r[q], z[q]);  // the stored values
+      sq[q] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sq[q] = fma2(z[q][k], z[q][k], sq[q]);
+    }
+    const f32x2 rs = both(rsqrtf(group_sum(sq[0], sq[1], sums[1]) * inv_h + p.eps));
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int at = q ? at1 : at0;
+      const bool on = q ? on1 : on0;
+      Vec8<A> t;
+      f32x2 w[4];
+      t.zero();
+      if (on) t.load_shared(weights, nvec + at);
+      get2(t, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[q][k] = mul2(mul2(z[q][k], rs), w[k]);
+      if (p.out) {
+        set2(t, z[q]);
+        if (on) t.store(p.out, (size_t)row * nvec + at);
+      }
+      if constexpr (OUT == kOutMx) store_mx(p, on, row, at, (size_t)row * nvec + at, z[q]);
+      if (OUT == kOutRow && on) m = max(m, largest8(z[q]));
+    }
     if constexpr (OUT == kOutRow) {
-      uint32_t m = __reduce_max_sync(0xffffffffu, on ? largest8(z) : 0u);
+      m = __reduce_max_sync(0xffffffffu, m);
       if (warps > 1) {
         if (lane == 0) top[group * warps + warp] = m;
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(per) : "memory");
+        barrier();
         m = __reduce_max_sync(0xffffffffu, lane < warps ? top[group * warps + lane] : 0u);
       }
       float scale;
       const float to_code = row_scale(m, scale);
-      if (on) store_codes(p.codes, at, z, to_code);
+      if (on0) store_codes(p.codes, (size_t)row * nvec + at0, z[0], to_code);
+      if (on1) store_codes(p.codes, (size_t)row * nvec + at1, z[1], to_code);
       if (leader) reinterpret_cast<float*>(p.scales)[row] = scale;
     }
     if (++stage == rows.stages) {
@@ -691,30 +828,42 @@ template <typename A, typename S, int OUT>
 cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
   const bool every = p.norm_w && p.next_w && p.residual && p.residual_out;
   const int gate = !every ? kAnyGate : p.gate_kind == kGateToken ? kGateNone : p.gate_kind;
-  const int row_threads = (p.H / 8 + 31) / 32 * 32, groups = min(512 / row_threads, kNormMaxGroups);
-  // many rows: persistent blocks, as many per SM as 56 registers a thread allow (fewer rows are
-  // done sooner by a block each).  Rows of calls without every argument, and of more than 4096
-  // values, have a block each.
-  const int per_sm = groups > 0 ? 1152 / (groups * row_threads) : 0, blocks = per_sm * device_sms();
-  if (every && groups > 0 && p.T >= 4 * groups * blocks) {
+  const int row_threads = (p.H / 8 + 31) / 32 * 32;
+  // many rows: persistent blocks, as many per SM as 56 registers a thread allow, or 64 of the
+  // kernel with codes (fewer rows are done sooner by a block each; the number is the same with and
+  // without codes, so that s is the same bits).  Rows of calls without every argument, and of more
+  // than 4096 values, have a block each.
+  constexpr bool CODES = OUT != kOut16;
+  const int groups16 = min(512 / row_threads, kNormMaxGroups), many = groups16 > 0 ? 1152 / (groups16 * row_threads) * groups16 * 4 : 0;
+  if (every && groups16 > 0 && p.T >= many * device_sms()) {
+    // (a row to a block, five of 192 threads per SM at 2880 values, measured 24.5 us against 19.1 for
+    // two rows a block: the named barriers are enough for four blocks)
+    const int per = CODES ? (p.H / 8 + 63) / 64 * 32 : row_threads, groups = min(512 / per, kNormMaxGroups);
+    const int per_sm = (CODES ? 1024 : 1152) / (groups * per), blocks = per_sm * device_sms();
     const void* src[3] = {p.block, p.residual, gate == kGateFull ? p.gate : nullptr};
-    const int size[3] = {2, (int)sizeof(S), 2};
+    const int size[3] = {2, (int)sizeof(S), 2}, weights = CODES ? 6 * p.H : 0;
     RowCopies r = make_rows(p.H, 3, src, size);
-    r.threads = row_threads;
-    r.stages = min(3, kNormSmem / per_sm / (groups * r.total));
+    r.threads = per;
+    r.stages = min(3, (kNormSmem / per_sm - weights) / (groups * r.total));
     auto launch = [&](auto kern, SmemOptIn& opt_in) {
       const cudaError_t e = opt_in.ensure(kern, kNormSmem);
-      return e != cudaSuccess ? e
-                              : launch_pdl(kern, dim3(blocks), dim3(groups * r.threads), groups * r.stages * r.total, stream, p, r);
+      return e != cudaSuccess ? e : launch_pdl(kern, dim3(blocks), dim3(groups * per), groups * r.stages * r.total + weights, stream, p, r);
     };
-    auto pick = [&](auto tight) {
-      constexpr bool TIGHT = decltype(tight)::value;
+    if constexpr (CODES) {
       static SmemOptIn o[3];
-      if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature, OUT, TIGHT>, o[0]);
-      if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull, OUT, TIGHT>, o[1]);
-      return launch(block_norm_rows_kernel<A, S, kGateNone, OUT, TIGHT>, o[2]);
-    };
-    return per_sm * groups * row_threads > 1024 ? pick(std::true_type{}) : pick(std::false_type{});
+      if (gate == kGateFeature) return launch(block_norm_codes_kernel<A, S, kGateFeature, OUT>, o[0]);
+      if (gate == kGateFull) return launch(block_norm_codes_kernel<A, S, kGateFull, OUT>, o[1]);
+      return launch(block_norm_codes_kernel<A, S, kGateNone, OUT>, o[2]);
+    } else {
+      auto pick = [&](auto tight) {
+        constexpr bool TIGHT = decltype(tight)::value;
+        static SmemOptIn o[3];
+        if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature, TIGHT>, o[0]);
+        if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull, TIGHT>, o[1]);
+        return launch(block_norm_rows_kernel<A, S, kGateNone, TIGHT>, o[2]);
+      };
+      return per_sm * groups * per > 1024 ? pick(std::true_type{}) : pick(std::false_type{});
+    }
   }
   auto launch = [&](auto kern) { return launch_pdl(kern, dim3(p.T), dim3(row_threads), 0, stream, p); };
   if (gate == kAnyGate) return launch(block_norm_kernel<A, S, kAnyGate, OUT>);
