@@ -96,17 +96,35 @@ at::Tensor row_of(const at::Tensor& m, int64_t i) {
   t.unsafeGetTensorImpl()->set_sizes_contiguous(m.sizes().slice(1));
   return t;
 }
-// The tensor of this shape at element `at` of a tensor's storage, sharing it.
-at::Tensor part_of(const at::Tensor& m, int64_t at, Shape shape) {
-  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(m.storage()), m.key_set(), m.dtype());
-  t.unsafeGetTensorImpl()->set_storage_offset(at);
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(shape));
-  return t;
-}
 // Results of up to this many bytes together share one allocation: each costs host time that a
 // decoded token's norm waits for (4.6 us a call among others, 4.1 shared), while larger
 // results had better be freed one by one.
 constexpr int64_t kShareBytes = 64 * 1024;
+// Results that share one allocation, each from a 16-byte boundary on.
+class Shared {
+ public:
+  template <size_t N>
+  Shared(const at::Device& device, const std::pair<at::ScalarType, int64_t> (&parts)[N]) {  // types and element counts
+    int64_t bytes = 0;
+    for (const auto& [type, n] : parts) bytes += size_of(type, n);
+    all_ = empty({bytes}, at::kByte, device);
+  }
+  // The next part.
+  at::Tensor take(Shape shape, at::ScalarType type) {
+    int64_t n = 1;
+    for (const int64_t d : shape) n *= d;
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all_.storage()), all_.key_set(), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(at_ / (int64_t)c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(shape));
+    at_ += size_of(type, n);
+    return t;
+  }
+  static int64_t size_of(at::ScalarType type, int64_t n) { return (n * (int64_t)c10::elementSize(type) + 15) / 16 * 16; }
+
+ private:
+  at::Tensor all_;
+  int64_t at_ = 0;
+};
 void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 PyObject* wrap(const at::Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
@@ -258,10 +276,21 @@ PyObject* block_norm_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
          *wz = need("norm_weight", norm_w, {H}, type, device), *wn = need("next_weight", &next_w, {H}, type, device);
     const int t = narrow(T), h = narrow(H);
     const bool mx = kind == MOE_SCALE_MX;
-    const at::Tensor res = empty({T, H}, stype, device), codes = empty({T, H}, at::kFloat8_e4m3fn, device);
-    const at::Tensor scales = mx ? empty({T, H / 32}, at::kFloat8_e8m0fnu, device) : empty({T, 1}, at::kFloat, device);
-    at::Tensor out;
-    if (with_out) out = empty({T, H}, type, device);
+    const at::ScalarType sctype = mx ? at::kFloat8_e8m0fnu : at::kFloat;
+    const int64_t per_row = mx ? H / 32 : 1;
+    at::Tensor res, codes, scales, out;
+    if (T > 0 && T * H * (with_out ? 9 : 7) <= kShareBytes) {
+      Shared all(device, {{stype, T * H}, {at::kFloat8_e4m3fn, T * H}, {sctype, T * per_row}, {type, with_out ? T * H : 0}});
+      res = all.take({T, H}, stype);
+      codes = all.take({T, H}, at::kFloat8_e4m3fn);
+      scales = all.take({T, per_row}, sctype);
+      if (with_out) out = all.take({T, H}, type);
+    } else {
+      res = empty({T, H}, stype, device);
+      codes = empty({T, H}, at::kFloat8_e4m3fn, device);
+      scales = empty({T, per_row}, sctype, device);
+      if (with_out) out = empty({T, H}, type, device);
+    }
     call("moe_block_norm_8bit", device, [&](moe_stream_t s) {
       return moe_block_norm_8bit(z, wz, g.ptr, g.kind, r, scale, wn, eps, t, h, code, scode, kind, res.data_ptr(),
                                  static_cast<uint8_t*>(codes.data_ptr()), scales.data_ptr(), address(out), s);
@@ -537,14 +566,25 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
          *ps = scales ? need("scales", scales, {T, scales->size(1)}, scales->scalar_type(), device) : nullptr;
     const int t = narrow(T), kk = narrow(k), rb = row_bytes(x), sb = scales ? row_bytes(*scales) : 0;
     if (T < 1 || k < 1 || E < 1 || T > INT32_MAX / k) refuse("moe_sort_tokens", MOE_ERR_UNSUPPORTED_SHAPE);
-    // offsets, perm and inv_perm in one allocation, each 16-byte aligned
-    const int64_t rows = T * k, at_perm = ((int64_t)E + 4) / 4 * 4, at_inv = at_perm + (rows + 3) / 4 * 4;
-    const at::Tensor order = empty({at_inv + rows}, at::kInt, device);
-    const at::Tensor offsets = part_of(order, 0, {(int64_t)E + 1}), perm = part_of(order, at_perm, {rows}),
-                     inv = part_of(order, at_inv, {T, k});
-    const at::Tensor sorted = empty({rows, x.size(1)}, x.scalar_type(), device);
-    at::Tensor sorted_scales;
-    if (scales) sorted_scales = empty({rows, scales->size(1)}, scales->scalar_type(), device);
+    const int64_t rows = T * k, H = x.size(1), S = scales ? scales->size(1) : 0;
+    const at::ScalarType type = x.scalar_type(), stype = scales ? scales->scalar_type() : type;
+    at::Tensor sorted, sorted_scales, offsets, perm, inv;
+    auto order = [&](Shared& all) {
+      offsets = all.take({(int64_t)E + 1}, at::kInt);
+      perm = all.take({rows}, at::kInt);
+      inv = all.take({T, k}, at::kInt);
+    };
+    if (Shared::size_of(type, rows * H) + Shared::size_of(stype, rows * S) <= kShareBytes) {
+      Shared all(device, {{at::kInt, E + 1}, {at::kInt, rows}, {at::kInt, rows}, {type, rows * H}, {stype, rows * S}});
+      order(all);
+      sorted = all.take({rows, H}, type);
+      if (scales) sorted_scales = all.take({rows, S}, stype);
+    } else {
+      Shared all(device, {{at::kInt, E + 1}, {at::kInt, rows}, {at::kInt, rows}});
+      order(all);
+      sorted = empty({rows, H}, type, device);
+      if (scales) sorted_scales = empty({rows, S}, stype, device);
+    }
     call("moe_sort_tokens", device, [&](moe_stream_t s) {
       return moe_sort_tokens(px, ps, static_cast<const int32_t*>(pi), t, kk, E, rb, sb, static_cast<int32_t*>(offsets.data_ptr()),
                              static_cast<int32_t*>(perm.data_ptr()), static_cast<int32_t*>(inv.data_ptr()), sorted.data_ptr(),
@@ -609,8 +649,14 @@ PyObject* unsort_tokens_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
          *pi = need("inv_perm", &inv, {T, k}, at::kInt, device), *pw = need("topk_w", w, {T, k}, at::kFloat, device);
     const int t = narrow(T), kk = narrow(k), h = narrow(H);
     at::Tensor d_y, d_w;
-    if (need_y) d_y = empty({T * k, H}, type, device);
-    if (need_w) d_w = empty({T, k}, at::kFloat, device);
+    if (need_y && need_w && Shared::size_of(type, T * k * H) <= kShareBytes) {
+      Shared all(device, {{type, T * k * H}, {at::kFloat, T * k}});
+      d_y = all.take({T * k, H}, type);
+      d_w = all.take({T, k}, at::kFloat);
+    } else {
+      if (need_y) d_y = empty({T * k, H}, type, device);
+      if (need_w) d_w = empty({T, k}, at::kFloat, device);
+    }
     call("moe_unsort_tokens_backward", device, [&](moe_stream_t s) {
       return moe_unsort_tokens_backward(pd, py, static_cast<const int32_t*>(pi), static_cast<const float*>(pw), t, kk, h, code,
                                         address(d_y), static_cast<float*>(address(d_w)), s);

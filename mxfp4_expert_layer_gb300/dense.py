@@ -70,7 +70,7 @@ def block_norm(block: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
 
 
 class BlockNorm8(NamedTuple):
-    """What block_norm_8bit returns."""
+    """What block_norm_8bit returns; small results share a storage."""
     residual: torch.Tensor            # s [T, H]
     codes: torch.Tensor               # float8_e4m3fn [T, H]: out / scale
     scales: torch.Tensor              # "mx": float8_e8m0fnu [T, H / 32]; "row": f32 [T, 1]
@@ -174,7 +174,8 @@ def linear_backward(d_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
 
 # ------------------------------------------------------------------ tokens sorted by expert
 class SortedTokens(NamedTuple):
-    """Token rows in expert order.  The three integer arrays share a storage."""
+    """Token rows in expert order.  The three integer arrays share a storage, where the rows are
+    small (64 KB) with them."""
     rows: torch.Tensor                # [T*k, H]: by expert, then by token; what was dropped comes last, as zeros
     scales: Optional[torch.Tensor]    # [T*k, S]: the rows' scales
     offsets: torch.Tensor             # i32 [E + 1]: rows of expert e are [offsets[e], offsets[e + 1])
@@ -206,7 +207,7 @@ def unsort_tokens(y: torch.Tensor, inv_perm: torch.Tensor, topk_w: Optional[torc
 
 
 class UnsortGrads(NamedTuple):
-    """Gradients of unsort_tokens; None for one that was not asked for."""
+    """Gradients of unsort_tokens; None for one that was not asked for.  Small ones share a storage."""
     y: Optional[torch.Tensor]         # [T*k, H]; 0 in the rows of what was dropped
     topk_w: Optional[torch.Tensor]    # f32 [T, k]; 0 where dropped
 
