@@ -333,8 +333,9 @@ size_t dense_partial_bytes(int M, int N, int K, int mode, bool b_mn);
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream);
 // Up to kDenseGroup plain products (g[i].M, N, K, out set) whose K takes at most two values,
-// in one launch where that is estimated to be faster.
-int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const DenseOperand* b, int dtype,
+// in one launch where that is estimated to be faster.  few_rows: the estimate takes account of
+// tiles too few to fill the GPU (the feed-forward block's does not: its results stay what they are).
+int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const DenseOperand* b, int dtype, bool few_rows,
                           cudaStream_t stream);
 
 }  // namespace moe

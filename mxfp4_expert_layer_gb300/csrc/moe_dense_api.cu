@@ -252,7 +252,7 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
   product(T, H, 2 * I, {dgu, T, 2 * I, 0}, {w_gateup, 2 * I, H, 1}, d_x);
   product(2 * I, H, T, {dgu, T, 2 * I, 1}, {x, T, H, 1}, d_w_gateup);
   product(H, I, T, {d_out, T, H, 1}, {h, T, I, 1}, d_w_down);
-  return launch_dense_products(q, n, a, b, dtype, s);
+  return launch_dense_products(q, n, a, b, dtype, false, s);
 }
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, int backward) {
@@ -359,7 +359,7 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
   };
   product(T, K, N, {dp, T, N, 0}, {weight, N, K, 1}, d_x);
   product(N, K, T, {dp, T, N, 1}, {x, T, K, 1}, d_weight);
-  return launch_dense_products(q, n, a, b, dtype, s);
+  return launch_dense_products(q, n, a, b, dtype, true, s);
 }
 
 int moe_dense_status(int* status, moe_stream_t stream) {

@@ -1056,7 +1056,7 @@ int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOpera
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const DenseOperand* b, int dtype,
+int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const DenseOperand* b, int dtype, bool few_rows,
                           cudaStream_t stream) {
   // the class of the larger K first
   int order[kDenseGroup] = {0, 1, 2};
@@ -1082,7 +1082,10 @@ int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const
   const float len[2] = {ceil_div(p.g[order[0]].K, 64) * 540.f, ceil_div(p.g[order[n - 1]].K, 64) * 540.f};
   q.lead = q.long_n < n ? (int)(len[0] / len[1] + 0.5f) : 0;
   const float work = (float)tiles[0] * len[0] + (q.long_n < n ? (float)tiles[1] * len[1] : 0.f);
-  const float together = work / (float)workers + 0.5f * len[q.long_n < n ? 1 : 0] + 1000.f;
+  float together = work / (float)workers + 0.5f * len[q.long_n < n ? 1 : 0] + 1000.f;
+  // a few long tiles that cannot be shared out take as long as one of them (128 x 4096 -> 1024 with
+  // its weights' gradient: see the projections' backward)
+  if (few_rows) together = fmaxf(together, (float)ceil_div((int)tiles[0], workers) * len[0] + 1000.f);
   if (n < 2 || together > apart + 5000.f * (float)(n - 1)) {
     for (int i = 0; i < n; ++i) {
       DenseGemmParams one = p;
