@@ -439,6 +439,8 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  *   kept in f32), which may be `residual` itself and overlap nothing else.
  *   act: MOE_ACT_NONE, _SILU or _GELU.  pre_out: f32 [T, N] for moe_linear_backward, or NULL;
  *   NULL with MOE_ACT_NONE, whose backward does not need it.
+ *   The tensor cores cut each step's addends below the largest: pre is off by up to about 4e-6 of
+ *   its terms' norm over 4096 of them (a chain of f32 additions: 6e-7).
  *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
  *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
  *   256-byte aligned, contents irrelevant before and after.  Up to 16 tokens take a kernel
@@ -473,7 +475,8 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
  *   rows [T*k] rows of row_bytes: x[perm / k].  row_scales, or NULL: the same of `scales`.
  *   x: [T] rows of row_bytes bytes (of any type), a multiple of 16 up to 65536; scales: [T]
  *   rows of scale_bytes (0 .. 4096; 0 with scales and row_scales NULL).  T, k and E as in the
- *   conventions above.  Arrays 16-byte aligned; no output may overlap an input.
+ *   conventions above.  Rows and scales 16-byte aligned, the i32 arrays 4; no output may overlap
+ *   an input.
  * Source: "Quick Start", "Fused MoE Dispatch" (permute).                             */
 int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, int T, int k, int E, int row_bytes,
                     int scale_bytes, int32_t* offsets, int32_t* perm, int32_t* inv_perm, void* rows, void* row_scales,
@@ -484,7 +487,7 @@ int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, 
  * over the j whose inv_perm is in [0, T*k); a token without any gets zeros, and no other row
  * of y is read.  With topk_w NULL (all 1) it is the gradient of moe_sort_tokens: d_x of d_rows.
  *   y [T*k, H], out [T, H] of dtype (MOE_DTYPE_BF16, _F16 or _F32); H a multiple of 8, a row
- *   at most 65536 bytes; arrays 16-byte aligned; out may not overlap an input.
+ *   at most 65536 bytes; y and out 16-byte aligned, the others 4; out may not overlap an input.
  * Source: "Quick Start", "Fused MoE Dispatch" (unpermute).                           */
 int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_w, int T, int k, int H, int dtype, void* out,
                       moe_stream_t stream);
@@ -503,7 +506,7 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
  *   indices as routed, not with assignments dropped); gating: moe_route's flag, or 0.
  *   d_logits f32 [T, E]: written whole, 0 where the weights do not depend on the logit.
  *   The selection itself has no gradient.  An expert listed twice gets the sum, an index
- *   outside [0, E) nothing.  Arrays 16-byte aligned; d_logits may not overlap an input. */
+ *   outside [0, E) nothing.  Arrays 4-byte aligned; d_logits may not overlap an input. */
 int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t* topk_idx, const float* topk_w, int T, int k,
                        int E, int gating, float* d_logits, moe_stream_t stream);
 

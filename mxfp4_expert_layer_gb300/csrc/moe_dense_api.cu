@@ -472,9 +472,11 @@ int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, 
   if (scale_bytes < 0 || scale_bytes > kMaxScaleBytes) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!x || !topk_idx || !offsets || !perm || !inv_perm || !rows) return MOE_ERR_INVALID_ARG;
   if ((scales != nullptr) != (scale_bytes > 0) || (row_scales != nullptr) != (scale_bytes > 0)) return MOE_ERR_INVALID_ARG;
-  const void* all[] = {x, scales, topk_idx, offsets, perm, inv_perm, rows, row_scales};
-  for (const void* q : all)
+  const void *moved[] = {x, scales, rows, row_scales}, *words[] = {topk_idx, offsets, perm, inv_perm};
+  for (const void* q : moved)
     if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  for (const void* q : words)
+    if (!aligned(q, 4)) return MOE_ERR_INVALID_ARG;
   // (rows are written while others are still read)
   const size_t n = (size_t)T * k;
   const Span in[] = {{x, (size_t)T * row_bytes}, {scales, (size_t)T * scale_bytes}, {topk_idx, n * 4}};
@@ -502,7 +504,7 @@ int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_
                       moe_stream_t stream) {
   if (!dtype_any(dtype)) return MOE_ERR_INVALID_ARG;
   if (!moved_shape(T, k, H, dtype)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (!y || !inv_perm || !out || !aligned(y, 16) || !aligned(inv_perm, 16) || !aligned(topk_w, 16) || !aligned(out, 16))
+  if (!y || !inv_perm || !out || !aligned(y, 16) || !aligned(inv_perm, 4) || !aligned(topk_w, 4) || !aligned(out, 16))
     return MOE_ERR_INVALID_ARG;
   const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
   const Span in[] = {{y, bytes * k}, {inv_perm, n}, {topk_w, n}}, written[] = {{out, bytes}};
@@ -523,9 +525,11 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
   if (!dtype_any(dtype)) return MOE_ERR_INVALID_ARG;
   if (!moved_shape(T, k, H, dtype)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!d_out || !inv_perm || (!d_y && !d_topk_w) || (d_topk_w && !y)) return MOE_ERR_INVALID_ARG;
-  const void* all[] = {d_out, y, inv_perm, topk_w, d_y, d_topk_w};
-  for (const void* q : all)
+  const void *moved[] = {d_out, y, d_y}, *words[] = {inv_perm, topk_w, d_topk_w};
+  for (const void* q : moved)
     if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  for (const void* q : words)
+    if (!aligned(q, 4)) return MOE_ERR_INVALID_ARG;
   const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
   const Span in[] = {{d_out, bytes}, {y, bytes * k}, {inv_perm, n}, {topk_w, n}}, out[] = {{d_y, bytes * k}, {d_topk_w, n}};
   if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
@@ -549,7 +553,7 @@ int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t
   if (kind < 0) return MOE_ERR_INVALID_ARG;
   const void* need[] = {d_topk_w, logits, topk_idx, topk_w, d_logits};
   for (const void* q : need)
-    if (!q || !aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+    if (!q || !aligned(q, 4)) return MOE_ERR_INVALID_ARG;
   const size_t all = (size_t)T * E * 4, n = (size_t)T * k * 4;
   const Span in[] = {{d_topk_w, n}, {logits, all}, {topk_idx, n}, {topk_w, n}}, out[] = {{d_logits, all}};
   if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;

@@ -373,6 +373,25 @@ def test_results_given():
     assert (out[0] == 7).all() and (out[T + 1] == 7).all()
 
 
+def test_parts_of_a_batch():
+    """Index and weight arrays that begin at any element: slices of a larger routing."""
+    import mxfp4_expert_layer_gb300 as pkg
+    T, k, E, H = 61, 3, 16, 96
+    idx, w, x = routing(T, k, E, 0.1, seed=1), torch.rand(T, k, device="cuda"), rows_of(T, H, BF16, 2)
+    for part in (slice(1, 20), slice(20, 61), slice(3, 4)):
+        n = part.stop - part.start
+        s = pkg.sort_tokens(x[part], idx[part], E)
+        check_sort(s, x[part], idx[part], E)
+        y, inv = rows_of(n * k, H, BF16, 3), torch.empty(n * k + 1, dtype=torch.int32, device="cuda")[1:].view(n, k)
+        inv.copy_(s.inv_perm)
+        check_unsort(pkg.unsort_tokens(y, inv, w[part]), y, s.inv_perm, w[part])
+        check_unsort_grads(pkg.unsort_tokens_backward(x[part], y, inv, w[part]), x[part], y, s.inv_perm, w[part])
+        logits = torch.randn(T, E, device="cuda")[part]
+        got = pkg.route_backward(w[part], logits, idx[part], w[part])
+        want, mag = logits_grad(w[part], logits, idx[part], w[part], "topk")
+        within(got, want, 128 * U32 * mag + floor_of(F32))
+
+
 def test_refusals():
     import mxfp4_expert_layer_gb300 as pkg
     T, k, E, H = 6, 2, 8, 32

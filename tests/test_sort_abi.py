@@ -23,7 +23,7 @@ def test_sort_refusals(L):
                dict(rb=24), dict(rb=65552), dict(sb=-1), dict(sb=4097)):
         assert f(**kw) == L.MOE_ERR_UNSUPPORTED_SHAPE, kw
     for kw in (dict(x=None), dict(idx=None), dict(off=None), dict(perm=None), dict(inv=None), dict(rows=None), dict(x=FAKE + 8),
-               dict(idx=FAKE + 4), dict(rows=FAR + 8), dict(inv=FAR + 4), dict(sc=3 * FAKE), dict(sb=4), dict(sb=4, sc=3 * FAKE),
+               dict(idx=2 * FAKE + 2), dict(rows=FAR + 8), dict(inv=FAR + 2 * FAKE + 2), dict(sc=3 * FAKE), dict(sb=4), dict(sb=4, sc=3 * FAKE),
                dict(sb=4, rsc=FAR + 4 * FAKE), dict(rsc=FAR + 4 * FAKE), dict(rows=FAKE), dict(rows=FAKE + 240), dict(perm=FAKE),
                dict(inv=2 * FAKE), dict(rows=FAKE - 496), dict(sb=4, sc=3 * FAKE, rsc=3 * FAKE)):
         assert f(**kw) == L.MOE_ERR_INVALID_ARG, kw
@@ -39,12 +39,12 @@ def test_unsort_refusals(L):
         for kw in (dict(T=0), dict(k=0), dict(k=33), dict(T=1 << 22, k=5), dict(H=0), dict(H=12), dict(H=32776),
                    dict(H=16392, dt=2)):
             assert call(**kw) == L.MOE_ERR_UNSUPPORTED_SHAPE, kw
-        for kw in (dict(inv=None), dict(y=FAKE + 8), dict(inv=FAKE + 4), dict(w=FAKE + 4), dict(dt=3), dict(dt=-1)):
+        for kw in (dict(inv=None), dict(y=FAKE + 8), dict(inv=3 * FAKE + 2), dict(w=4 * FAKE + 1), dict(dt=3), dict(dt=-1)):
             assert call(**kw) == L.MOE_ERR_INVALID_ARG, kw
     for kw in (dict(y=None), dict(out=None), dict(out=FAR + 8), dict(out=FAKE), dict(out=FAKE + 1008), dict(out=2 * FAKE),
                dict(out=3 * FAKE)):
         assert f(**kw) == L.MOE_ERR_INVALID_ARG, kw
-    for kw in (dict(d=None), dict(y=None), dict(dy=None, dw=None), dict(dy=FAR + 8), dict(dw=FAR + 4), dict(dy=FAKE),
+    for kw in (dict(d=None), dict(y=None), dict(dy=None, dw=None), dict(dy=FAR + 8), dict(dw=FAR + 2), dict(dy=FAKE),
                dict(dy=2 * FAKE), dict(dw=4 * FAKE), dict(dw=3 * FAKE)):
         assert b(**kw) == L.MOE_ERR_INVALID_ARG, kw
 
@@ -54,7 +54,7 @@ def test_route_backward_refusals(L):
         return L.moe_route_backward(dw, l, idx, w, T, k, E, gating, out, None)
     for kw in (dict(T=0), dict(k=0), dict(k=9), dict(E=257), dict(k=33, E=256), dict(T=1 << 24, k=2)):
         assert f(**kw) == L.MOE_ERR_UNSUPPORTED_SHAPE, kw
-    for kw in (dict(dw=None), dict(l=None), dict(idx=None), dict(w=None), dict(out=None), dict(out=FAR + 8), dict(w=FAKE + 8),
+    for kw in (dict(dw=None), dict(l=None), dict(idx=None), dict(w=None), dict(out=None), dict(out=FAR + 2), dict(w=4 * FAKE + 1),
                dict(gating=1), dict(gating=6), dict(gating=8), dict(out=2 * FAKE), dict(out=FAKE), dict(out=4 * FAKE)):
         assert f(**kw) == L.MOE_ERR_INVALID_ARG, kw
 
