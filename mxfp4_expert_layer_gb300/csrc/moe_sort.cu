@@ -159,19 +159,35 @@ __global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThr
   }
 }
 
-// One row of scales of `bytes` bytes to another place, or zeros, by a warp.
-template <typename U>
-__device__ __forceinline__ void move_units(void* dst, const void* src, size_t to, size_t from, int units, bool kept) {
-  for (int i = threadIdx.x & 31; i < units; i += 32)
-    reinterpret_cast<U*>(dst)[to * units + i] = kept ? __ldcg(reinterpret_cast<const U*>(src) + from * units + i) : U(0);
+// A token's scales to the places of its assignments (zeros to those of dropped ones), by a
+// warp: read once, four units a lane at a time.  place(j): as in inv_perm, the same in every lane.
+template <typename U, typename Place>
+__device__ __forceinline__ void move_units(const SortParams& p, size_t t, Place place) {
+  constexpr int kAtOnce = 4;
+  const int units = p.scale_bytes / (int)sizeof(U), lane = threadIdx.x & 31;
+  const U* from = reinterpret_cast<const U*>(p.scales) + t * units;
+  for (int i0 = 0; i0 < units; i0 += 32 * kAtOnce) {
+    U held[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (i0 + 32 * i + lane < units) held[i] = __ldcg(from + i0 + 32 * i + lane);
+    for (int j = 0; j < p.k; ++j) {
+      const int at = place(j);
+      U* to = reinterpret_cast<U*>(p.row_scales) + (size_t)(at >= 0 ? at : -1 - at) * units;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (i0 + 32 * i + lane < units) to[i0 + 32 * i + lane] = at >= 0 ? held[i] : U(0);
+    }
+  }
 }
-__device__ __forceinline__ void move_scales(const SortParams& p, size_t to, size_t from, bool kept) {
+template <typename Place>
+__device__ __forceinline__ void move_scales(const SortParams& p, size_t t, Place place) {
   if ((p.scale_bytes & 3) == 0)
-    move_units<unsigned>(p.row_scales, p.scales, to, from, p.scale_bytes >> 2, kept);
+    move_units<unsigned>(p, t, place);
   else if ((p.scale_bytes & 1) == 0)
-    move_units<unsigned short>(p.row_scales, p.scales, to, from, p.scale_bytes >> 1, kept);
+    move_units<unsigned short>(p, t, place);
   else
-    move_units<unsigned char>(p.row_scales, p.scales, to, from, p.scale_bytes, kept);
+    move_units<unsigned char>(p, t, place);
 }
 
 // Zeros to a dropped assignment's row, by a warp.
@@ -227,11 +243,7 @@ __global__ void __launch_bounds__(128) gather_kernel(const __grid_constant__ Sor
     }
     unsigned gone = __ballot_sync(0xffffffffu, on && at < 0);
     for (; gone; gone &= gone - 1) zero_row(p, -1 - __shfl_sync(0xffffffffu, at, __ffs(gone) - 1));
-    if (p.scale_bytes)
-      for (int j = 0; j < p.k; ++j) {
-        const int to = __shfl_sync(0xffffffffu, at, j);
-        move_scales(p, to >= 0 ? to : -1 - to, t, to >= 0);
-      }
+    if (p.scale_bytes) move_scales(p, t, [&](int j) { return __shfl_sync(0xffffffffu, at, j); });
     if (on) ptx::bulk_wait_read();
     __syncwarp();
     if (lane == 0 && ok && t + (long long)kGatherStages * step < p.T) issue(s, (int)(t + kGatherStages * step));
@@ -325,11 +337,7 @@ __global__ void __launch_bounds__(kFewThreads) sort_few_kernel(const __grid_cons
   for (int i = 0; i < kFewHeld; ++i)
     if (tid + i * kFewThreads < vecs) put(tid + i * kFewThreads, held[i]);
   for (int v = tid + kFewHeld * kFewThreads; v < vecs; v += kFewThreads) put(v, __ldcg(x + v));
-  if (p.scale_bytes)
-    for (int j = warp; j < p.k; j += kFewThreads / 32) {
-      const int at = place[j];
-      move_scales(p, at >= 0 ? at : -1 - at, t, at >= 0);
-    }
+  if (p.scale_bytes && warp == 0) move_scales(p, t, [&](int j) { return place[j]; });
 }
 
 // ------------------------------------------------------------------ back to tokens
@@ -652,7 +660,8 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
   float top = -INFINITY, sum = 0.f, l[kMaxExperts / 32];
   if (all) {
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) l[i] = lane + 32 * i < p.E ? __ldcg(logits + lane + 32 * i) : -INFINITY;
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+      if (32 * i < p.E) l[i] = lane + 32 * i < p.E ? __ldcg(logits + lane + 32 * i) : -INFINITY;
   }
   int e = -1;
   float g = 0.f, w = 0.f;
@@ -670,11 +679,13 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
   if (p.gating == kGatingSigmoid && e >= 0) part *= 1.f / (1.f + expf(__ldcg(logits + e)));
   if (all) {
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) top = fmaxf(top, l[i]);
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+      if (32 * i < p.E) top = fmaxf(top, l[i]);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
 #pragma unroll
     for (int i = 0; i < kMaxExperts / 32; ++i) {
+      if (32 * i >= p.E) break;  // (every expert slot for 8 experts: 6.3 us for 8192 tokens)
       l[i] = lane + 32 * i < p.E ? expf(l[i] - top) : 0.f;
       sum += l[i];
     }
