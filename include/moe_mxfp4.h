@@ -510,8 +510,8 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
 int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t* topk_idx, const float* topk_w, int T, int k,
                        int E, int gating, float* d_logits, moe_stream_t stream);
 
-/* moe_dense_status: the device status of the dense operators' pipelines (feed-forward
- * GEMMs, MXFP4 products, norms' row copies) on the current device, as moe_get_device_status (bits and
+/* moe_dense_status: the device status of the dense operators' pipelines (GEMMs, MXFP4
+ * products, row copies of the norms and of the sorted tokens) on the current device, as moe_get_device_status (bits and
  * returns) for words that the library holds per GPU: synchronises `stream`, reads them
  * into *status and clears them when set.  A bounded wait that gave up sets a bit (the
  * GEMMs' limit is moe_set_wait_limit_ns, the others' 1 s); results of calls since the

@@ -565,7 +565,7 @@ PyObject* sort_tokens(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void *px = need("x", &x, {T, x.size(1)}, x.scalar_type(), device), *pi = need("topk_idx", &idx, {T, k}, at::kInt, device),
          *ps = scales ? need("scales", scales, {T, scales->size(1)}, scales->scalar_type(), device) : nullptr;
     const int t = narrow(T), kk = narrow(k), rb = row_bytes(x), sb = scales ? row_bytes(*scales) : 0;
-    if (T < 1 || k < 1 || E < 1 || T > INT32_MAX / k) refuse("moe_sort_tokens", MOE_ERR_UNSUPPORTED_SHAPE);
+    if (T < 1 || k < 1 || E < k || E > 256 || T > INT32_MAX / k) refuse("moe_sort_tokens", MOE_ERR_UNSUPPORTED_SHAPE);
     const int64_t rows = T * k, H = x.size(1), S = scales ? scales->size(1) : 0;
     const at::ScalarType type = x.scalar_type(), stype = scales ? scales->scalar_type() : type;
     at::Tensor sorted, sorted_scales, offsets, perm, inv;

@@ -135,8 +135,8 @@ def test_many_assignments(T, k, E, H):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
-@pytest.mark.parametrize("T,k,E,H", [(2500, 9, 32, 2888), (1300, 2, 8, 8192), (700, 17, 32, 16384), (3000, 4, 128, 2880),
-                                     (12000, 3, 7, 40), (5000, 8, 64, 4096), (613, 32, 40, 4104)])
+@pytest.mark.parametrize("T,k,E,H", [(2500, 9, 32, 2888), (2000, 2, 8, 8192), (2000, 17, 32, 16384), (3000, 4, 128, 2880),
+                                     (15000, 3, 7, 40), (5000, 8, 64, 4096), (2000, 32, 40, 4104), (1000, 4, 16, 2880)])
 def test_many_tokens_of_wide_rows(T, k, E, H, dtype):
     """Rows in several column chunks, more than eight rows a token, and both at once, where
     persistent blocks take the tokens in turn."""
