@@ -443,8 +443,8 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  *   its terms' norm over 4096 of them (a chain of f32 additions: 6e-7).
  *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
  *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
- *   256-byte aligned, contents irrelevant before and after.  Up to 16 tokens take a kernel
- *   that streams the weights through mma.sync, more the tcgen05 GEMMs.
+ *   256-byte aligned, contents irrelevant before and after.  Few tokens take a kernel that
+ *   streams the weights through mma.sync, batches of up to 128 and more the tcgen05 ones.
  * The pages have no counterpart ("triton-kernels" README, "Kernels", lists the fused GEMMs
  * of the feed-forward block).                                                        */
 size_t moe_linear_workspace_bytes(int T, int K, int N, int backward);

@@ -103,6 +103,23 @@ int check_ffn(int T, int H, int I, int dtype, int act) {
 struct LinearLayout {
   size_t sums, partial, total;
 };
+// Which kernel a projection takes, by sizes (us on one GB300, 16 bits, with bias and residual):
+//   thin    a block for 16 rows of W, while those are one round of blocks: 8 x 4096 -> 4096 8.0 against
+//           9.6 of a batch, 16 x 4096 -> 4096 9.2 against 9.9; beyond, or with more of x to read again by
+//           every block, a batch is faster: 8 x 2880 -> 5120 9.5 against 8.8, 16 x 14336 -> 4096 25.2
+//           against 22.2; one to four tokens stay thin for three rounds (1 x 4096 -> 14336 20.8 against
+//           23.5, 1 x 2880 -> 32768 34.8 against 31.3);
+//   batch   up to 32 tokens (24 x 4096 -> 2880 8.3, tiles 11.6), 64 where K is not short (64 x 4096 ->
+//           2880 9.7 against 12.2, but 64 x 1024 -> 4096 7.3 against 6.4), 128 where K is cut in four at
+//           least (128 x 4096 -> 4096 13.0 against 14.6, but 128 x 2880 -> 5120 15.0 against 12.2);
+//   tiles   else.
+enum class LinearPath { thin, batch, tiles };
+LinearPath linear_path(int T, int K, int N) {
+  const int sms = device_sms(), rows16 = ceil_div(N, kThinRows), rows128 = ceil_div(N, 128);
+  if (T <= 4 ? N <= 16384 : T <= kThinTokens && rows16 <= 2 * sms && T * K <= 98304) return LinearPath::thin;
+  if (T <= 32 || (T <= 64 && K > 1024) || (T <= kBatchTokens && K > 1024 && 4 * rows128 <= sms)) return LinearPath::batch;
+  return LinearPath::tiles;
+}
 LinearLayout linear_layout(int T, int K, int N, bool backward) {
   LinearLayout L{};
   size_t part = 0;
@@ -115,7 +132,7 @@ LinearLayout linear_layout(int T, int K, int N, bool backward) {
     L.partial = align_up(L.sums + (size_t)linear_grad_splits(T, N) * N * sizeof(float), 256);
     need(T, K, N);
     need(N, K, T);
-  } else if (T > kThinTokens) {
+  } else if (linear_path(T, K, N) == LinearPath::tiles) {
     need(T, N, K);
   }
   L.total = L.partial + align_up(part, 256);
@@ -282,7 +299,8 @@ int moe_linear_forward(const void* x, const void* weight, const float* bias, con
   if (L.total && (!workspace || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T <= kThinTokens) {
+  const LinearPath path = linear_path(T, K, N);
+  if (path == LinearPath::thin) {
     ThinParams g{};
     g.x = x;
     g.w = weight;
@@ -307,6 +325,7 @@ int moe_linear_forward(const void* x, const void* weight, const float* bias, con
   g.bias = bias;
   g.residual = residual;
   g.partial = ws_ptr<float>(workspace, L.partial);
+  if (path == LinearPath::batch) return launch_linear_batch(g, {x, T, K, 0}, {weight, N, K, 0}, dtype, out_dtype == MOE_DTYPE_F32, s);
   return launch_dense_gemm(g, {x, T, K, 0}, {weight, N, K, 0}, out_dtype == MOE_DTYPE_F32 ? kDenseLinear32 : kDenseLinear,
                            dtype, s);
 }

@@ -807,6 +807,215 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
   if (warp == 1) tmem_dealloc_g<PAIR>(tmem, C::kTmemCols);
 }
 
+// ------------------------------------------------------------------ projections of a batch
+// Up to 128 tokens: the weights' rows are the MMA's M, the tokens its N, so that every SM
+// streams weights and the results of a warp are neighbours in memory.  A block takes 128 rows;
+// the blocks of a cluster split K and push their sums, by token, into the shared memory of the
+// block that finishes the token (added there in rank order): one launch where the tiles above
+// need a second one to join their K slices.
+template <int TN>
+struct BatchCfg {
+  static constexpr int kStageBytes = 16384 + TN * 128;  // 64 values of K
+  static constexpr int kStages = TN == 128 ? 4 : TN == 64 ? 3 : 4;
+  static constexpr int kSumBytes = TN * 128 * 4;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSumBytes + 1024;
+  static constexpr int kPerSm = TN == 128 ? 1 : 2;
+};
+constexpr int kBatchEpiWarps = 8, kBatchThreads = 64 + 32 * kBatchEpiWarps, kBatchMaxSplit = 8;
+
+template <typename X, int TN, bool WIDE>
+__global__ void __launch_bounds__(kBatchThreads, BatchCfg<TN>::kPerSm) linear_batch_kernel(const __grid_constant__ DenseGemmParams p) {
+  using C = BatchCfg<TN>;
+  using O = std::conditional_t<WIDE, float, X>;
+  extern __shared__ uint8_t dense_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dense_smem_raw) + 1023) & ~uintptr_t(1023));
+  float* const sums = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [split][token of this block's][row]
+  __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages], acc_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t late;
+  const DenseProblem& g = p.g[0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = p.splits;
+  const int rank = S > 1 ? (int)cluster_rank() : 0, tile = blockIdx.x / S;
+  const int k0 = (int)((long long)rank * g.kgroups / S), k1 = (int)((long long)(rank + 1) * g.kgroups / S);
+  const int per = (g.M + S - 1) / S;  // tokens that a block finishes
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(&acc_bar, 1);
+    late = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&g.tm_a);
+    tma_prefetch_desc(&g.tm_b);
+  }
+  constexpr uint32_t kCols = TN < 32 ? 32 : TN;
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (S > 1) cluster_arrive_release();  // (this block has started: its sums may be written)
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (warp == 0) {
+    const uint32_t base = smem_u32(smem);
+    int s = 0;
+    uint32_t phase = 0;
+    for (int k = k0; k < k1; ++k) {
+      if (!wait_warp(&empty_bar[s], phase ^ 1, p.wait_ns)) {
+        give_up(&late, kStatusTimeoutProducer);
+        break;
+      }
+      const uint32_t bar = smem_u32(&full_bar[s]), dst = base + s * C::kStageBytes;
+      mbar_arrive_expect_tx_if(lane == 0, &full_bar[s], C::kStageBytes);
+      tma_load_2d<false>(dst, &g.tm_a, bar, k * 64, tile * 128);
+      tma_load_2d<false>(dst + 16384, &g.tm_b, bar, k * 64, 0);
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t kFmt = std::is_same<X, __half>::value ? 0u : 1u;
+    constexpr uint32_t idesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
+    const uint64_t a_desc = smem_desc(smem_u32(smem), 16, 1024, 2), b_desc = smem_desc(smem_u32(smem) + 16384, 16, 1024, 2);
+    int s = 0;
+    uint32_t phase = 0;
+    for (int k = k0; k < k1; ++k) {
+      if (!wait_warp(&full_bar[s], phase, p.wait_ns)) {
+        give_up(&late, kStatusTimeoutMain);
+        break;
+      }
+      tc_fence_after();
+      const uint64_t at = (uint64_t)(s * (C::kStageBytes / 16));
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_f16<false>(tmem, a_desc + at + (uint64_t)(2 * ks), b_desc + at + (uint64_t)(2 * ks), idesc, k > k0 || ks > 0 ? 1u : 0u);
+      commit<false>(&empty_bar[s]);
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    }
+    // (also after a time-out: the sums' readers and the tensor memory's release wait for what was issued)
+    commit<false>(&acc_bar);
+    if (!wait_warp(&acc_bar, 0, kDrainLimit)) give_up(&late, kStatusTimeoutMain);
+  }
+  // the tokens that this block finishes, a warp to each in turn, a lane to four neighbouring rows;
+  // the residual of the first ones comes in while the products run
+  constexpr int kAtOnce = 4;
+  const int n = tile * 128 + 4 * lane, mine = min(per, g.M - rank * per), w0 = warp - 2;
+  using Four = std::conditional_t<WIDE, uint4, uint2>;
+  Four res[kAtOnce];
+  auto load_residual4 = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int t = w0 + kBatchEpiWarps * (i0 + i);
+      if (p.residual && t < mine && n < g.N)
+        res[i] = __ldcg(reinterpret_cast<const Four*>(reinterpret_cast<const O*>(p.residual) + (size_t)(rank * per + t) * g.N + n));
+    }
+  };
+  if (warp >= 2) load_residual4(0);
+  const int q = warp & 3, row = q * 32 + lane;
+  if (warp >= 2 && !wait_warp(&acc_bar, 0, p.wait_ns + kDrainLimit)) give_up(&late, kStatusTimeoutEpi);
+  __syncwarp();
+  if (S > 1) cluster_wait_acquire();
+  tc_fence_after();
+  if (warp >= 2) {
+    // (two warps a quarter of the rows, sixteen tokens each in turn)
+#pragma unroll 1
+    for (int c = 16 * (w0 >> 2); c < g.M; c += 32) {
+      int owner = c / per, local = c - owner * per;  // of token c + i
+      uint32_t raw[16];
+      float v[16];
+      tmem_ld_32x32b_x16(tmem + ((uint32_t)(q * 32) << 16) + c, raw);
+      const uint32_t first = smem_u32(sums + rank * per * 128 + row);  // of the owner's first token
+      uint32_t to = (S > 1 ? mapa_shared(first, owner) : first) + local * 512;
+      tmem_wait_ld();
+      landed(raw, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (c + i >= g.M) break;
+        if (S > 1)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v[i]) : "memory");
+        else
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v[i]) : "memory");
+        to += 512;
+        if (++local == per) {
+          local = 0;
+          ++owner;
+          to = S > 1 && owner < S ? mapa_shared(first, owner) : first;
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (S > 1) {
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kCols);
+  if (warp >= 2 && n < g.N) {  // (N is a multiple of 8: four rows are all in it, or none)
+    float bias[4] = {};
+    if (p.bias) {
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(p.bias + n));
+      bias[0] = b.x; bias[1] = b.y; bias[2] = b.z; bias[3] = b.w;
+    }
+    O* out = reinterpret_cast<O*>(g.out);
+    for (int i0 = 0; w0 + kBatchEpiWarps * i0 < mine; i0 += kAtOnce) {
+      if (i0 > 0) load_residual4(i0);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int t = w0 + kBatchEpiWarps * (i0 + i);
+        if (t >= mine) break;
+        const size_t at = (size_t)(rank * per + t) * g.N + n;
+        float v[4] = {};
+        for (int b = 0; b < S; ++b) {
+          const float4 f = *reinterpret_cast<const float4*>(sums + (b * per + t) * 128 + 4 * lane);
+          v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += bias[j];
+        if (p.gateup) *reinterpret_cast<float4*>(p.gateup + at) = make_float4(v[0], v[1], v[2], v[3]);
+        if (p.act == kActSilu) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = act_f<kActSilu>(v[j]);
+        } else if (p.act == kActGelu) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = act_f<kActGelu>(v[j]);
+        }
+        if constexpr (WIDE) {
+          if (p.residual) {
+            v[0] += __uint_as_float(res[i].x); v[1] += __uint_as_float(res[i].y);
+            v[2] += __uint_as_float(res[i].z); v[3] += __uint_as_float(res[i].w);
+          }
+          *reinterpret_cast<float4*>(out + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          if (p.residual) {
+            const float2 a = unpack2<X>(res[i].x), b = unpack2<X>(res[i].y);
+            v[0] += a.x; v[1] += a.y; v[2] += b.x; v[3] += b.y;
+          }
+          *reinterpret_cast<uint2*>(out + at) = make_uint2(pack2<X>(v[0], v[1]), pack2<X>(v[2], v[3]));
+        }
+      }
+    }
+  }
+  // after a time-out some copies may still be on their way: stay until they have surely landed
+  __syncthreads();
+  if (threadIdx.x == 0 && late) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kLandingNs) __nanosleep(1000);
+  }
+}
+
 // The split tiles: the slices' sums in slice order, then the epilogue (about 4 us, from L2).
 // 16 columns (of gate and of up) per thread.
 template <typename X, int MODE>
@@ -1103,6 +1312,55 @@ int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const
   const cudaError_t e = dtype == kDtypeF16
                             ? launch_kernel<__half, kDenseProducts, 256, true>(q, tiles[0] + tiles[1], stream)
                             : launch_kernel<__nv_bfloat16, kDenseProducts, 256, true>(q, tiles[0] + tiles[1], stream);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+namespace {
+template <typename X, int TN, bool WIDE>
+cudaError_t launch_batch_t(const DenseGemmParams& p, cudaStream_t stream) {
+  using C = BatchCfg<TN>;
+  auto kern = linear_batch_kernel<X, TN, WIDE>;
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in.ensure(kern, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(p.g[0].N, 128) * p.splits);
+  cfg.blockDim = dim3(kBatchThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)p.splits, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+template <typename X, int TN>
+cudaError_t launch_batch_out(const DenseGemmParams& p, bool wide, cudaStream_t stream) {
+  return wide ? launch_batch_t<X, TN, true>(p, stream) : launch_batch_t<X, TN, false>(p, stream);
+}
+template <typename X>
+cudaError_t launch_batch_x(const DenseGemmParams& p, int tn, bool wide, cudaStream_t stream) {
+  return tn == 32 ? launch_batch_out<X, 32>(p, wide, stream)
+         : tn == 64 ? launch_batch_out<X, 64>(p, wide, stream)
+                    : launch_batch_out<X, 128>(p, wide, stream);
+}
+}  // namespace
+
+int launch_linear_batch(DenseGemmParams p, const DenseOperand& x, const DenseOperand& w, int dtype, bool wide, cudaStream_t stream) {
+  DenseProblem& g = p.g[0];
+  const int tn = g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128, tiles = ceil_div(g.N, 128);
+  g.kgroups = ceil_div(g.K, 64);
+  p.wait_ns = gemm_wait_limit_ns();
+  // K is split while the blocks find room and keep two groups each
+  p.splits = 1;
+  while (p.splits < kBatchMaxSplit && tiles * 2 * p.splits <= (tn == 128 ? 1 : 2) * device_sms() && g.kgroups >= 4 * p.splits)
+    p.splits *= 2;
+  if (!operand_map(&g.tm_a, w, 128, dtype) || !operand_map(&g.tm_b, x, tn, dtype)) return MOE_ERR_CUDA;
+  const cudaError_t e = dtype == kDtypeF16 ? launch_batch_x<__half>(p, tn, wide, stream)
+                                           : launch_batch_x<__nv_bfloat16>(p, tn, wide, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

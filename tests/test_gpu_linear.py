@@ -120,6 +120,17 @@ def test_small_tiles(T, K, N, dtype, out, act):
     check(make(T, K, N, dtype, out, seed=T + K), act)
 
 
+@pytest.mark.parametrize("act,residual", [("none", True), ("gelu", False), ("silu", True)])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)])
+@pytest.mark.parametrize("T,K,N", [(24, 64, 128), (32, 8, 8), (17, 520, 136), (33, 1096, 520), (61, 1160, 264), (64, 4096, 2880),
+                                   (48, 1088, 20000), (100, 2880, 328), (128, 4104, 4096), (65, 16384, 136), (5, 72, 5000),
+                                   (16, 14344, 512), (1, 72, 16400)])
+def test_batches(T, K, N, dtype, out, act, residual):
+    """Blocks of 128 weight rows: every width of the token side, K whole and cut in two to eight
+    (by short K, by many rows), tokens that do not divide by the cut, partial blocks of rows."""
+    check(make(T, K, N, dtype, out, residual=residual, seed=T + N), act, backward=False)
+
+
 @pytest.mark.parametrize("T,K,N,act,out", [(1001, 2880, 2880, "gelu", BF16), (2048, 1024, 1032, "silu", F32),
                                            (257, 4104, 4096, "none", F32), (4096, 264, 3000, "gelu", BF16),
                                            (1500, 2880, 1448, "none", BF16)])
@@ -132,6 +143,8 @@ def test_pair_tiles(T, K, N, act, out):
 def test_split_k(out):
     check(make(64, 16384, 1024, BF16, out, seed=1), "silu")
     check(make(40, 30000, 264, BF16, out, seed=2), "none", backward=False)
+    check(make(150, 16384, 1024, BF16, out, seed=4), "silu", backward=False)
+    check(make(200, 8192, 136, BF16, out, seed=5), "gelu", backward=False)
     check(make(3000, 72, 40, BF16, out, seed=3), "gelu")
 
 
@@ -143,7 +156,7 @@ def test_absent_arguments(T, K, N, bias, residual):
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 136, 200), (16, 520, 1000), (70, 136, 200), (700, 520, 1032), (64, 16384, 1024),
-                                   (2048, 264, 4096)])
+                                   (2048, 264, 4096), (40, 264, 1000), (100, 4096, 520), (80, 30000, 2000)])
 @pytest.mark.parametrize("out", [BF16, F32])
 def test_onto_the_residual(T, K, N, out):
     """out may be the residual: the same bits as apart."""

@@ -15,7 +15,8 @@ def L():
 
 
 def test_sizes(L):
-    assert L.moe_linear_workspace_bytes(16, 4096, 2880, 0) == 0     # few tokens: one launch
+    for T in (1, 16, 64, 128):
+        assert L.moe_linear_workspace_bytes(T, 4096, 2880, 0) == 0  # few tokens and batches: one launch
     assert L.moe_linear_workspace_bytes(4096, 4096, 4096, 1) >= 4096 * 4096 * 2
     for T, K, N in ((0, 64, 64), ((1 << 24) + 1, 64, 64), (4, 60, 64), (4, 64, 60), (4, 0, 64), (4, 64, 0),
                     (4, (1 << 17) + 8, 64), (4, 64, (1 << 20) + 8)):
@@ -32,9 +33,9 @@ def test_forward_refusals(L):
                dict(act=0, pre=FAR + FAKE + 4), dict(out=FAKE), dict(out=FAKE + 496), dict(out=2 * FAKE), dict(out=3 * FAKE),
                dict(r=FAR + 16), dict(act=0, pre=FAR), dict(act=0, pre=FAKE), dict(act=0, pre=4 * FAKE, r=4 * FAKE)):
         assert f(**kw) == L.MOE_ERR_INVALID_ARG, kw
-    need = L.moe_linear_workspace_bytes(64, 16384, 1024, 0)
+    need = L.moe_linear_workspace_bytes(160, 16384, 1024, 0)
     assert need > 0
-    big = dict(T=64, K=16384, N=1024, w=64 * FAKE)
+    big = dict(T=160, K=16384, N=1024, w=64 * FAKE)
     assert f(**big, ws=FAR + 64 * FAKE, n=need - 1) == L.MOE_ERR_WORKSPACE_TOO_SMALL
     assert f(**big, ws=None, n=need) == L.MOE_ERR_INVALID_ARG
     assert f(**big, ws=FAR + 16, n=need) == L.MOE_ERR_INVALID_ARG
