@@ -332,7 +332,8 @@ struct DenseOperand {
 size_t dense_partial_bytes(int M, int N, int K, int mode, bool b_mn);
 int launch_dense_gemm(DenseGemmParams p, const DenseOperand& a, const DenseOperand& b, int mode, int dtype,
                       cudaStream_t stream);
-// A projection (bias, act, residual, gateup as kDenseLinear) of up to kBatchTokens tokens.
+// A projection (bias, act, residual, gateup as kDenseLinear) of up to kBatchTokens tokens, or,
+// with w MN-major, the product with its columns.
 constexpr int kBatchTokens = 128;
 int launch_linear_batch(DenseGemmParams p, const DenseOperand& x, const DenseOperand& w, int dtype, bool wide, cudaStream_t stream);
 // Up to kDenseGroup plain products (g[i].M, N, K, out set) whose K takes at most two values,

@@ -113,12 +113,16 @@ struct LinearLayout {
 //           2880 9.7 against 12.2, but 64 x 1024 -> 4096 7.3 against 6.4), 128 where K is cut in four at
 //           least (128 x 4096 -> 4096 13.0 against 14.6, but 128 x 2880 -> 5120 15.0 against 12.2);
 //   tiles   else.
+// The gradient into x of a batch takes the same kernel (64 tokens: 27 us against 22 at 4096 <- 14336,
+// 9.9 against 7 at 2880 <- 2880).
 enum class LinearPath { thin, batch, tiles };
+bool linear_batch(int T, int K, int N) {
+  return T <= 32 || (T <= 64 && K > 1024) || (T <= kBatchTokens && K > 1024 && 4 * ceil_div(N, 128) <= device_sms());
+}
 LinearPath linear_path(int T, int K, int N) {
-  const int sms = device_sms(), rows16 = ceil_div(N, kThinRows), rows128 = ceil_div(N, 128);
+  const int sms = device_sms(), rows16 = ceil_div(N, kThinRows);
   if (T <= 4 ? N <= 16384 : T <= kThinTokens && rows16 <= 2 * sms && T * K <= 98304) return LinearPath::thin;
-  if (T <= 32 || (T <= 64 && K > 1024) || (T <= kBatchTokens && K > 1024 && 4 * rows128 <= sms)) return LinearPath::batch;
-  return LinearPath::tiles;
+  return linear_batch(T, K, N) ? LinearPath::batch : LinearPath::tiles;
 }
 LinearLayout linear_layout(int T, int K, int N, bool backward) {
   LinearLayout L{};
@@ -365,6 +369,15 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
     if (launch_linear_grad(g, dtype, out_dtype, s) != cudaSuccess) return MOE_ERR_CUDA;
   }
   if (!products) return MOE_OK;
+  const bool batch = d_x && linear_batch(T, N, K);
+  if (batch) {
+    DenseGemmParams b{};
+    b.g[0].M = T; b.g[0].N = K; b.g[0].K = N;
+    b.g[0].out = d_x;
+    b.act = MOE_ACT_NONE;
+    const int launched = launch_linear_batch(b, {dp, T, N, 0}, {weight, N, K, 1}, dtype, false, s);
+    if (launched != MOE_OK || !d_weight) return launched;
+  }
   DenseGemmParams q{};
   q.partial = ws_ptr<float>(workspace, L.partial);
   DenseOperand a[kDenseGroup], b[kDenseGroup];
@@ -376,7 +389,7 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
     a[n] = am;
     b[n++] = bm;
   };
-  product(T, K, N, {dp, T, N, 0}, {weight, N, K, 1}, d_x);
+  product(T, K, N, {dp, T, N, 0}, {weight, N, K, 1}, batch ? nullptr : d_x);
   product(N, K, T, {dp, T, N, 1}, {x, T, K, 1}, d_weight);
   return launch_dense_products(q, n, a, b, dtype, true, s);
 }

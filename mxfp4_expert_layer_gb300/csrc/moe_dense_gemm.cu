@@ -808,7 +808,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) dense_gemm_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ projections of a batch
-// Up to 128 tokens: the weights' rows are the MMA's M, the tokens its N, so that every SM
+// Up to 128 tokens: the weights' rows (for the gradient into x, their columns: an MN-major
+// operand) are the MMA's M, the tokens its N, so that every SM
 // streams weights and the results of a warp are neighbours in memory.  A block takes 128 rows;
 // the blocks of a cluster split K and push their sums, by token, into the shared memory of the
 // block that finishes the token (added there in rank order): one launch where the tiles above
@@ -872,7 +873,12 @@ __global__ void __launch_bounds__(kBatchThreads, BatchCfg<TN>::kPerSm) linear_ba
       }
       const uint32_t bar = smem_u32(&full_bar[s]), dst = base + s * C::kStageBytes;
       mbar_arrive_expect_tx_if(lane == 0, &full_bar[s], C::kStageBytes);
-      tma_load_2d<false>(dst, &g.tm_a, bar, k * 64, tile * 128);
+      if (g.a_mn) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tma_load_2d<false>(dst + c * 8192, &g.tm_a, bar, tile * 128 + 64 * c, k * 64);
+      } else {
+        tma_load_2d<false>(dst, &g.tm_a, bar, k * 64, tile * 128);
+      }
       tma_load_2d<false>(dst + 16384, &g.tm_b, bar, k * 64, 0);
       if (++s == C::kStages) {
         s = 0;
@@ -881,8 +887,11 @@ __global__ void __launch_bounds__(kBatchThreads, BatchCfg<TN>::kPerSm) linear_ba
     }
   } else if (warp == 1) {
     constexpr uint32_t kFmt = std::is_same<X, __half>::value ? 0u : 1u;
-    constexpr uint32_t idesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
-    const uint64_t a_desc = smem_desc(smem_u32(smem), 16, 1024, 2), b_desc = smem_desc(smem_u32(smem) + 16384, 16, 1024, 2);
+    const uint32_t idesc =
+        (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((uint32_t)g.a_mn << 15) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t a_step = g.a_mn ? 128 : 2;  // (operand forms as in dense_gemm_kernel)
+    const uint64_t a_desc = smem_desc(smem_u32(smem), g.a_mn ? 8192 : 16, 1024, 2);
+    const uint64_t b_desc = smem_desc(smem_u32(smem) + 16384, 16, 1024, 2);
     int s = 0;
     uint32_t phase = 0;
     for (int k = k0; k < k1; ++k) {
@@ -894,7 +903,8 @@ __global__ void __launch_bounds__(kBatchThreads, BatchCfg<TN>::kPerSm) linear_ba
       const uint64_t at = (uint64_t)(s * (C::kStageBytes / 16));
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        mma_f16<false>(tmem, a_desc + at + (uint64_t)(2 * ks), b_desc + at + (uint64_t)(2 * ks), idesc, k > k0 || ks > 0 ? 1u : 0u);
+        mma_f16<false>(tmem, a_desc + at + (uint64_t)(a_step * ks), b_desc + at + (uint64_t)(2 * ks), idesc,
+                       k > k0 || ks > 0 ? 1u : 0u);
       commit<false>(&empty_bar[s]);
       if (++s == C::kStages) {
         s = 0;
@@ -1358,7 +1368,8 @@ int launch_linear_batch(DenseGemmParams p, const DenseOperand& x, const DenseOpe
   p.splits = 1;
   while (p.splits < kBatchMaxSplit && tiles * 2 * p.splits <= (tn == 128 ? 1 : 2) * device_sms() && g.kgroups >= 4 * p.splits)
     p.splits *= 2;
-  if (!operand_map(&g.tm_a, w, 128, dtype) || !operand_map(&g.tm_b, x, tn, dtype)) return MOE_ERR_CUDA;
+  g.a_mn = w.mn_major;
+  if (!operand_map(&g.tm_a, w, w.mn_major ? 64 : 128, dtype) || !operand_map(&g.tm_b, x, tn, dtype)) return MOE_ERR_CUDA;
   const cudaError_t e = dtype == kDtypeF16 ? launch_batch_x<__half>(p, tn, wide, stream)
                                            : launch_batch_x<__nv_bfloat16>(p, tn, wide, stream);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

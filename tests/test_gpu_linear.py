@@ -131,6 +131,15 @@ def test_batches(T, K, N, dtype, out, act, residual):
     check(make(T, K, N, dtype, out, residual=residual, seed=T + N), act, backward=False)
 
 
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("T,K,N", [(24, 128, 64), (32, 8, 8), (1, 136, 520), (33, 520, 1096), (61, 264, 1160), (64, 2880, 4096),
+                                   (48, 20000, 1088), (100, 328, 2880), (128, 4096, 4104), (65, 136, 16384), (5, 5000, 72)])
+def test_gradients_of_batches(T, K, N, dtype, out, act):
+    """The same sizes, with K and N changed, for the gradient into x."""
+    check(make(T, K, N, dtype, out, seed=T + N), act)
+
+
 @pytest.mark.parametrize("T,K,N,act,out", [(1001, 2880, 2880, "gelu", BF16), (2048, 1024, 1032, "silu", F32),
                                            (257, 4104, 4096, "none", F32), (4096, 264, 3000, "gelu", BF16),
                                            (1500, 2880, 1448, "none", BF16)])
