@@ -269,6 +269,14 @@ struct ThinParams {
   const void* residual;     // projections: [T, n_out] of out's type, or null
   int out_f32;              // projections: out's type
 };
+// Outer products of up to kThinOuterTokens tokens: out [N, K] = a^T b, a [T, N], b [T, K].
+constexpr int kThinOuterTokens = 64;
+struct ThinOuterParams {
+  const void *a, *b;
+  int T, N, K;
+  void* out;
+};
+cudaError_t launch_thin_outer(const ThinOuterParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_thin_linear(const ThinParams& p, int dtype, cudaStream_t stream);
 cudaError_t launch_matvec(const ThinParams& p, int dtype, bool gated, cudaStream_t stream);
 cudaError_t launch_thin16(const ThinParams& p, int dtype, bool gated, cudaStream_t stream);

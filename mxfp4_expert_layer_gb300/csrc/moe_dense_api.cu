@@ -378,6 +378,19 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
     const int launched = launch_linear_batch(b, {dp, T, N, 0}, {weight, N, K, 1}, dtype, false, s);
     if (launched != MOE_OK || !d_weight) return launched;
   }
+  // The weights' gradient from few tokens is written more than computed (us, tiles against this: 1 x
+  // 4096 -> 14336 38.8 and 27.0, 16 tokens 37.3 and 35.3, 64 37.6 and 55.8; 64 x 1024 -> 4096 5.8 and 4.8).
+  const bool outer = T <= 16 || (T <= kThinOuterTokens && (long long)N * K <= 1 << 23);
+  if (outer && d_weight && (batch || !d_x)) {
+    ThinOuterParams o{};
+    o.a = dp;
+    o.b = x;
+    o.T = T;
+    o.N = N;
+    o.K = K;
+    o.out = d_weight;
+    return cuda_status(launch_thin_outer(o, dtype, s));
+  }
   DenseGemmParams q{};
   q.partial = ws_ptr<float>(workspace, L.partial);
   DenseOperand a[kDenseGroup], b[kDenseGroup];
