@@ -150,6 +150,23 @@ def test_widest_rows(H):
         all_of(13, 2, 16, H, F32, 0.1, seed=H)
 
 
+@pytest.mark.parametrize("T,k,E,drop", [(512, 4, 128, 0.0), (2048, 1, 9, 0.2), (683, 3, 7, 0.1), (2049, 1, 256, 0.0), (128, 16, 16, 0.3),
+                                        (8192, 8, 32, 0.0), (8193, 8, 31, 0.01)])
+def test_where_the_ways_to_the_order_meet(T, k, E, drop):
+    """2048 assignments and the next: one launch and two; 65536 and more: runs in registers and not."""
+    all_of(T, k, E, 48, BF16, drop, seed=T)
+
+
+@pytest.mark.parametrize("dtype", [torch.float64, torch.int32, torch.int64, torch.bool, torch.float8_e5m2, torch.complex64])
+def test_rows_of_any_type(dtype):
+    import mxfp4_expert_layer_gb300 as pkg
+    for T in (7, 3000):
+        x = torch.randint(0, 256, (T, 80), device="cuda", dtype=torch.uint8)
+        x = (x & 1 if dtype == torch.bool else x).view(dtype)
+        idx = routing(T, 2, 16, 0.2, seed=T)
+        check_sort(pkg.sort_tokens(x, idx, 16), x, idx, 16)
+
+
 def test_without_weights():
     all_of(77, 4, 16, 136, F16, 0.1, weighted=False)
 
@@ -307,6 +324,24 @@ def test_logits_gradient(T, k, E, gating):
     (ref,) = torch.autograd.grad(weights64(l, idx, gating), l, d_w.double())
     # against the definition: w is an input here, itself rounded by the routing (its tests hold it to 1e-5)
     within(got, ref, 128 * U32 * mag + 2e-5 * mag + floor_of(F32))
+
+
+@pytest.mark.parametrize("lowest", [float("-inf"), torch.finfo(F32).min])
+@pytest.mark.parametrize("gating", list(GATINGS))
+def test_logits_gradient_of_masked_experts(gating, lowest):
+    """Experts masked by -inf or the type's lowest value get no gradient, and give no NaN, also
+    where fewer experts than k are left."""
+    import mxfp4_expert_layer_gb300 as pkg
+    T, k, E = 40, 4, 48
+    logits = rows_of(T, E, F32, 1)
+    logits[:, 5:] = lowest
+    logits[::2, 2:] = lowest
+    logits, idx, w = pkg.route(None, None, k, logits=logits, from_logits=True, gating=GATINGS[gating])
+    d_w = rows_of(T, k, F32, 2)
+    got = pkg.route_backward(d_w, logits, idx, w, gating=GATINGS[gating])
+    want, mag = logits_grad(d_w, logits, idx, w, gating)
+    within(got, want, 128 * U32 * mag + floor_of(F32))
+    assert not got[:, 5:].any() and not got[::2, 2:].any()
 
 
 @pytest.mark.parametrize("gating", list(GATINGS))
