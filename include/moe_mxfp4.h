@@ -336,7 +336,7 @@ int moe_tensor_peak(int kind, int mmas_per_sm, double* tflops, moe_stream_t stre
  * (MOE_DTYPE_BF16 or MOE_DTYPE_F16); every array is contiguous, row major.           */
 #define MOE_DTYPE_BF16 0
 #define MOE_DTYPE_F16 1
-#define MOE_DTYPE_F32 2 /* only as stream_dtype of the norms */
+#define MOE_DTYPE_F32 2 /* where a function names it: the norms' stream, out of a projection, rows */
 
 #define MOE_GATE_NONE 0
 #define MOE_GATE_FEATURE 1 /* gate [H], of `dtype`                                    */
@@ -439,8 +439,9 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  *   kept in f32), which may be `residual` itself and overlap nothing else.
  *   act: MOE_ACT_NONE, _SILU or _GELU.  pre_out: f32 [T, N] for moe_linear_backward, or NULL;
  *   NULL with MOE_ACT_NONE, whose backward does not need it.
- *   The tensor cores cut each step's addends below the largest: pre is off by up to about 4e-6 of
- *   its terms' norm over 4096 of them (a chain of f32 additions: 6e-7).
+ *   The tensor cores cut each step's addends below the largest: of its terms' norm, pre is off by
+ *   4e-6 rms over 4096 terms (2.5e-5 the worst of 4 million; a chain of f32 additions: 6e-7 rms),
+ *   by more the longer the sum.
  *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
  *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
  *   256-byte aligned, contents irrelevant before and after.  Few tokens take a kernel that
