@@ -514,10 +514,10 @@ int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t
 /* moe_dense_status: the device status of the dense operators' pipelines (GEMMs, MXFP4
  * products, row copies of the norms and of the sorted tokens) on the current device, as moe_get_device_status (bits and
  * returns) for words that the library holds per GPU: synchronises `stream`, reads them
- * into *status and clears them when set.  A bounded wait that gave up sets a bit (the
- * GEMMs' limit is moe_set_wait_limit_ns, the others' 1 s); results of calls since the
- * last reading are then not reliable.  The launch that gave up stays until its copies
- * have landed (20 ms); others are not held up.  Not for the hot path.                */
+ * into *status and clears them when set.  A bounded wait that gave up sets a bit (the limit
+ * of the GEMMs and of the sorted tokens' rows is moe_set_wait_limit_ns's, the others' 1 s);
+ * results of calls since the last reading are then not reliable.  The launch that gave up
+ * stays until its copies have landed (20 ms); others are not held up.  Not for the hot path. */
 int moe_dense_status(int* status, moe_stream_t stream);
 
 /* moe_prepare_matvec: one-time re-layout of raw MXFP4 weights [rows][K/2] codes and
@@ -552,10 +552,10 @@ size_t moe_matvec_workspace_bytes(int T, int K);
 int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int rows, int K, int kind, int act,
                      int dtype, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
-/* moe_set_wait_limit_ns: how long (ns) each pipeline wait of the expert GEMMs (and of
- * the dense feed-forward GEMMs, whose status moe_dense_status reads) may take before it gives up, for launches made after the call (process-wide; 0
- * restores the default of 1 s; at most 10 s, else MOE_ERR_INVALID_ARG).  A wait
- * that gives up sets a bit of the workspace status word (moe_get_device_status), the
+/* moe_set_wait_limit_ns: how long (ns) each pipeline wait of the expert GEMMs (and of the
+ * dense GEMMs and the copies of sorted tokens' rows, whose status moe_dense_status reads) may
+ * take before it gives up, for launches made after the call (process-wide; 0 restores the
+ * default of 1 s; at most 10 s, else MOE_ERR_INVALID_ARG).  A wait that gives up sets a bit of the workspace status word (moe_get_device_status), the
  * kernel drops its remaining work, waits (up to 1 s) for the copies and tensor-core
  * operations it has already issued, frees its tensor memory and exits: no trap, and
  * the context stays usable.  Limits under 2 us are polled without suspending the

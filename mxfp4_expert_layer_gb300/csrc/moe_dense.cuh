@@ -184,6 +184,7 @@ struct SortParams {
   int T, k, E, row_bytes, scale_bytes;
   int32_t *offsets, *perm, *inv_perm;  // [E + 1], [T k], [T k]
   void *rows, *row_scales;  // [T k] rows
+  uint64_t wait_ns;         // limit of a wait for a row
 };
 struct UnsortParams {
   const void* y;            // [T k, H]
@@ -191,6 +192,7 @@ struct UnsortParams {
   const float* w;           // [T, k] or null: 1
   int T, k, H;
   void* out;                // [T, H]
+  uint64_t wait_ns;         // limit of a wait for a row
 };
 struct UnsortBackwardParams {
   UnsortParams f;           // out unused

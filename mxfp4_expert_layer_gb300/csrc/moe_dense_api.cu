@@ -542,6 +542,7 @@ int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, 
   p.inv_perm = inv_perm;
   p.rows = rows;
   p.row_scales = row_scales;
+  p.wait_ns = gemm_wait_limit_ns();
   return cuda_status(launch_sort(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -562,6 +563,7 @@ int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_
   p.k = k;
   p.H = H;
   p.out = out;
+  p.wait_ns = gemm_wait_limit_ns();
   return cuda_status(launch_unsort(p, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -585,6 +587,7 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
   q.f.T = T;
   q.f.k = k;
   q.f.H = H;
+  q.f.wait_ns = gemm_wait_limit_ns();
   q.d_out = d_out;
   q.d_y = d_y;
   q.d_w = d_topk_w;

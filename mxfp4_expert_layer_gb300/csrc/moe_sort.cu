@@ -16,7 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kKeys = kMaxExperts + 1;  // the experts, and what is dropped
-constexpr uint64_t kCopyWaitNs = 1000000000ull;  // a wait for a row may take 1 s
+constexpr uint64_t kLandingNs = 20000000ull;  // after a wait that gave up: in this time every issued copy has landed (20 ms)
 
 __device__ uint32_t g_sort_status;  // bits as in the layer's status word
 
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(128) gather_kernel(const __grid_constant__ Sor
   for (long long t = t0; t < p.T; t += step) {
     const int at = next;
     if (t + step < p.T && lane < p.k) next = __ldcg(p.inv_perm + (size_t)(t + step) * p.k + lane);
-    if (ok && !ptx::mbar_wait_bounded(&bar[s], phase, kCopyWaitNs)) ok = false;
+    if (ok && !ptx::mbar_wait_bounded(&bar[s], phase, p.wait_ns)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     const bool on = lane < p.k;
     if (on) {  // (here, where every SM writes, and not by the few that found the order)
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(128) gather_kernel(const __grid_constant__ Sor
   if (!ok && lane == 0) {
     report_status(&g_sort_status, kStatusTimeoutMain);
     const uint64_t since = ptx::globaltimer_ns();
-    while (ptx::globaltimer_ns() - since < kCopyWaitNs / 50) __nanosleep(1000);
+    while (ptx::globaltimer_ns() - since < kLandingNs) __nanosleep(1000);
   }
 }
 
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
   __shared__ uint64_t full_bar[kMaxRowStages], empty_bar[kMaxRowStages];
   __shared__ RowStage info[kMaxRowStages];
   __shared__ float part[2][kRowThreads / 32][kGroupRows];
+  __shared__ volatile uint32_t late;  // a taker gave up its wait: what it frees has not been filled
   const UnsortParams& p = q.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.k, takers = (blockDim.x >> 5) - 1;
   const bool need_y = !BACKWARD || q.d_w;
@@ -503,6 +504,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
       ptx::mbar_init(&full_bar[s], 1);
       ptx::mbar_init(&empty_bar[s], takers);
     }
+    late = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
           const float my_w = __shfl_sync(0xffffffffu, w, (g * kGroupRows + j) & 31);
           const bool live = j < here && row_of(my_at, n) >= 0 && need_y;
           const int copies = __popc(__ballot_sync(0xffffffffu, live)) + (BACKWARD ? 1 : 0);
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&empty_bar[s], phase ^ 1, kCopyWaitNs));
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&empty_bar[s], phase ^ 1, p.wait_ns) && !late);
           if (!ok) break;
           const int col = c * r.cols, bytes = min(r.cols, p.H - col) * (int)sizeof(A);
           uint8_t* stage = rows_smem + (size_t)s * r.stage_bytes;
@@ -562,8 +564,9 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
     }
   } else {
     // ------------------------------------------------------------ their use
-    // (after a time-out they go on to the end without waiting, so that their barriers are met;
-    // the places are checked against the rows where they are used)
+    // (after a time-out they go on to the end without waiting, so that their barriers are met; no
+    // stage is filled again then, as its last copies may still be under way; the places are checked
+    // against the rows where they are used)
     const int v = threadIdx.x - 32;
     int turn = 0;
     for (long long t = blockIdx.x; t < p.T; t += gridDim.x)
@@ -571,7 +574,10 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
         float sum[8] = {};  // forward: of a chunk, over the groups; backward: each row's share, over the chunks
         for (int i = 0; i < inner; ++i) {
           const int g = BACKWARD ? o : i, c = BACKWARD ? i : o, here = min(kGroupRows, p.k - g * kGroupRows);
-          if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full_bar[s], phase, kCopyWaitNs));
+          if (ok) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full_bar[s], phase, p.wait_ns));
+            if (!ok && lane == 0) late = 1;  // (before the arrival below, which the producer's wait acquires)
+          }
           const int col = c * r.cols + 8 * v;
           const bool on = 8 * v < r.cols && col < p.H;
           const uint8_t* stage = rows_smem + (size_t)s * r.stage_bytes;
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
     // a copy waited for in vain may still land: report, and stay until it surely has
     report_status(&g_sort_status, kStatusTimeoutMain);
     const uint64_t since = ptx::globaltimer_ns();
-    while (ptx::globaltimer_ns() - since < kCopyWaitNs / 50) __nanosleep(1000);
+    while (ptx::globaltimer_ns() - since < kLandingNs) __nanosleep(1000);
   }
 }
 
