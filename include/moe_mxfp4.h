@@ -368,10 +368,13 @@ int moe_block_norm(const void* block, const void* norm_weight, const void* gate,
 
 /* moe_block_norm_8bit: moe_block_norm with `out` in 8 bits, for products with 8-bit
  * activations and for moe_sort_tokens to move: E4M3 codes and scales of the f32 y,
- *   code = E4M3(y / scale), nearest, ties to even
+ *   code = E4M3(y (1 / scale)), nearest, ties to even
  *   MOE_SCALE_MX: E8M0 bytes [T, H / 32], scale 2^(byte - 127), one for 32 values: the least
  *     with |y| <= 448 scale (2^-126 at least), so that no value saturates.  H % 32 == 0.
- *   MOE_SCALE_ROW: f32 [T], one for a row: max |y| / 448 (2^-126 at least).
+ *     (Powers of two: the product is exact.)
+ *   MOE_SCALE_ROW: f32 [T], one for a row: max |y| (1 / 448) (2^-126 at least).  Here 1 / 448,
+ *     1 / scale and both products are rounded to f32, so that a y within 4 2^-24 of itself of
+ *     a tie between two codes may get the other of the two.
  * A group with an infinite or NaN y has a NaN scale (E8M0 255) and NaN codes.
  *   codes [T, H] bytes, written, and scales: overlap nothing else.  residual_out, or NULL.
  *   out: y rounded to dtype as well (for a router, say), or NULL.  next_weight is needed;

@@ -90,7 +90,10 @@ __device__ __forceinline__ void set2(V& v, const f32x2 (&f)[4]) {
 // infinity is above every finite value and a NaN above that), and becomes the group's scale:
 //   MX: 2^e, e the least in [-126, 120] with largest <= 448 2^e, so that nothing saturates (the
 //       rule of the layer's own encoding; the floor of log2 would cut mantissas above 1.75);
-//   row: largest / 448, 2^-126 at least.
+//   row: largest (1 / 448), 2^-126 at least, and codes of y (1 / scale).  Quotients rounded as
+//        division rounds them, by one correction each, decide no more than which of two codes a
+//        value next to a tie gets, and cost 4096 x 2880 bf16 20.3 us against 19.2, 8192 x 4096 40.6
+//        against 37.3.
 // A group with an infinity or a NaN gets a NaN as its scale, and NaN codes.
 __device__ __forceinline__ uint32_t largest8(const f32x2 (&y)[4]) {
   uint32_t m = 0;
