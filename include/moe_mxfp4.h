@@ -509,8 +509,11 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
  *   d_topk_w f32 [T, k]; logits f32 [T, E], topk_idx and topk_w as moe_route gave them (the
  *   indices as routed, not with assignments dropped); gating: moe_route's flag, or 0.
  *   d_logits f32 [T, E]: written whole, 0 where the weights do not depend on the logit.
- *   The selection itself has no gradient.  An expert listed twice gets the sum, an index
- *   outside [0, E) nothing.  Arrays 4-byte aligned; d_logits may not overlap an input. */
+ *   The selection itself has no gradient.  An expert listed twice gets the sum.  An index
+ *   outside [0, E) gets nothing; its weight and gradient count in sum_i w_i g_i as given.
+ *   A d_topk_w of 0 (a dropped assignment's) counts as 0 whatever its weight, and a token
+ *   whose d_topk_w are all 0 gets zeros, also where its weights or logits are not finite (a
+ *   mask that leaves no expert).  Arrays 4-byte aligned; d_logits may not overlap an input. */
 int moe_route_backward(const float* d_topk_w, const float* logits, const int32_t* topk_idx, const float* topk_w, int T, int k,
                        int E, int gating, float* d_logits, moe_stream_t stream);
 

@@ -654,7 +654,9 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2)
 //   softmax over the k selected   dl_j = w_j (g_j - S)
 //   sigmoids over their sum       dl_j = w_j (1 - sigmoid(l_j)) (g_j - S)
 //   softmax over all E            dl_e = p_e (g_e - S), g_e = 0 where e was not selected
-// added where an expert was selected twice, in the order of j; 0 elsewhere.
+// added where an expert was selected twice, in the order of j; 0 elsewhere.  A term whose g is 0
+// adds nothing to S whatever its weight, and a token all of whose g are 0 gets zeros: one that a mask
+// leaves no expert has NaN weights, and the zero gradients of its dropped assignments stay zeros.
 __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_constant__ RouteBackwardParams p) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
@@ -677,12 +679,14 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
     g = __ldcg(p.d_w + t * p.k + lane);
     w = __ldcg(p.w + t * p.k + lane);
   }
-  float s = w * g;
+  float s = g == 0.f ? 0.f : w * g;
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   float* out = p.d_logits + t * p.E;
+  const bool none = __all_sync(0xffffffffu, g == 0.f);
   float part = all ? g : w * (g - s);
   if (p.gating == kGatingSigmoid && e >= 0) part *= 1.f / (1.f + expf(__ldcg(logits + e)));
+  if (none) part = 0.f;
   if (all) {
 #pragma unroll
     for (int i = 0; i < kMaxExperts / 32; ++i)
@@ -692,11 +696,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < kMaxExperts / 32; ++i) {
       if (32 * i >= p.E) break;  // (every expert slot for 8 experts: 6.3 us for 8192 tokens)
-      l[i] = lane + 32 * i < p.E ? expf(l[i] - top) : 0.f;
+      l[i] = lane + 32 * i < p.E && !none ? expf(l[i] - top) : 0.f;
       sum += l[i];
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (none) sum = 1.f;
   }
 #pragma unroll
   for (int i = 0; i < kMaxExperts / 32; ++i) {
