@@ -479,8 +479,8 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
  *   rows [T*k] rows of row_bytes: x[perm / k].  row_scales, or NULL: the same of `scales`.
  *   x: [T] rows of row_bytes bytes (of any type), a multiple of 16 up to 65536; scales: [T]
  *   rows of scale_bytes (0 .. 4096; 0 with scales and row_scales NULL).  T, k and E as in the
- *   conventions above.  Rows and scales 16-byte aligned, the i32 arrays 4; no output may overlap
- *   an input.
+ *   conventions above.  Rows 16-byte aligned, the i32 arrays 4; scales and row_scales may begin
+ *   at any byte.  No output may overlap an input.
  * Source: "Quick Start", "Fused MoE Dispatch" (permute).                             */
 int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, int T, int k, int E, int row_bytes,
                     int scale_bytes, int32_t* offsets, int32_t* perm, int32_t* inv_perm, void* rows, void* row_scales,

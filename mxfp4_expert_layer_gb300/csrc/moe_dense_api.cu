@@ -517,7 +517,7 @@ int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, 
   if (scale_bytes < 0 || scale_bytes > kMaxScaleBytes) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!x || !topk_idx || !offsets || !perm || !inv_perm || !rows) return MOE_ERR_INVALID_ARG;
   if ((scales != nullptr) != (scale_bytes > 0) || (row_scales != nullptr) != (scale_bytes > 0)) return MOE_ERR_INVALID_ARG;
-  const void *moved[] = {x, scales, rows, row_scales}, *words[] = {topk_idx, offsets, perm, inv_perm};
+  const void *moved[] = {x, rows}, *words[] = {topk_idx, offsets, perm, inv_perm};
   for (const void* q : moved)
     if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
   for (const void* q : words)

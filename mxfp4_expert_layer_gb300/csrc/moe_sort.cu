@@ -182,9 +182,12 @@ __device__ __forceinline__ void move_units(const SortParams& p, size_t t, Place 
 }
 template <typename Place>
 __device__ __forceinline__ void move_scales(const SortParams& p, size_t t, Place place) {
-  if ((p.scale_bytes & 3) == 0)
+  // (the widest unit that the rows' length and both arrays' beginnings are multiples of)
+  const unsigned bits = (unsigned)p.scale_bytes | (unsigned)reinterpret_cast<uintptr_t>(p.scales) |
+                        (unsigned)reinterpret_cast<uintptr_t>(p.row_scales);
+  if ((bits & 3) == 0)
     move_units<unsigned>(p, t, place);
-  else if ((p.scale_bytes & 1) == 0)
+  else if ((bits & 1) == 0)
     move_units<unsigned short>(p, t, place);
   else
     move_units<unsigned char>(p, t, place);
