@@ -447,8 +447,8 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  *   by more the longer the sum.
  *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
  *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
- *   256-byte aligned, contents irrelevant before and after.  Few tokens take a kernel that
- *   streams the weights through mma.sync, batches of up to 128 and more the tcgen05 ones.
+ *   256-byte aligned, apart from every other array, contents irrelevant before and after.  Few
+ *   tokens take a kernel that streams the weights through mma.sync, batches of up to 128 and more the tcgen05 ones.
  * The pages have no counterpart ("triton-kernels" README, "Kernels", lists the fused GEMMs
  * of the feed-forward block).                                                        */
 size_t moe_linear_workspace_bytes(int T, int K, int N, int backward);
@@ -462,8 +462,10 @@ int moe_linear_forward(const void* x, const void* weight, const float* bias, con
  *   dp is formed in f32, summed into d_bias (f32 [N]) in a fixed order, and rounded to dtype
  *   as the products' operand (in f16 with f16's range: scale d_out where it is small).
  *   d_x [T, K], d_weight [N, K] of dtype, d_bias: overwritten; each may be NULL (not all).
- *   weight may be NULL without d_x, x without d_weight.  No output may overlap an input.
- *   workspace: moe_linear_workspace_bytes(T, K, N, 1) bytes, 256-byte aligned.       */
+ *   weight may be NULL without d_x, x without d_weight.  No output may overlap an input or
+ *   another output.
+ *   workspace: moe_linear_workspace_bytes(T, K, N, 1) bytes, 256-byte aligned, apart from every
+ *   other array; enough for any of these calls.                                      */
 int moe_linear_backward(const void* d_out, const void* x, const void* weight, const float* pre, int T, int K, int N, int act,
                         int dtype, int out_dtype, void* d_x, void* d_weight, float* d_bias, void* workspace,
                         size_t workspace_bytes, moe_stream_t stream);
@@ -480,7 +482,7 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
  *   x: [T] rows of row_bytes bytes (of any type), a multiple of 16 up to 65536; scales: [T]
  *   rows of scale_bytes (0 .. 4096; 0 with scales and row_scales NULL).  T, k and E as in the
  *   conventions above.  Rows 16-byte aligned, the i32 arrays 4; scales and row_scales may begin
- *   at any byte.  No output may overlap an input.
+ *   at any byte.  No output may overlap an input or another output.
  * Source: "Quick Start", "Fused MoE Dispatch" (permute).                             */
 int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, int T, int k, int E, int row_bytes,
                     int scale_bytes, int32_t* offsets, int32_t* perm, int32_t* inv_perm, void* rows, void* row_scales,

@@ -161,6 +161,14 @@ bool any_overlap(const Span (&a)[N], const Span (&b)[M]) {
       if (x.p && y.p && overlap(x.p, x.bytes, y.p, y.bytes)) return true;
   return false;
 }
+// Whether any two of them overlap.
+template <int N>
+bool overlap_within(const Span (&a)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < i; ++j)
+      if (a[i].p && a[j].p && overlap(a[i].p, a[i].bytes, a[j].p, a[j].bytes)) return true;
+  return false;
+}
 
 // Tokens and experts of a routing, as the layer's.
 bool routing_shape(int T, int k, int E) {
@@ -302,6 +310,8 @@ int moe_linear_forward(const void* x, const void* weight, const float* bias, con
   const LinearLayout L = linear_layout(T, K, N, false);
   if (L.total && (!workspace || !aligned(workspace, 256))) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const Span ws[] = {{L.total ? workspace : nullptr, L.total}};
+  if (any_overlap(ws, read) || any_overlap(ws, kept) || any_overlap(ws, written)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const LinearPath path = linear_path(T, K, N);
   if (path == LinearPath::thin) {
@@ -348,10 +358,12 @@ int moe_linear_backward(const void* d_out, const void* x, const void* weight, co
   const Span in[] = {{d_out, cells * (out_dtype == MOE_DTYPE_F32 ? 4 : 2)}, {x, (size_t)T * K * 2}, {weight, (size_t)N * K * 2},
                      {pre, cells * 4}};
   const Span out[] = {{d_x, (size_t)T * K * 2}, {d_weight, (size_t)N * K * 2}, {d_bias, (size_t)N * 4}};
-  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
+  if (any_overlap(out, in) || overlap_within(out)) return MOE_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
   const LinearLayout L = linear_layout(T, K, N, true);
   if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const Span ws[] = {{workspace, L.total}};
+  if (any_overlap(ws, in) || any_overlap(ws, out)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool products = d_x || d_weight;
   const void* dp = d_out;  // without an activation, a 16-bit d_out is dp
@@ -527,7 +539,7 @@ int moe_sort_tokens(const void* x, const void* scales, const int32_t* topk_idx, 
   const Span in[] = {{x, (size_t)T * row_bytes}, {scales, (size_t)T * scale_bytes}, {topk_idx, n * 4}};
   const Span out[] = {{offsets, (size_t)(E + 1) * 4}, {perm, n * 4}, {inv_perm, n * 4}, {rows, n * row_bytes},
                       {row_scales, n * scale_bytes}};
-  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
+  if (any_overlap(out, in) || overlap_within(out)) return MOE_ERR_INVALID_ARG;
   SortParams p{};
   p.idx = topk_idx;
   p.x = x;
@@ -579,7 +591,7 @@ int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* 
     if (!aligned(q, 4)) return MOE_ERR_INVALID_ARG;
   const size_t bytes = (size_t)T * H * (dtype == MOE_DTYPE_F32 ? 4 : 2), n = (size_t)T * k * 4;
   const Span in[] = {{d_out, bytes}, {y, bytes * k}, {inv_perm, n}, {topk_w, n}}, out[] = {{d_y, bytes * k}, {d_topk_w, n}};
-  if (any_overlap(out, in)) return MOE_ERR_INVALID_ARG;
+  if (any_overlap(out, in) || overlap_within(out)) return MOE_ERR_INVALID_ARG;
   UnsortBackwardParams q{};
   q.f.y = y;
   q.f.inv_perm = inv_perm;
