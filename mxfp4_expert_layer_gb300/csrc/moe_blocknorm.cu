@@ -527,13 +527,8 @@ __global__ void __launch_bounds__(512)
 // the backward; the weights stay in registers as they were loaded.  Two reductions a row
 // (the second is of the rounded stream), each a barrier of the group's own.  Bound by HBM,
 // past the first rows' latency: 4096 x 2880 bf16 17.4 us, 5.4 TB/s (a copy: 6.7).
-//
-// TIGHT: 56 registers a thread, for widths at which that lets one more block reside on an SM
-// (2880: 4096 rows bf16 with a feature gate 24.4 -> 19.0 us); elsewhere the compiler's 64 are better
-// (8192 x 4096, f32 stream: 63 us against 76).
-template <typename A, typename S, int GATE, bool TIGHT>
-__global__ void __maxnreg__(TIGHT ? 56 : 64)
-    block_norm_rows_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
+template <typename A, typename S, int GATE>
+__device__ __forceinline__ void block_norm_rows(const BlockNormParams& p, const RowCopies& rows) {
   extern __shared__ __align__(128) uint8_t norm_smem[];
   __shared__ float sums[2][16];
   __shared__ uint64_t full_bar[kNormMaxGroups][3];
@@ -626,6 +621,20 @@ __global__ void __maxnreg__(TIGHT ? 56 : 64)
     }
   }
   if (!ok) leave_late();
+}
+template <typename A, typename S, int GATE>
+__global__ void __launch_bounds__(512, 2)
+    block_norm_rows_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
+  block_norm_rows<A, S, GATE>(p, rows);
+}
+// With 56 registers a thread, for widths at which that lets one more block reside on an SM, and the
+// instances that take more of themselves: bf16 with a feature or a full gate (4096 x 2880 onto bf16 24.0
+// and 25.9 -> 19.2 and 20.1 us, onto f32, with 8 bytes spilled, 34.0 and 34.2 -> 27.4 and 30.4).  Those that keep
+// to 56 by themselves lose by being told to (bf16 onto f32 without a gate 23.8 -> 24.6).
+template <typename A, typename S, int GATE>
+__global__ void __maxnreg__(56)
+    block_norm_rows_tight_kernel(const __grid_constant__ BlockNormParams p, const __grid_constant__ RowCopies rows) {
+  block_norm_rows<A, S, GATE>(p, rows);
 }
 
 // The same with 8-bit codes.  Sixteen values a thread: with eight, a row's 300 instructions a
@@ -858,14 +867,15 @@ cudaError_t forward_t(const BlockNormParams& p, cudaStream_t stream) {
       if (gate == kGateFull) return launch(block_norm_codes_kernel<A, S, kGateFull, OUT>, o[1]);
       return launch(block_norm_codes_kernel<A, S, kGateNone, OUT>, o[2]);
     } else {
-      auto pick = [&](auto tight) {
-        constexpr bool TIGHT = decltype(tight)::value;
-        static SmemOptIn o[3];
-        if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature, TIGHT>, o[0]);
-        if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull, TIGHT>, o[1]);
-        return launch(block_norm_rows_kernel<A, S, kGateNone, TIGHT>, o[2]);
-      };
-      return per_sm * groups * per > 1024 ? pick(std::true_type{}) : pick(std::false_type{});
+      static SmemOptIn o[5];
+      if constexpr (std::is_same<A, __nv_bfloat16>::value)
+        if (per_sm * groups * per > 1024) {
+          if (gate == kGateFeature) return launch(block_norm_rows_tight_kernel<A, S, kGateFeature>, o[3]);
+          if (gate == kGateFull) return launch(block_norm_rows_tight_kernel<A, S, kGateFull>, o[4]);
+        }
+      if (gate == kGateFeature) return launch(block_norm_rows_kernel<A, S, kGateFeature>, o[0]);
+      if (gate == kGateFull) return launch(block_norm_rows_kernel<A, S, kGateFull>, o[1]);
+      return launch(block_norm_rows_kernel<A, S, kGateNone>, o[2]);
     }
   }
   auto launch = [&](auto kern) { return launch_pdl(kern, dim3(p.T), dim3(row_threads), 0, stream, p); };
