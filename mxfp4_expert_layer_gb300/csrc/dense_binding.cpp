@@ -69,6 +69,9 @@ void* need(const char* name, const at::Tensor* t, Shape shape, at::ScalarType ty
       << (t->is_contiguous() ? "" : ", not contiguous");
     value_error(s.str());
   }
+  if (t->is_conj() || t->is_neg())  // (a flag: the memory holds other values)
+    value_error(std::string(name) + ": its " + (t->is_conj() ? "conjugation" : "negation") + " is pending: resolve_" +
+                (t->is_conj() ? "conj" : "neg") + "() first");
   return t->data_ptr();
 }
 
