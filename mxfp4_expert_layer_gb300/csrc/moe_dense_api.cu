@@ -99,7 +99,8 @@ int check_ffn(int T, int H, int I, int dtype, int act) {
 }
 
 // A projection's workspace: dp [T, N] and the bias gradient's partial sums (backward), then
-// the partial sums of whichever product splits K.
+// the partial sums of whichever product splits K.  By sizes alone: a call without an activation, or
+// without some of the gradients, leaves parts of it unused.
 struct LinearLayout {
   size_t sums, partial, total;
 };
@@ -134,7 +135,7 @@ LinearLayout linear_layout(int T, int K, int N, bool backward) {
   if (backward) {
     L.sums = align_up((size_t)T * N * 2, 256);
     L.partial = align_up(L.sums + (size_t)linear_grad_splits(T, N) * N * sizeof(float), 256);
-    need(T, K, N);
+    if (!linear_batch(T, N, K)) need(T, K, N);
     need(N, K, T);
   } else if (linear_path(T, K, N) == LinearPath::tiles) {
     need(T, N, K);
