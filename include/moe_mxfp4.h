@@ -443,8 +443,8 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  *   act: MOE_ACT_NONE, _SILU or _GELU.  pre_out: f32 [T, N] for moe_linear_backward, or NULL;
  *   NULL with MOE_ACT_NONE, whose backward does not need it.
  *   The tensor cores cut each step's addends below the largest: of its terms' norm, pre is off by
- *   4e-6 rms over 4096 terms (2.5e-5 the worst of 4 million; a chain of f32 additions: 6e-7 rms),
- *   by more the longer the sum.
+ *   4.4e-6 rms over 4096 bf16 terms and 4.9e-6 over f16 ones (2.7e-5 and 3.1e-5 the worst of 4
+ *   million; f32 products: 6e-7 and 1.1e-6 rms), by more the longer the sum (16384: 1.9e-5 rms).
  *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
  *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
  *   256-byte aligned, apart from every other array, contents irrelevant before and after.  Few
@@ -460,7 +460,8 @@ int moe_linear_forward(const void* x, const void* weight, const float* bias, con
  *   dp = d_out act'(pre);  d_x = dp W;  d_weight = dp^T x;  d_bias = sum_t dp
  *   d_out [T, N] of out_dtype; pre: what pre_out received, NULL exactly with MOE_ACT_NONE.
  *   dp is formed in f32, summed into d_bias (f32 [N]) in a fixed order, and rounded to dtype
- *   as the products' operand (in f16 with f16's range: scale d_out where it is small).
+ *   as the products' operand, that of an f32 d_out too (in f16 with f16's range: scale d_out
+ *   where it is small): d_x and d_weight are off by about 1.4 of their own rounding.
  *   d_x [T, K], d_weight [N, K] of dtype, d_bias: overwritten; each may be NULL (not all).
  *   weight may be NULL without d_x, x without d_weight.  No output may overlap an input or
  *   another output.

@@ -108,14 +108,15 @@ struct LinearLayout {
 //   thin    a block for 16 rows of W, while those are one round of blocks: 8 x 4096 -> 4096 8.0 against
 //           9.6 of a batch, 16 x 4096 -> 4096 9.2 against 9.9; beyond, or with more of x to read again by
 //           every block, a batch is faster: 8 x 2880 -> 5120 9.5 against 8.8, 16 x 14336 -> 4096 25.2
-//           against 22.2; one to four tokens stay thin for three rounds (1 x 4096 -> 14336 20.8 against
-//           23.5, 1 x 2880 -> 32768 34.8 against 31.3);
+//           against 22.2; one to four tokens stay thin up to 16384 rows, 3.4 rounds of two blocks on each
+//           of 152 SMs (1 x 4096 -> 14336 20.8 against 23.5, but 1 x 2880 -> 32768 34.8 against 31.3), however
+//           long K is (131072 -> 24: 1 token 69.1, and 17 as a batch 69.6);
 //   batch   up to 32 tokens (24 x 4096 -> 2880 8.3, tiles 11.6), 64 where K is not short (64 x 4096 ->
 //           2880 9.7 against 12.2, but 64 x 1024 -> 4096 7.3 against 6.4), 128 where K is cut in four at
 //           least (128 x 4096 -> 4096 13.0 against 14.6, but 128 x 2880 -> 5120 15.0 against 12.2);
 //   tiles   else.
-// The gradient into x of a batch takes the same kernel (64 tokens: 27 us against 22 at 4096 <- 14336,
-// 9.9 against 7 at 2880 <- 2880).
+// The gradient into x of a batch takes the same kernel (64 tokens: 22.8 us against the tiles' 26.8 at
+// 4096 <- 14336, 8.7 against 10.2 at 2880 <- 2880).
 enum class LinearPath { thin, batch, tiles };
 bool linear_batch(int T, int K, int N) {
   return T <= 32 || (T <= 64 && K > 1024) || (T <= kBatchTokens && K > 1024 && 4 * ceil_div(N, 128) <= device_sms());

@@ -1118,7 +1118,7 @@ Shape estimate_shape(int M, int N, int K, int mode, bool b_mn, int sms) {
   return best;
 }
 // The estimate is a function of the sizes alone; the last ones are kept per thread, since a
-// small product's launch would wait for its 3 us otherwise.
+// small product's launch would wait for its 0.9 us otherwise.
 Shape pick_shape(int M, int N, int K, int mode, bool b_mn) {
   if (mode == kDenseLinear32) mode = kDenseLinear;
   struct Entry {
@@ -1302,8 +1302,9 @@ int launch_dense_products(DenseGemmParams p, int n, const DenseOperand* a, const
   q.lead = q.long_n < n ? (int)(len[0] / len[1] + 0.5f) : 0;
   const float work = (float)tiles[0] * len[0] + (q.long_n < n ? (float)tiles[1] * len[1] : 0.f);
   float together = work / (float)workers + 0.5f * len[q.long_n < n ? 1 : 0] + 1000.f;
-  // a few long tiles that cannot be shared out take as long as one of them (128 x 4096 -> 1024 with
-  // its weights' gradient: see the projections' backward)
+  // a few long tiles that cannot be shared out take as long as one of them: both gradients of 200 x 1024
+  // -> 8192 take 27.1 us apart and 43.8 together, of 256 x 1024 -> 32768 60 and 158 (but 256 x 4096 ->
+  // 14336, whose weights' tiles would have hidden them, 79.9 and 75.1)
   if (few_rows) together = fmaxf(together, (float)ceil_div((int)tiles[0], workers) * len[0] + 1000.f);
   if (n < 2 || together > apart + 5000.f * (float)(n - 1)) {
     for (int i = 0; i < n; ++i) {

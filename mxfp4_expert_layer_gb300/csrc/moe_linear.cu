@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const __grid_constant_
 }
 
 // The sums of the partial rows: eight threads take those of one column in turn, then add in
-// order.  Every load at once (one thread after the other's load: 11 us for 107 rows).
+// order.  Every load of a thread at once, up to eight: one after the other each is a memory round trip.
 constexpr int kMaxSplits = 64;
 __global__ void __launch_bounds__(256) linear_bias_kernel(const float* partial, int splits, int N, float* d_bias) {
   __shared__ float buf[8][33];
