@@ -448,7 +448,8 @@ int moe_ffn_backward(const void* d_out, const void* x, const float* gateup, cons
  *   1 <= T <= 2^24, K and N multiples of 8, K up to 2^17, N up to 2^20; arrays 16-byte
  *   aligned; workspace moe_linear_workspace_bytes(T, K, N, 0) bytes (0: it may be NULL),
  *   256-byte aligned, apart from every other array, contents irrelevant before and after.  Few
- *   tokens take a kernel that streams the weights through mma.sync, batches of up to 128 and more the tcgen05 ones.
+ *   tokens take a kernel that streams the weights through mma.sync, batches of up to 128 and
+ *   more the tcgen05 ones.
  * The pages have no counterpart ("triton-kernels" README, "Kernels", lists the fused GEMMs
  * of the feed-forward block).                                                        */
 size_t moe_linear_workspace_bytes(int T, int K, int N, int backward);
@@ -503,8 +504,8 @@ int moe_unsort_tokens(const void* y, const int32_t* inv_perm, const float* topk_
  *   d_y[inv_perm[t, j]] = topk_w[t, j] * d_out[t]; a dropped assignment's row (-1 - inv_perm):
  *   zeros, so that after moe_sort_tokens every row of d_y is written
  *   d_topk_w[t, j] = sum_h d_out[t, h] * y[inv_perm[t, j], h]   (f32; 0 where dropped)
- * Either may be NULL; y is read for d_topk_w alone, and may be NULL without it.  Types,
- * sizes and overlaps as for moe_unsort_tokens.                                       */
+ * Either may be NULL; y is read for d_topk_w alone, and may be NULL without it.  Types and
+ * sizes as for moe_unsort_tokens; no output may overlap an input or the other output. */
 int moe_unsort_tokens_backward(const void* d_out, const void* y, const int32_t* inv_perm, const float* topk_w, int T, int k,
                                int H, int dtype, void* d_y, float* d_topk_w, moe_stream_t stream);
 
@@ -564,8 +565,9 @@ int moe_matvec_mxfp4(const void* x, const void* w, const float* bias, int T, int
 /* moe_set_wait_limit_ns: how long (ns) each pipeline wait of the expert GEMMs (and of the
  * dense GEMMs and the copies of sorted tokens' rows, whose status moe_dense_status reads) may
  * take before it gives up, for launches made after the call (process-wide; 0 restores the
- * default of 1 s; at most 10 s, else MOE_ERR_INVALID_ARG).  A wait that gives up sets a bit of the workspace status word (moe_get_device_status), the
- * kernel drops its remaining work, waits (up to 1 s) for the copies and tensor-core
+ * default of 1 s; at most 10 s, else MOE_ERR_INVALID_ARG).  A wait that gives up sets a
+ * bit of the workspace status word (moe_get_device_status) or of the dense one, the kernel
+ * drops its remaining work, waits (up to 1 s) for the copies and tensor-core
  * operations it has already issued, frees its tensor memory and exits: no trap, and
  * the context stays usable.  Limits under 2 us are polled without suspending the
  * waiting thread, so a limit shorter than the pipeline's own latency (a copy landing
